@@ -152,13 +152,13 @@ def _paged(gen, total, page, extra):
     return table, pages
 
 
-def _cache(dev_gen, pages, heads, rows, cols, bits):
+def _cache(dev_gen, pages, heads, inner, bits):
     """Codes of unit normal values and power-of-two scales for each page and head."""
     exps = torch.randint(-7, -4, (pages, heads), generator=dev_gen, device=DEV)
-    codes = torch.empty((pages, heads, rows, cols), dtype=E4M3, device=DEV)
-    step = max(1, (1 << 27) // (heads * rows * cols))
+    codes = torch.empty((pages, heads) + inner, dtype=E4M3, device=DEV)
+    step = max(1, (1 << 27) // (heads * math.prod(inner)))
     for a in range(0, pages, step):  # in parts: the normal values take four times the codes' room
-        x = torch.randn((min(step, pages - a), heads, rows, cols), generator=dev_gen, device=DEV)
+        x = torch.randn((min(step, pages - a), heads) + inner, generator=dev_gen, device=DEV)
         codes[a:a + step] = (x * bits).to(E4M3)
     return codes, torch.exp2(exps.float())
 
@@ -207,8 +207,8 @@ def prepare(case, seed):
         seq = torch.repeat_interleave(torch.arange(case["n"]), new)
         pos = torch.arange(tokens) - cu[:-1].long()[seq] + (ctx - first * page)[seq]
         slots = table[seq, pos // page].long() * page + pos % page
-        kc, ks = _cache(dev, pages, hkv, page, case["dk"], 24.0)
-        vc, vs = _cache(dev, pages, hkv, case["dv"], page, 24.0)
+        kc, ks = _cache(dev, pages, hkv, (page, case["dk"]), 24.0)
+        vc, vs = _cache(dev, pages, hkv, (page // 16, case["dv"], 16), 24.0)
         # a few channels carry much larger values, so pages' scales differ and some of them grow
         wide = torch.exp(1.5 * randn(1, hkv, 1))
         return dict(op=op, page=page, slots=slots.to(torch.int32).to(DEV), kc=kc, ks=ks, vc=vc, vs=vs,
@@ -216,8 +216,8 @@ def prepare(case, seed):
     if op == "attention":
         page, hkv, t = case["page"], case["hkv"], _type(case)
         table, pages = _paged(gen, ctx + new, page, 2)
-        kc, ks = _cache(dev, pages, hkv, page, case["dk"], 64.0)
-        vc, vs = _cache(dev, pages, hkv, case["dv"], page, 64.0)
+        kc, ks = _cache(dev, pages, hkv, (page, case["dk"]), 64.0)
+        vc, vs = _cache(dev, pages, hkv, (page // 16, case["dv"], 16), 64.0)
         return dict(op=op, page=page, kc=kc, ks=ks, vc=vc, vs=vs, table=table.to(DEV),
                     kv_lens=(ctx + new).to(torch.int32).to(DEV), cu=cu.to(DEV),
                     q=randn(tokens, case["heads"], case["dk"]).to(t), scale=case["dk"] ** -0.5,
@@ -298,8 +298,18 @@ def _codes(x):
     return torch.where(torch.isfinite(x), x, float("nan")).to(E4M3)
 
 
+def _tokens(v):
+    """The values' pages [.., page / 16, dv, 16] as [.., page, dv]."""
+    return v.transpose(-1, -2).flatten(-3, -2)
+
+
+def _packed(v):
+    """[.., page, dv] as the cache holds values."""
+    return v.unflatten(-2, (-1, 16)).transpose(-1, -2)
+
+
 def _plain_write_one(x, cache, scales, slots, page, across):
-    """`across`: the tokens of a page are the last axis of the cache."""
+    """`across`: the cache is that of the values."""
     x = x.float()
     pages, heads = scales.shape
     at, off = slots.long() // page, slots.long() % page
@@ -311,14 +321,14 @@ def _plain_write_one(x, cache, scales, slots, page, across):
     need = _scale_of(amax[touched])
     now = torch.where((first == 0)[:, None], need, torch.maximum(need, was))
     held = cache.view(torch.uint8)[touched].view(E4M3).float()
-    held = held.transpose(2, 3) if across else held
+    held = _tokens(held) if across else held
     held = held * (was / now)[:, :, None, None]
     held = torch.where((first == 0)[:, None, None, None], 0.0, held)
     where = torch.full((pages,), 0, device=DEV, dtype=torch.long)
     where[touched] = torch.arange(touched.numel(), device=DEV)
     held = held.to(E4M3).view(torch.uint8)
     held[where[at], :, off] = _codes(x / now[where[at]][:, :, None]).view(torch.uint8)
-    cache.view(torch.uint8)[touched] = held.transpose(2, 3) if across else held
+    cache.view(torch.uint8)[touched] = _packed(held) if across else held
     scales[touched] = now
 
 
@@ -338,9 +348,9 @@ def _plain_attention(s):
     table = s["table"][:, :cols].long()
     at = table.clamp(min=0)
     k = s["kc"].view(torch.uint8)[at].view(E4M3).float() * s["ks"][at][..., None, None]
-    v = s["vc"].view(torch.uint8)[at].view(E4M3).float() * s["vs"][at][..., None, None]
+    v = _tokens(s["vc"].view(torch.uint8)[at].view(E4M3).float()) * s["vs"][at][..., None, None]
     k = k.permute(0, 2, 1, 3, 4).reshape(n, hkv, cols * page, dk)
-    v = v.permute(0, 2, 1, 4, 3).reshape(n, hkv, cols * page, -1)
+    v = v.permute(0, 2, 1, 3, 4).reshape(n, hkv, cols * page, -1)
     lens = cu[1:] - cu[:-1]
     i = torch.arange(longest, device=DEV)
     padded = q.float()[(cu[:-1, None] + i[None, :]).clamp(max=tokens - 1)]
@@ -446,7 +456,7 @@ def work(case):
 
 def _exact_write_one(x, cache, scales, slots, page, across):
     codes = cache.double().cpu()
-    codes = codes.transpose(2, 3).contiguous() if across else codes
+    codes = codes.permute(0, 1, 2, 4, 3).flatten(2, 3) if across else codes
     scales, x = scales.double().cpu(), x.double().cpu()
     slots = slots.cpu().tolist()
     runs = {}
@@ -465,7 +475,7 @@ def _exact_write_one(x, cache, scales, slots, page, across):
             codes[p] = _nearest(codes[p] * (scales[p] / now)[:, None, None])
         codes[p, :, a:a + len(ts)] = _nearest(part / now[None, :, None]).transpose(0, 1)
         scales[p] = now
-    return codes.transpose(2, 3).contiguous() if across else codes, scales
+    return codes.unflatten(2, (-1, 16)).permute(0, 1, 2, 4, 3).contiguous() if across else codes, scales
 
 
 def _nearest(x):
@@ -487,7 +497,7 @@ def exact(case, seed):
     if op == "attention":
         cu, kv_lens, table = s["cu"].tolist(), s["kv_lens"].tolist(), s["table"].tolist()
         tokens, heads, dk = s["q"].shape
-        hkv, page, dv = s["kc"].shape[1], s["page"], s["vc"].shape[2]
+        hkv, page, dv = s["kc"].shape[1], s["page"], s["vc"].shape[3]
         o = torch.zeros((tokens, heads, dv), dtype=torch.float64, device=DEV)
         for n, length in enumerate(kv_lens):
             a, b = cu[n], cu[n + 1]
@@ -496,7 +506,8 @@ def exact(case, seed):
             pages = table[n][:-(-length // page)]
             for h in range(hkv):
                 keys = torch.cat([s["kc"][p, h].double() * s["ks"][p, h].double() for p in pages])[:length]
-                values = torch.cat([s["vc"][p, h].double().T * s["vs"][p, h].double() for p in pages])[:length]
+                values = torch.cat([s["vc"][p, h].double().permute(0, 2, 1).flatten(0, 1) * s["vs"][p, h].double()
+                                    for p in pages])[:length]
                 for head in range(h * (heads // hkv), (h + 1) * (heads // hkv)):
                     x = s["q"][a:b, head].double() @ keys.T * s["scale"]
                     future = torch.triu(torch.ones_like(x, dtype=torch.bool), diagonal=length - (b - a) + 1)
