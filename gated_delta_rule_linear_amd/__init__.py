@@ -5,6 +5,9 @@ names and only marshal arguments: PyTorch tensors supply device memory and
 the current stream; every step of the computation runs in the HIP kernels of
 libgdn.so.  There is no CPU fallback: the first call raises ImportError when
 libgdn.so has not been built (python -m gated_delta_rule_linear_amd.build).
+The calls a server makes beside the layer (include/gdn_serve.h: batch tables,
+a paged 8-bit cache and its attention, a pool of states) are in the submodule
+`serve` and have the same form; all are reached from here.
 The submodule `inputs` (seeded synthetic inputs) does not need the library.
 """
 
@@ -25,6 +28,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 # (tests/run_host_sanitizers.sh).
 LIB_PATH = os.path.join(_HERE, "libgdn_hostsan.so" if os.environ.get("GDN_HOST_SANITIZE") == "1" else "libgdn.so")
 HEADER = os.path.join(os.path.dirname(_HERE), "include", "gdn.h")
+SERVE_HEADER = os.path.join(os.path.dirname(_HERE), "include", "gdn_serve.h")
 
 GDN_OK, GDN_ERR_INVALID_ARG, GDN_ERR_UNSUPPORTED, GDN_ERR_DOMAIN, GDN_ERR_OOM, GDN_ERR_HIP, GDN_ERR_SCRATCH_LIMIT = range(7)
 GDN_NOALLOC_SCRATCH_BYTES = 64 << 20
@@ -86,6 +90,7 @@ def _load():
     lib.gdn_prefill_backward.restype = i32
     lib.gdn_prefill_tiles.argtypes = [P, P, P, P, P, P, i32, i64, P, P, P, i32, i32, i32, i32, i32, P]
     lib.gdn_prefill_tiles.restype = i32
+    serve.bind(lib)
     _LIB = lib
     return lib
 
@@ -95,9 +100,9 @@ def load_library():
     return _load()
 
 
-def exported_symbols_in_header() -> list:
-    """Names of the functions include/gdn.h declares."""
-    with open(HEADER) as f:
+def exported_symbols_in_header(header: str = HEADER) -> list:
+    """Names of the functions a header (include/gdn.h unless named) declares."""
+    with open(header) as f:
         text = f.read()
     return re.findall(r"^\s*(?:const\s+)?[a-z_0-9]+\**\s+\**(gdn_[a-z_0-9]+)\s*\(", text, flags=re.M)
 
@@ -506,3 +511,8 @@ __all__ = [
     "gdn_decode_head_gate", "gdn_prefill_backward", "gdn_prefill_backward_workspace_bytes", "gdn_prefill_tiles", "GdnError", "load_library", "LIB_PATH",
     "GDN_GATE_LOG", "GDN_GATE_SCALED_SIGMOID", "GDN_GATE_ALPHA_MIN", "GDN_TILES_DENSE", "GDN_TILES_PAIRS",
 ]
+
+from . import serve  # noqa: E402  (it uses the helpers above)
+from .serve import *  # noqa: E402,F401,F403
+
+__all__ += serve.__all__

@@ -20,7 +20,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libgdn.so")
 SOURCES = ["gdn_api.cpp", "gdn_api_backward.cpp", "gdn_api_tiles.cpp", "gdn_prefill.hip", "gdn_decode.hip",
-           "gdn_backward.hip", "gdn_tiles.hip", "gdn_noalloc.hip"]
+           "gdn_backward.hip", "gdn_tiles.hip", "gdn_noalloc.hip", "gdn_api_serve.cpp", "gdn_tables.hip",
+           "gdn_cache_write.hip", "gdn_cache_attention.hip", "gdn_pool.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 FLAGS = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}", "-Wall", "-Wno-unused-function",
