@@ -114,7 +114,8 @@ int32_t attention_sizes(const gdn::CacheAttentionLaunch& p) {
     if (p.H < 1 || p.H_kv < 1 || p.H % p.H_kv != 0 || p.H_kv > 65535) return GDN_ERR_INVALID_ARG;
     if (!supported_d(p.dk) || !supported_d(p.dv) || !supported_page(p.page_size)) return GDN_ERR_UNSUPPORTED;
     if (p.T_total > 0 && p.num_seqs == 0) return GDN_ERR_INVALID_ARG;
-    if (p.T_total * p.H > ((int64_t)1 << 31)) return GDN_ERR_UNSUPPORTED;  // grids of one workgroup per few rows
+    // grids of less than 2^24 workgroups
+    if (p.T_total * p.H > ((int64_t)1 << 27) || (int64_t)p.num_seqs * p.H_kv > ((int64_t)1 << 22)) return GDN_ERR_UNSUPPORTED;
     return GDN_OK;
 }
 
@@ -164,6 +165,7 @@ int32_t gdn_cache_write(const void* k, const void* v, const int32_t* slots, int6
     if (!supported_dtype(dtype) || !supported_d(d_k) || !supported_d(d_v) || !supported_page(page_size))
         return GDN_ERR_UNSUPPORTED;
     if (num_pages > ((int64_t)INT32_MAX + 1) / page_size) return GDN_ERR_UNSUPPORTED;  // slots are int32
+    if (T_total > ((int64_t)1 << 28)) return GDN_ERR_UNSUPPORTED;
     if (T_total == 0 || num_pages == 0) return GDN_OK;
     for (const void* x : {k, v, static_cast<const void*>(k_cache), static_cast<const void*>(v_cache)})
         if (!aligned(x, 16)) return GDN_ERR_INVALID_ARG;
@@ -222,7 +224,7 @@ int32_t gdn_decode_pool(const void* q, const void* k, const void* v, const float
     if (num_seqs < 0 || T_total < 0 || T_total > INT32_MAX || num_slots < 0) return GDN_ERR_INVALID_ARG;
     if (H < 1 || H_k < 1 || H % H_k != 0) return GDN_ERR_INVALID_ARG;
     if (!supported_dtype(dtype) || !supported_d(d_k) || !supported_d(d_v)) return GDN_ERR_UNSUPPORTED;
-    if ((int64_t)num_seqs * H > INT32_MAX) return GDN_ERR_UNSUPPORTED;  // one workgroup each
+    if ((int64_t)num_seqs * H >= ((int64_t)1 << 24)) return GDN_ERR_UNSUPPORTED;  // one workgroup each
     if (!std::isfinite(q_scale) || !std::isfinite(l2_eps) || l2_eps < 0.f) return GDN_ERR_INVALID_ARG;
     if (!cu_seqlens && T_total != num_seqs) return GDN_ERR_INVALID_ARG;
     if (T_total > 0 && num_seqs == 0) return GDN_ERR_INVALID_ARG;

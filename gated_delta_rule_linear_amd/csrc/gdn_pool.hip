@@ -19,7 +19,7 @@
 namespace gdn {
 namespace {
 
-constexpr int kCols = 16;                   // value columns of a wave
+constexpr int kCols = 32;                   // value columns of a wave
 constexpr int kColLanes = kCols / 4;        // lanes side by side along a row
 constexpr int kRowGroups = 64 / kColLanes;  // lanes along the rows
 

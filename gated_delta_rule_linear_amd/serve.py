@@ -8,8 +8,8 @@ on the device of its tensors, which all have to be on one device.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
-import functools
 
 import torch
 
@@ -37,47 +37,77 @@ def bind(lib):
     lib.gdn_decode_pool.restype = i32
 
 
-def _on_its_device(fn):
-    """Runs fn with the device of its first tensor current."""
-
-    @functools.wraps(fn)
-    def call(first, *args, **kw):
-        if first.is_cuda and first.device.index != torch.cuda.current_device():
-            with torch.cuda.device(first.device):
-                return fn(first, *args, **kw)
-        return fn(first, *args, **kw)
-
-    return call
-
-
+# These calls are made many times per generated token, so a check that passes
+# costs a few attribute reads; what is wrong is found out in _refuse.
 def _take(t, name, dtype, shape, device):
-    """The address of a contiguous device tensor of this type and shape (None in shape: any length)."""
-    if not t.is_cuda or t.device != device:
-        raise ValueError(f"{name} must be on the device of the call's first tensor")
-    if t.dtype != dtype:
+    """The address of a contiguous tensor of this type and shape on device number `device`."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous():
+        return t.data_ptr()
+    _refuse(t, name, dtype, shape)
+
+
+def _refuse(t, name, dtype, shape):
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != len(shape) or any(want is not None and want != have for want, have in zip(shape, t.shape)):
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
-
-
-def _maybe(t, name, dtype, shape, device):
-    return None if t is None else _take(t, name, dtype, shape, device)
+    raise ValueError(f"{name} must be on the device of the call's first tensor")
 
 
 def _dims(t, name, dims):
     if t.dim() != dims:
-        raise ValueError(f"{name} must have {dims} dimensions")
+        raise ValueError(f"{name} must have {dims} dimensions, got {list(t.shape)}")
     return t.shape
+
+
+class _Device:
+    """The device and the stream of a call while it allocates and enqueues.  Entered only where they are not the
+    current ones: a context manager costs as much as several checks."""
+
+    def __init__(self, device, stream):
+        self.device, self.stream = torch.cuda.device(device), None if stream is None else torch.cuda.stream(stream)
+
+    def __enter__(self):
+        self.device.__enter__()
+        if self.stream is not None:
+            self.stream.__enter__()
+
+    def __exit__(self, *exc):
+        if self.stream is not None:
+            self.stream.__exit__(*exc)
+        self.device.__exit__(*exc)
+
+
+_HERE_ALREADY = contextlib.nullcontext()
+
+
+def _device_of(t, name):
+    device = t.get_device()
+    if device < 0:
+        raise ValueError(f"{name} must be a device tensor")
+    return device
+
+
+def _on(device, stream):
+    if stream is None and device == torch.cuda.current_device():
+        return _HERE_ALREADY
+    return _Device(device, stream)
+
+
+def _stream(device, stream):
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+
+
+def _bytes(t):
+    return t.numel() * t.element_size()
 
 
 def gdn_batch_tables_workspace_bytes(num_seqs: int, T_total: int) -> int:
     return int(_gdn._load().gdn_batch_tables_workspace_bytes(int(num_seqs), int(T_total)))
 
 
-@_on_its_device
 def gdn_batch_tables(context_lens, new_lens, T_total: int, page_size: int, block_table, page_counts, free_pages,
                      free_state, rows=None, workspace=None, stream=None):
     """Packed offsets, lengths, slots and positions of one step: returns (cu_seqlens [num_seqs + 1], kv_lens
@@ -86,53 +116,52 @@ def gdn_batch_tables(context_lens, new_lens, T_total: int, page_size: int, block
 
     context_lens and new_lens are int32 [num_seqs] on the device (new_lens < 0: the request has ended); rows int32
     [num_seqs] names each request's row (None: row n)."""
-    lib, dev, i32 = _gdn._load(), context_lens.device, torch.int32
-    n = _dims(context_lens, "context_lens", 1)[0]
+    lib, dev, i32 = _gdn._load(), _device_of(context_lens, "context_lens"), torch.int32
+    (n,) = _dims(context_lens, "context_lens", 1)
     num_rows, max_blocks = _dims(block_table, "block_table", 2)
-    args = [_take(context_lens, "context_lens", i32, (n,), dev), _take(new_lens, "new_lens", i32, (n,), dev),
-            _maybe(rows, "rows", i32, (n,), dev)]
-    table = _take(block_table, "block_table", i32, (None, None), dev)
+    (pages,) = _dims(free_pages, "free_pages", 1)
+    cp, np = _take(context_lens, "context_lens", i32, (n,), dev), _take(new_lens, "new_lens", i32, (n,), dev)
+    rp = None if rows is None else _take(rows, "rows", i32, (n,), dev)
+    table = _take(block_table, "block_table", i32, (num_rows, max_blocks), dev)
     counts = _take(page_counts, "page_counts", i32, (num_rows,), dev)
-    ring, state = _take(free_pages, "free_pages", i32, (None,), dev), _take(free_state, "free_state", i32, (3,), dev)
+    ring, state = _take(free_pages, "free_pages", i32, (pages,), dev), _take(free_state, "free_state", i32, (3,), dev)
     T = int(T_total)
     if T < 0:
         raise ValueError("T_total must be >= 0")
-    with _gdn._on(stream):
-        # one block for the four results: each begins on a 16-byte boundary
-        a, b, c = (n + 4) // 4 * 4, (n + 3) // 4 * 4, (T + 3) // 4 * 4
-        out = torch.empty(a + b + 2 * c, dtype=i32, device=dev)
-        cu, kv, slots, pos = out[:n + 1], out[a:a + n], out[a + b:a + b + T], out[a + b + c:a + b + c + T]
-        if workspace is None:
-            workspace = torch.empty(max(16, gdn_batch_tables_workspace_bytes(n, T)), dtype=torch.uint8, device=dev)
-        base = out.data_ptr()
-        st = lib.gdn_batch_tables(*args, n, T, int(page_size), table, num_rows, max_blocks, counts, ring,
-                                  free_pages.shape[0], state, base, base + 4 * a, base + 4 * (a + b),
-                                  base + 4 * (a + b + c), workspace.data_ptr(),
-                                  workspace.numel() * workspace.element_size(), _gdn._stream(stream))
-        _gdn._check(st, "gdn_batch_tables")
+    need = 0 if workspace is not None else lib.gdn_batch_tables_workspace_bytes(n, T) // 4
+    with _on(dev, stream):
+        # one block for the four results and the workspace
+        cu, kv, slots, pos, own = torch.empty(2 * n + 1 + 2 * T + need, dtype=i32,
+                                              device=context_lens.device).split((n + 1, n, T, T, need))
+        base = cu.data_ptr()
+        wp, wb = (own.data_ptr(), 4 * need) if workspace is None else (workspace.data_ptr(), _bytes(workspace))
+        st = lib.gdn_batch_tables(cp, np, rp, n, T, page_size, table, num_rows, max_blocks, counts, ring, pages, state,
+                                  base, base + 4 * (n + 1), base + 4 * (2 * n + 1), base + 4 * (2 * n + 1 + T), wp, wb,
+                                  _stream(dev, stream))
+    _gdn._check(st, "gdn_batch_tables")
     return cu, kv, slots, pos
 
 
-def _cache(k_cache, v_cache, k_scale, v_scale, device):
+def _cache(k_cache, v_cache, k_scale, v_scale, dev):
     pages, hkv, page, dk = _dims(k_cache, "k_cache", 4)
     dv = _dims(v_cache, "v_cache", 5)[3]
-    return (pages, page, hkv, dk, dv, _take(k_cache, "k_cache", E4M3, (pages, hkv, page, dk), device),
-            _take(v_cache, "v_cache", E4M3, (pages, hkv, page // 16, dv, 16), device),
-            _take(k_scale, "k_scale", torch.float32, (pages, hkv), device),
-            _take(v_scale, "v_scale", torch.float32, (pages, hkv), device))
+    return (pages, page, hkv, dk, dv, _take(k_cache, "k_cache", E4M3, (pages, hkv, page, dk), dev),
+            _take(v_cache, "v_cache", E4M3, (pages, hkv, page // 16, dv, 16), dev),
+            _take(k_scale, "k_scale", torch.float32, (pages, hkv), dev),
+            _take(v_scale, "v_scale", torch.float32, (pages, hkv), dev))
 
 
-@_on_its_device
 def gdn_cache_write(k, v, slots, k_cache, v_cache, k_scale, v_scale, stream=None) -> None:
     """New keys k [T, H_kv, dk] and values v [T, H_kv, dv] (bf16 or fp32) to their slots (int32 [T]) of the paged cache:
     k_cache [pages, H_kv, page, dk] and v_cache [pages, H_kv, page / 16, dv, 16] (torch.float8_e4m3fn), k_scale and
     v_scale [pages, H_kv] (fp32 powers of two), updated in place."""
-    lib, dev, dt = _gdn._load(), k.device, _gdn._dtype_code(k)
+    lib, dt, dev = _gdn._load(), _gdn._dtype_code(k), _device_of(k, "k")
     pages, page, hkv, dk, dv, kc, vc, ks, vs = _cache(k_cache, v_cache, k_scale, v_scale, dev)
     T = _dims(k, "k", 3)[0]
-    st = lib.gdn_cache_write(_take(k, "k", k.dtype, (T, hkv, dk), dev), _take(v, "v", k.dtype, (T, hkv, dv), dev),
-                             _take(slots, "slots", torch.int32, (T,), dev), T, kc, vc, ks, vs, pages, page, hkv, dk, dv,
-                             dt, _gdn._stream(stream))
+    kp, vp = _take(k, "k", k.dtype, (T, hkv, dk), dev), _take(v, "v", k.dtype, (T, hkv, dv), dev)
+    sp = _take(slots, "slots", torch.int32, (T,), dev)
+    with _on(dev, stream):
+        st = lib.gdn_cache_write(kp, vp, sp, T, kc, vc, ks, vs, pages, page, hkv, dk, dv, dt, _stream(dev, stream))
     _gdn._check(st, "gdn_cache_write")
 
 
@@ -142,41 +171,39 @@ def gdn_cache_attention_workspace_bytes(num_seqs: int, T_total: int, max_new: in
                                                                 max_blocks, H, H_kv, dk, dv))
 
 
-@_on_its_device
 def gdn_cache_attention(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, cu_seqlens, rows=None, scale=None,
                         max_new: int = 0, max_kv: int = 0, o=None, workspace=None, stream=None):
     """Causal attention of the step's queries q [T, H, dk] (bf16 or fp32) over the paged cache (see gdn_cache_write);
     returns o [T, H, dv].  Request n's queries are rows cu_seqlens[n] .. cu_seqlens[n + 1] - 1 and the last of the
     kv_lens[n] tokens that row rows[n] (None: row n) of block_table holds.  scale: 1 / sqrt(dk) by default.  max_new
     and max_kv, host-side bounds on a request's new tokens and on kv_lens, help to plan (0: unknown)."""
-    lib, dev, dt = _gdn._load(), q.device, _gdn._dtype_code(q)
+    lib, dt, dev, i32 = _gdn._load(), _gdn._dtype_code(q), _device_of(q, "q"), torch.int32
     pages, page, hkv, dk, dv, kc, vc, ks, vs = _cache(k_cache, v_cache, k_scale, v_scale, dev)
     T, H, _ = _dims(q, "q", 3)
-    n = _dims(kv_lens, "kv_lens", 1)[0]
+    (n,) = _dims(kv_lens, "kv_lens", 1)
     num_rows, max_blocks = _dims(block_table, "block_table", 2)
     qp = _take(q, "q", q.dtype, (T, H, dk), dev)
-    table = _take(block_table, "block_table", torch.int32, (None, None), dev)
-    rp = _maybe(rows, "rows", torch.int32, (n,), dev)
-    kv = _take(kv_lens, "kv_lens", torch.int32, (n,), dev)
-    cu = _take(cu_seqlens, "cu_seqlens", torch.int32, (n + 1,), dev)
-    with _gdn._on(stream):
+    table = _take(block_table, "block_table", i32, (num_rows, max_blocks), dev)
+    rp = None if rows is None else _take(rows, "rows", i32, (n,), dev)
+    kv, cu = _take(kv_lens, "kv_lens", i32, (n,), dev), _take(cu_seqlens, "cu_seqlens", i32, (n + 1,), dev)
+    with _on(dev, stream):
         if o is None:
-            o = torch.empty((T, H, dv), dtype=q.dtype, device=dev)
-        op = _take(o, "o", q.dtype, (T, H, dv), dev)
+            o = torch.empty((T, H, dv), dtype=q.dtype, device=q.device)
+            op = o.data_ptr()
+        else:
+            op = _take(o, "o", q.dtype, (T, H, dv), dev)
         if workspace is None:
-            need = lib.gdn_cache_attention_workspace_bytes(n, T, int(max_new), int(max_kv), page, max_blocks, H, hkv, dk,
-                                                           dv)
+            need = lib.gdn_cache_attention_workspace_bytes(n, T, max_new, max_kv, page, max_blocks, H, hkv, dk, dv)
             if need:
-                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        wp, wb = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
-        st = lib.gdn_cache_attention(qp, kc, vc, ks, vs, table, rp, kv, cu, n, T, int(max_new), int(max_kv), pages, page,
-                                     num_rows, max_blocks, dk ** -0.5 if scale is None else float(scale), op, H, hkv, dk,
-                                     dv, dt, wp, wb, _gdn._stream(stream))
-        _gdn._check(st, "gdn_cache_attention")
+                workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        wp, wb = (None, 0) if workspace is None else (workspace.data_ptr(), _bytes(workspace))
+        st = lib.gdn_cache_attention(qp, kc, vc, ks, vs, table, rp, kv, cu, n, T, max_new, max_kv, pages, page, num_rows,
+                                     max_blocks, dk ** -0.5 if scale is None else scale, op, H, hkv, dk, dv, dt, wp, wb,
+                                     _stream(dev, stream))
+    _gdn._check(st, "gdn_cache_attention")
     return o
 
 
-@_on_its_device
 def gdn_decode_pool(q, k, v, g, beta, states, slots, cu_seqlens=None, commit=None, q_scale: float = 1.0,
                     l2_eps: float = 0.0, o=None, stream=None):
     """The delta rule on a pool of states [num_slots, H, dk, dv] (fp32, updated in place), one or a few tokens for each
@@ -184,24 +211,26 @@ def gdn_decode_pool(q, k, v, g, beta, states, slots, cu_seqlens=None, commit=Non
     h // (H // H_k)); g [T, H, dk] or [T, H] and beta [T, H] in fp32; slots int32 [num_seqs]; cu_seqlens int32
     [num_seqs + 1] (None: one token each); commit int32 [num_seqs]: the tokens whose update is kept (None: all);
     l2_eps > 0: q and k are L2-normalised in the kernel."""
-    lib, dev, dt = _gdn._load(), q.device, _gdn._dtype_code(q)
+    lib, dt, dev, i32, f32 = _gdn._load(), _gdn._dtype_code(q), _device_of(q, "q"), torch.int32, torch.float32
     T, hk, dk = _dims(q, "q", 3)
     num_slots, H, _, dv = _dims(states, "states", 4)
-    n = _dims(slots, "slots", 1)[0]
+    (n,) = _dims(slots, "slots", 1)
     head_gate = g.dim() == 2
     qp, kp = _take(q, "q", q.dtype, (T, hk, dk), dev), _take(k, "k", q.dtype, (T, hk, dk), dev)
     vp = _take(v, "v", q.dtype, (T, H, dv), dev)
-    gp = _take(g, "g", torch.float32, (T, H) if head_gate else (T, H, dk), dev)
-    bp, sp = _take(beta, "beta", torch.float32, (T, H), dev), _take(states, "states", torch.float32, (None, H, dk, dv), dev)
-    lp = _take(slots, "slots", torch.int32, (n,), dev)
-    cp, mp = _maybe(cu_seqlens, "cu_seqlens", torch.int32, (n + 1,), dev), _maybe(commit, "commit", torch.int32, (n,), dev)
-    with _gdn._on(stream):
+    gp, bp = _take(g, "g", f32, (T, H) if head_gate else (T, H, dk), dev), _take(beta, "beta", f32, (T, H), dev)
+    sp, lp = _take(states, "states", f32, (num_slots, H, dk, dv), dev), _take(slots, "slots", i32, (n,), dev)
+    cp = None if cu_seqlens is None else _take(cu_seqlens, "cu_seqlens", i32, (n + 1,), dev)
+    mp = None if commit is None else _take(commit, "commit", i32, (n,), dev)
+    with _on(dev, stream):
         if o is None:
-            o = torch.empty((T, H, dv), dtype=q.dtype, device=dev)
-        op = _take(o, "o", q.dtype, (T, H, dv), dev)
-        st = lib.gdn_decode_pool(qp, kp, vp, gp, int(head_gate), bp, sp, lp, cp, mp, n, T, num_slots, float(q_scale),
-                                 float(l2_eps), op, H, hk, dk, dv, dt, _gdn._stream(stream))
-        _gdn._check(st, "gdn_decode_pool")
+            o = torch.empty((T, H, dv), dtype=q.dtype, device=q.device)
+            op = o.data_ptr()
+        else:
+            op = _take(o, "o", q.dtype, (T, H, dv), dev)
+        st = lib.gdn_decode_pool(qp, kp, vp, gp, head_gate, bp, sp, lp, cp, mp, n, T, num_slots, q_scale, l2_eps, op, H,
+                                 hk, dk, dv, dt, _stream(dev, stream))
+    _gdn._check(st, "gdn_decode_pool")
     return o
 
 
