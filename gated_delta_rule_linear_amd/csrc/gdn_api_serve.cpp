@@ -115,7 +115,7 @@ int32_t attention_sizes(const gdn::CacheAttentionLaunch& p) {
     if (!supported_d(p.dk) || !supported_d(p.dv) || !supported_page(p.page_size)) return GDN_ERR_UNSUPPORTED;
     if (p.T_total > 0 && p.num_seqs == 0) return GDN_ERR_INVALID_ARG;
     // grids of less than 2^24 workgroups
-    if (p.T_total * p.H > ((int64_t)1 << 27) || (int64_t)p.num_seqs * p.H_kv > ((int64_t)1 << 22)) return GDN_ERR_UNSUPPORTED;
+    if (p.T_total * p.H > ((int64_t)1 << 27) || (int64_t)p.num_seqs * p.H_kv > ((int64_t)1 << 18)) return GDN_ERR_UNSUPPORTED;
     return GDN_OK;
 }
 

@@ -29,7 +29,7 @@ namespace {
 typedef float floatx16 __attribute__((ext_vector_type(16)));
 
 constexpr int kTile = 64;      // tokens of a tile
-constexpr int kFewRows = 32;   // requests with up to so many rows go to the rows kernel
+constexpr int kFewRows = 32;   // a request with up to so many rows is one of few rows
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kInf = __builtin_inff();
 
@@ -44,10 +44,14 @@ struct Attention {
     float scale2;  // scale * log2(e): scores in units of log 2
     void* o;
     int32_t H, Hkv, G;
-    int32_t splits, min_chunk;
-    int64_t more_rows, most_rows;  // a kernel takes the requests with more_rows < rows <= most_rows
-    float* ws_o;   // [splits][T * H][d_v]
-    float* ws_ml;  // [splits][T * H][2]: maximum and sum
+    // Requests of few rows (at most few_rows) and the others: at most so many
+    // parts of a request's cache, of at least so many tokens.
+    int32_t few_rows;
+    int32_t splits[2], min_chunk[2];
+    bool tiled;  // the others go to the tile kernel
+    // Parts before they are joined, [part][row][d_v] and [part][row][2] (maximum
+    // and sum).  Rows: for few, (n * Hkv + h) * few_rows + row; else those of q.
+    float *ws_o[2], *ws_ml[2];
 };
 
 // Tiles of BR rows that the requests before n take at most: the tiles of
@@ -65,50 +69,67 @@ __device__ __forceinline__ int32_t request_of(const Attention& a, int64_t b, int
     }
     return below - 1;
 }
-// A request's cache is cut into parts of `chunk` tokens (a multiple of kTile).
-__device__ __forceinline__ int64_t chunk_of(const Attention& a, int64_t kv) {
-    const int64_t c = ((kv + a.splits - 1) / a.splits + kTile - 1) / kTile * kTile;
-    return c > a.min_chunk ? c : a.min_chunk;
+
+// A request, as every kernel sees it.
+struct Request {
+    int64_t t0;       // first new token
+    int32_t len;      // new tokens
+    int32_t rows;     // len * G
+    int64_t kv;       // tokens held
+    int64_t chunk;    // tokens of a part of its cache
+    bool few;
+    __device__ __forceinline__ Request(const Attention& a, int32_t n) {
+        int64_t t1 = a.cu[n + 1];
+        t0 = a.cu[n];
+        const int64_t most = (int64_t)a.max_blocks << a.page_log2, held = a.kv_lens[n];
+        t0 = t0 < 0 ? 0 : t0;
+        t1 = t1 < a.T ? t1 : a.T;
+        len = t1 > t0 ? (int32_t)(t1 - t0) : 0;
+        rows = len * a.G;
+        kv = held < 0 ? 0 : held < most ? held : most;
+        few = rows <= a.few_rows;
+        const int c = few ? 0 : 1;
+        chunk = ((kv + a.splits[c] - 1) / a.splits[c] + kTile - 1) / kTile * kTile;
+        if (chunk < a.min_chunk[c]) chunk = a.min_chunk[c];
+        if (!few && !a.tiled && chunk < kv) chunk = (kv + kTile - 1) / kTile * kTile;  // there is no room for its parts
+    }
+    __device__ __forceinline__ bool alone() const { return kv <= chunk; }
+};
+
+__device__ __forceinline__ const int32_t* table_of(const Attention& a, int32_t n) {
+    const int32_t row = a.rows ? a.rows[n] : n;
+    return row >= 0 && row < a.num_rows && a.num_pages > 0 ? a.table + (int64_t)row * a.max_blocks : nullptr;
 }
-__device__ __forceinline__ int64_t held_tokens(const Attention& a, int32_t n) {
-    const int64_t most = (int64_t)a.max_blocks << a.page_log2, kv = a.kv_lens[n];
-    return kv < 0 ? 0 : kv < most ? kv : most;
+// Where row `row` of request n and head h stands among the rows of parts.
+__device__ __forceinline__ int64_t part_row(const Attention& a, const Request& q, int32_t n, int32_t h, int32_t row,
+                                            int64_t orow) {
+    return q.few ? ((int64_t)n * a.Hkv + h) * a.few_rows + row : orow;
+}
+__device__ __forceinline__ int64_t part_rows(const Attention& a, bool few) {
+    return few ? (int64_t)a.num_seqs * a.Hkv * a.few_rows : a.T * a.H;
 }
 
-// What a workgroup works on: rows row0 .. of request n and key/value head h, in
-// part z of its cache.
-struct Job {
-    int64_t t0, len, kv, row0, rows;  // first token, tokens, held tokens, first row, rows of the request
-    int64_t from, to;                 // tokens of the part that some row of the tile sees
-    int64_t all_see;                  // every row of the tile sees the tokens up to this one
-    const int32_t* table;             // the request's row, null: it has none
-    bool alone;                       // the request's cache is one part
+// Pages and scales of 64 tiles, `step` tokens apart, a lane for each: fetched
+// ahead in one go, since a load in the tiles' loop whose result is needed at
+// once would wait for every load before it, the keys and values among them.
+struct Pages {
+    int32_t page;  // -1: left out
+    float ks, vs;
+    __device__ __forceinline__ void fetch(const Attention& a, const int32_t* table, int32_t h, int64_t base, int64_t to, int step) {
+        const int64_t at = base + (int64_t)(threadIdx.x & 63) * step;
+        page = table && at < to ? table[at >> a.page_log2] : -1;
+        if (page >= a.num_pages) page = -1;
+        ks = vs = 0.f;
+        if (page >= 0) {
+            const int64_t ph = (int64_t)page * a.Hkv + h;
+            ks = a.ks[ph];
+            vs = a.vs[ph];
+        }
+    }
+    __device__ __forceinline__ static float lane_of(float x, int i) {
+        return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), i));
+    }
 };
-template <int BR>
-__device__ __forceinline__ bool find_job(const Attention& a, int64_t tile, int z, Job& j) {
-    const int32_t n = request_of(a, tile, BR);
-    if (n < 0) return false;
-    int64_t t1 = a.cu[n + 1];
-    j.t0 = a.cu[n];
-    j.row0 = (tile - first_tile(a, n, BR)) * BR;
-    j.t0 = j.t0 < 0 ? 0 : j.t0;
-    t1 = t1 < a.T ? t1 : a.T;
-    j.len = t1 - j.t0;
-    j.rows = j.len * a.G;
-    if (j.len <= 0 || j.row0 < 0 || j.row0 >= j.rows || j.rows <= a.more_rows || j.rows > a.most_rows) return false;
-    j.kv = held_tokens(a, n);
-    const int64_t chunk = chunk_of(a, j.kv);
-    j.from = z * chunk;
-    if (z > 0 && j.from >= j.kv) return false;
-    j.alone = j.kv <= chunk;
-    const int64_t last = j.row0 + BR < j.rows ? j.row0 + BR - 1 : j.rows - 1;
-    j.to = j.kv - j.len + last / a.G + 1;
-    j.to = j.to < j.from + chunk ? j.to : j.from + chunk;
-    j.all_see = j.kv - j.len + j.row0 / a.G;
-    const int32_t row = a.rows ? a.rows[n] : n;
-    j.table = row >= 0 && row < a.num_rows ? a.table + (int64_t)row * a.max_blocks : nullptr;
-    return true;
-}
 
 // A value split into NS bf16 parts: one rounds it, three hold all of an fp32.
 template <int NS>
@@ -120,6 +141,33 @@ __device__ __forceinline__ void split_bf16(float x, bf16* part) {
     }
 }
 
+// Eight neighbouring values, as they are in memory and as NS bf16 operands.
+template <typename TI>
+struct Eight;
+template <>
+struct Eight<float> {
+    floatx4 a, b;
+    __device__ __forceinline__ void load(const float* p) {
+        a = *reinterpret_cast<const floatx4*>(p);
+        b = *reinterpret_cast<const floatx4*>(p + 4);
+    }
+    __device__ __forceinline__ void split(bf16x8* part) const {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            bf16 x[3];
+            split_bf16<3>(j < 4 ? a[j & 3] : b[j & 3], x);
+#pragma unroll
+            for (int s = 0; s < 3; ++s) part[s][j] = x[s];
+        }
+    }
+};
+template <>
+struct Eight<bf16> {
+    bf16x8 a;
+    __device__ __forceinline__ void load(const bf16* p) { a = *reinterpret_cast<const bf16x8*>(p); }
+    __device__ __forceinline__ void split(bf16x8* part) const { part[0] = a; }
+};
+
 template <typename TI>
 __device__ __forceinline__ void store4(TI* p, floatx4 x) {
     if constexpr (sizeof(TI) == 4) *reinterpret_cast<floatx4*>(p) = x;
@@ -127,9 +175,6 @@ __device__ __forceinline__ void store4(TI* p, floatx4 x) {
 }
 
 constexpr int kWaves = 4;
-#ifndef ROWS_OCC
-#define ROWS_OCC 2
-#endif
 
 // ---------------------------------------------------------------- few rows
 //
@@ -143,95 +188,117 @@ constexpr int kWaves = 4;
 // asked for when the last keys have become scores, values when the last values
 // have been used.
 template <typename TI, int DK, int DV>
-__global__ __launch_bounds__(64 * kWaves, ROWS_OCC) void attention_rows_kernel(Attention a) {
+__global__ __launch_bounds__(64 * kWaves, 2) void attention_rows_kernel(Attention a) {
     constexpr int NS = sizeof(TI) == 4 ? 3 : 1;
     constexpr int BR = 16, KS = DK / 32, VT = DV / 16;
-    __shared__ float s_o[kWaves][BR][DV + 4];
+    // Of each wave: a tile's keys, and in the end its output.
+    constexpr int PR = DK / 16, KEYS = kTile * PR, OUT = BR * (DV + 4) / 4;
+    __shared__ uintx4 s_wave[kWaves][KEYS > OUT ? KEYS : OUT];
     __shared__ float s_m[kWaves][BR], s_l[kWaves][BR];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
-    const int h = blockIdx.y;
-    Job job;
-    if (!find_job<BR>(a, blockIdx.x, blockIdx.z, job)) return;
+    const int h = blockIdx.y, per = (a.few_rows + BR - 1) / BR;  // workgroups side by side along a request's rows
+    const int32_t n = blockIdx.x / per;
+    const Request job(a, n);
+    if (a.tiled && !job.few) return;
+    const int64_t from = blockIdx.z * job.chunk;
+    if (blockIdx.z > 0 && from >= job.kv) return;
+    const int32_t* const table = table_of(a, n);
     const int page_mask = (1 << a.page_log2) - 1;
+    // (With a request of more rows than it was planned for, more than one turn.)
+    for (int32_t row0 = (blockIdx.x - n * per) * BR; row0 < job.rows; row0 += per * BR) {
+    const int32_t last_row = (row0 + BR < job.rows ? row0 + BR : job.rows) - 1;
+    int64_t to = job.kv - job.len + last_row / a.G + 1;  // no row of the tile sees more
+    to = !table ? from : to < from + job.chunk ? to : from + job.chunk;
+    const int64_t all_see = job.kv - job.len + row0 / a.G;  // every row of the tile sees up to here
 
-    uintx4 kr[4][DK / 64], vr[VT];
-    int32_t page = -1, next_page = -1;  // of the tile in kr and vr, and of the one after it
-    float ks = 0.f, vs = 0.f;           // of the tile in kr and vr
-    auto page_of = [&](int64_t base) -> int32_t {
-        if (!job.table || base >= job.to) return -1;
-        const int32_t p = __builtin_amdgcn_readfirstlane(job.table[base >> a.page_log2]);
-        return p < a.num_pages ? p : -1;  // negative entries stay so: left out
-    };
+    // this lane's row; lanes behind the last one work on the first, unseen
+    const int32_t row = row0 + r;
+    const bool live = row < job.rows;
+    const int32_t i = live ? row / a.G : 0, head = h * a.G + (live ? row - i * a.G : 0);
+    const int64_t sees = live ? job.kv - job.len + i : -1;  // the last token that the row sees
+    Eight<TI> q8[KS];
+#pragma unroll
+    for (int m = 0; m < KS; ++m)
+        q8[m].load(static_cast<const TI*>(a.q) + ((job.t0 + i) * a.H + head) * DK + 16 * g + 64 * (m >> 1) + 8 * (m & 1));
+
+    uintx4 kr[PR], vr[VT];
+    // Keys are read as they lie, whole lines at a time (a row of a product takes
+    // half a line from each load otherwise, which halved the rate), and change
+    // places through the wave's LDS: piece `c` of 16 channels of token `row` goes
+    // to place c ^ turn(row), so that the 16 rows of a product's operand spread
+    // over the banks.
+    uintx4* const s_k = s_wave[wave];
+    auto turn = [&](int row) { return ((row & 3) | (row >> 4 & 1) << 2) & (PR - 1); };
+    // (The loads have no branch: one would make the wait for the loads before it
+    // a wait for these too.  Where there is no tile they read page 0.)
     auto load_keys = [&](int64_t base, int32_t p) {
-        if (p < 0) return;
-        const int64_t ph = (int64_t)p * a.Hkv + h;
-        const uint8_t* at = a.kc + ((ph << a.page_log2) + (base & page_mask)) * DK + (16 * (r >> 2) + (r & 3)) * DK + 16 * g;
+        const int64_t ph = (int64_t)(p < 0 ? 0 : p) * a.Hkv + h;
+        const uintx4* at = reinterpret_cast<const uintx4*>(a.kc + ((ph << a.page_log2) + (base & page_mask)) * DK) + lane;
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int j = 0; j < DK / 64; ++j) kr[c][j] = *reinterpret_cast<const uintx4*>(at + 4 * c * DK + 64 * j);
-        ks = a.ks[ph];
+        for (int j = 0; j < PR; ++j) kr[j] = __builtin_nontemporal_load(at + 64 * j);
     };
     auto load_values = [&](int64_t base, int32_t p) {
-        if (p < 0) return;
-        const int64_t ph = (int64_t)p * a.Hkv + h;
+        const int64_t ph = (int64_t)(p < 0 ? 0 : p) * a.Hkv + h;
         const uint8_t* at = a.vc + ((ph << a.page_log2) + (base & page_mask)) * DV + (g * DV + r) * 16;
 #pragma unroll
-        for (int d = 0; d < VT; ++d) vr[d] = *reinterpret_cast<const uintx4*>(at + d * 256);
-        vs = a.vs[ph];
+        for (int d = 0; d < VT; ++d) vr[d] = __builtin_nontemporal_load(reinterpret_cast<const uintx4*>(at + d * 256));
     };
     constexpr int STEP = kWaves * kTile;
-    const int64_t first = job.from + wave * kTile;
-    page = page_of(first);
-    next_page = page_of(first + STEP);
-    load_keys(first, page);
-    load_values(first, page);
-
-    // this lane's row
-    const int64_t row = job.row0 + r;
-    const bool live = row < job.rows;
-    const int64_t i = live ? row / a.G : 0;
-    const int32_t head = h * a.G + (int32_t)(live ? row - i * a.G : 0);
-    const int64_t sees = live ? job.kv - job.len + i : -1;  // the last token that the row sees
-    bf16x8 qf[NS][KS];
-    {
-        const TI* q = static_cast<const TI*>(a.q) + ((job.t0 + i) * a.H + head) * DK + 16 * g;
-#pragma unroll
-        for (int m = 0; m < KS; ++m)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                bf16 part[NS];
-                split_bf16<NS>(live ? to_f32(q[64 * (m >> 1) + 8 * (m & 1) + j]) : 0.f, part);
-#pragma unroll
-                for (int s = 0; s < NS; ++s) qf[s][m][j] = part[s];
-            }
+    const int64_t first = from + wave * kTile;
+    Pages pages;
+    pages.fetch(a, table, h, first, to, STEP);
+    int at = 0;  // the tile's lane of `pages`
+    int32_t page = __builtin_amdgcn_readlane(pages.page, 0);
+    float ks = Pages::lane_of(pages.ks, 0), vs = Pages::lane_of(pages.vs, 0);
+    if (first < to) {
+        load_keys(first, page);
+        load_values(first, page);
     }
+
+    bf16x8 qf[KS][NS];
+#pragma unroll
+    for (int m = 0; m < KS; ++m) q8[m].split(qf[m]);
 
     floatx4 O[VT];
 #pragma unroll
     for (int d = 0; d < VT; ++d) O[d] = zero4();
     float mx = -kInf, sum = 0.f;
-    for (int64_t base = first; base < job.to; base += STEP) {
+    for (int64_t base = first; base < to; base += STEP) {
         const bool there = page >= 0;
         float s[16];
         if (there) {
             const float c2 = ks * a.scale2;
 #pragma unroll
+            for (int j = 0; j < PR; ++j) {
+                const int row = (64 * j + lane) / PR, c = lane % PR;
+                s_k[row * PR + (c ^ turn(row))] = kr[j];
+            }
+            __builtin_amdgcn_wave_barrier();  // the wave's own writes and reads of s_k stay in this order
+#pragma unroll
             for (int c = 0; c < 4; ++c) {
                 floatx4 x = zero4();
+                const int row = 16 * (r >> 2) + 4 * c + (r & 3);
+                uintx4 k16[DK / 64];
+#pragma unroll
+                for (int j = 0; j < DK / 64; ++j) k16[j] = s_k[row * PR + ((4 * j + g) ^ turn(row))];
 #pragma unroll
                 for (int m = 0; m < KS; ++m) {
-                    const bf16x8 k8 = e4m3_to_bf16x8(kr[c][m >> 1][2 * (m & 1)], kr[c][m >> 1][2 * (m & 1) + 1]);
+                    const bf16x8 k8 = e4m3_to_bf16x8(k16[m >> 1][2 * (m & 1)], k16[m >> 1][2 * (m & 1) + 1]);
 #pragma unroll
-                    for (int p = NS - 1; p >= 0; --p) x = Mma<bf16>::mma(k8, qf[p][m], x);
+                    for (int p = NS - 1; p >= 0; --p) x = Mma<bf16>::mma(k8, qf[m][p], x);
                 }
 #pragma unroll
                 for (int j = 0; j < 4; ++j) s[4 * c + j] = x[j] * c2;
             }
         }
-        load_keys(base + STEP, next_page);
+        if (++at == 64) {
+            pages.fetch(a, table, h, base + STEP, to, STEP);
+            at = 0;
+        }
+        page = __builtin_amdgcn_readlane(pages.page, at);
+        load_keys(base + STEP, page);
         if (there) {
-            const bool edge = base + kTile - 1 > job.all_see;  // some row does not see all of the tile
+            const bool edge = base + kTile - 1 > all_see;  // some row does not see all of the tile
             const int64_t see = sees - (base + 16 * g);
             if (edge) {
 #pragma unroll
@@ -298,14 +365,16 @@ __global__ __launch_bounds__(64 * kWaves, ROWS_OCC) void attention_rows_kernel(A
                 }
             }
         }
-        load_values(base + STEP, next_page);
-        page = next_page;
-        next_page = page_of(base + 2 * STEP);
+        load_values(base + STEP, page);
+        ks = Pages::lane_of(pages.ks, at);
+        vs = Pages::lane_of(pages.vs, at);
     }
     sum += __shfl_xor(sum, 16);
     sum += __shfl_xor(sum, 32);
+    // The wave's output takes the place of its keys.
+    float(*const s_o)[DV + 4] = reinterpret_cast<float(*)[DV + 4]>(s_k);
 #pragma unroll
-    for (int d = 0; d < VT; ++d) *reinterpret_cast<floatx4*>(&s_o[wave][r][16 * d + 4 * g]) = O[d];
+    for (int d = 0; d < VT; ++d) *reinterpret_cast<floatx4*>(&s_o[r][16 * d + 4 * g]) = O[d];
     if (g == 0) {
         s_m[wave][r] = mx;
         s_l[wave][r] = sum;
@@ -314,38 +383,41 @@ __global__ __launch_bounds__(64 * kWaves, ROWS_OCC) void attention_rows_kernel(A
     // Join the waves: a thread takes DV / 16 channels of one row.
     constexpr int C = DV / 16;
     const int jr = threadIdx.x >> 4, c0 = (threadIdx.x & 15) * C;
-    if (job.row0 + jr >= job.rows) return;
-    float m = s_m[0][jr];
+    if (row0 + jr < job.rows) {
+        float m = s_m[0][jr];
 #pragma unroll
-    for (int w = 1; w < kWaves; ++w) m = fmaxf(m, s_m[w][jr]);
-    const float ref = m == -kInf ? 0.f : m;
-    float l = 0.f, out[C];
+        for (int w = 1; w < kWaves; ++w) m = fmaxf(m, s_m[w][jr]);
+        const float ref = m == -kInf ? 0.f : m;
+        float l = 0.f, out[C];
 #pragma unroll
-    for (int c = 0; c < C; ++c) out[c] = 0.f;
+        for (int k = 0; k < C; ++k) out[k] = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-        const float f = __builtin_amdgcn_exp2f(s_m[w][jr] - ref);
-        l += f * s_l[w][jr];
+        for (int w = 0; w < kWaves; ++w) {
+            const float f = __builtin_amdgcn_exp2f(s_m[w][jr] - ref);
+            l += f * s_l[w][jr];
 #pragma unroll
-        for (int c = 0; c < C; ++c) out[c] += f * s_o[w][jr][c0 + c];
+            for (int k = 0; k < C; ++k) out[k] += f * reinterpret_cast<const float(*)[DV + 4]>(s_wave[w])[jr][c0 + k];
+        }
+        const int32_t ji = (row0 + jr) / a.G;
+        const int64_t orow = (job.t0 + ji) * a.H + h * a.G + (row0 + jr - ji * a.G);
+        if (job.alone()) {
+            const float inv = l == 0.f && m == -kInf ? 0.f : 1.f / l;
+#pragma unroll
+            for (int k = 0; k < C; k += 4)
+                store4(static_cast<TI*>(a.o) + orow * DV + c0 + k,
+                       floatx4{out[k] * inv, out[k + 1] * inv, out[k + 2] * inv, out[k + 3] * inv});
+        } else {
+            const int64_t prow = blockIdx.z * part_rows(a, true) + part_row(a, job, n, h, row0 + jr, orow);
+#pragma unroll
+            for (int k = 0; k < C; k += 4)
+                *reinterpret_cast<floatx4*>(a.ws_o[0] + prow * DV + c0 + k) = floatx4{out[k], out[k + 1], out[k + 2], out[k + 3]};
+            if (c0 == 0) {
+                a.ws_ml[0][2 * prow] = m;
+                a.ws_ml[0][2 * prow + 1] = l;
+            }
+        }
     }
-    const int64_t ji = (job.row0 + jr) / a.G;
-    const int64_t orow = (job.t0 + ji) * a.H + h * a.G + (job.row0 + jr - ji * a.G);
-    if (job.alone) {
-        const float inv = l == 0.f && m == -kInf ? 0.f : 1.f / l;
-#pragma unroll
-        for (int c = 0; c < C; c += 4)
-            store4(static_cast<TI*>(a.o) + orow * DV + c0 + c,
-                   floatx4{out[c] * inv, out[c + 1] * inv, out[c + 2] * inv, out[c + 3] * inv});
-        return;
-    }
-    const int64_t at = blockIdx.z * (a.T * a.H) + orow;
-#pragma unroll
-    for (int c = 0; c < C; c += 4)
-        *reinterpret_cast<floatx4*>(a.ws_o + at * DV + c0 + c) = floatx4{out[c], out[c + 1], out[c + 2], out[c + 3]};
-    if (c0 == 0) {
-        a.ws_ml[2 * at] = m;
-        a.ws_ml[2 * at + 1] = l;
+    __syncthreads();  // before the next turn's waves write s_o
     }
 }
 
@@ -380,8 +452,19 @@ __global__ __launch_bounds__(64 * kWaves, sizeof(TI) == 4 ? 1 : 2) void attentio
     // last rows, which see most, come first.
     const int h = blockIdx.x % a.Hkv;
     const int64_t id = blockIdx.x / a.Hkv, tiles = gridDim.x / a.Hkv;
-    Job job;
-    if (!find_job<BR>(a, tiles - 1 - id, blockIdx.y, job)) return;
+    const int64_t tile = tiles - 1 - id;
+    const int32_t n = request_of(a, tile, BR);
+    if (n < 0) return;
+    const Request job(a, n);
+    const int64_t row0_ = (tile - first_tile(a, n, BR)) * BR;
+    if (job.few || row0_ < 0 || row0_ >= job.rows) return;
+    const int32_t row0 = (int32_t)row0_, last_row = (row0 + BR < job.rows ? row0 + BR : job.rows) - 1;
+    const int64_t from = blockIdx.y * job.chunk;
+    if (blockIdx.y > 0 && from >= job.kv) return;
+    const int32_t* const table = table_of(a, n);
+    int64_t to = job.kv - job.len + last_row / a.G + 1;  // no row of the tile sees more
+    to = !table ? from : to < from + job.chunk ? to : from + job.chunk;
+    const int64_t all_see = job.kv - job.len + row0 / a.G;  // every row of the tile sees up to here
     const int page_mask = (1 << a.page_log2) - 1;
 
     // Staging: a thread takes 16-byte pieces of keys (a token's 16 channels) and
@@ -390,23 +473,22 @@ __global__ __launch_bounds__(64 * kWaves, sizeof(TI) == 4 ? 1 : 2) void attentio
     uintx4 kr[KP], vr[VP];
     float ks = 0.f, vs = 0.f;
     int32_t page = -1;  // of the tile in kr and vr
-    auto page_of = [&](int64_t base) -> int32_t {
-        if (!job.table || base >= job.to) return -1;
-        const int32_t p = __builtin_amdgcn_readfirstlane(job.table[base >> a.page_log2]);
-        return p < a.num_pages ? p : -1;
-    };
-    auto load = [&](int64_t base, int32_t p) {
-        page = p;
-        if (p < 0) return;
-        const int64_t ph = (int64_t)p * a.Hkv + h, place = (ph << a.page_log2) + (base & page_mask);
+    Pages pages;
+    int at = 0;  // the next tile's lane of `pages`
+    auto load = [&](int64_t base) {
+        if (at == 64) at = 0;
+        if (at == 0) pages.fetch(a, table, h, base, to, kTile);
+        page = __builtin_amdgcn_readlane(pages.page, at);
+        ks = Pages::lane_of(pages.ks, at);
+        vs = Pages::lane_of(pages.vs, at);
+        ++at;
+        const int64_t ph = (int64_t)(page < 0 ? 0 : page) * a.Hkv + h, place = (ph << a.page_log2) + (base & page_mask);
         const uintx4* k = reinterpret_cast<const uintx4*>(a.kc + place * DK) + threadIdx.x;
         const uintx4* v = reinterpret_cast<const uintx4*>(a.vc + place * DV) + threadIdx.x;
 #pragma unroll
         for (int j = 0; j < KP; ++j) kr[j] = k[j * NT];
 #pragma unroll
         for (int j = 0; j < VP; ++j) vr[j] = v[j * NT];
-        ks = a.ks[ph];
-        vs = a.vs[ph];
     };
     auto stage = [&](int64_t base, int buf) {
         if (threadIdx.x == 0) s_there[buf] = page >= 0;
@@ -419,7 +501,7 @@ __global__ __launch_bounds__(64 * kWaves, sizeof(TI) == 4 ? 1 : 2) void attentio
             to[row ^ (step & 7)] = __builtin_bit_cast(uintx4, e4m3_to_bf16x8(kr[j][0], kr[j][1], ks));
             to[(row + 32) ^ (step & 7)] = __builtin_bit_cast(uintx4, e4m3_to_bf16x8(kr[j][2], kr[j][3], ks));
         }
-        const bool edge = base + kTile - 1 > job.all_see;
+        const bool edge = base + kTile - 1 > all_see;
         bool nan = false;
 #pragma unroll
         for (int j = 0; j < VP; ++j) {
@@ -438,33 +520,24 @@ __global__ __launch_bounds__(64 * kWaves, sizeof(TI) == 4 ? 1 : 2) void attentio
         if (nan) s_nan[buf] = 1;
     };
 
-    int32_t next_page = page_of(job.from + kTile);
-    load(job.from, page_of(job.from));
+    if (from < to) load(from);
 
     // this lane's row
-    const int64_t row = job.row0 + 32 * wave + c;
+    const int32_t row = row0 + 32 * wave + c;
     const bool live = row < job.rows;
-    const int64_t i = live ? row / a.G : 0;
-    const int32_t head = h * a.G + (int32_t)(live ? row - i * a.G : 0);
-    const int64_t sees = live ? job.kv - job.len + i : -1;
+    const int32_t i = live ? row / a.G : 0, head = h * a.G + (live ? row - i * a.G : 0);
+    const int64_t sees = live ? job.kv - job.len + i : -1;  // the last token that the row sees
     const int64_t orow = (job.t0 + i) * a.H + head;
-    // Tokens that some row of this wave sees end here; before all_see every row does.
-    const int64_t wrow = job.row0 + 32 * wave, wlast = wrow + 31 < job.rows ? wrow + 31 : job.rows - 1;
+    // Of this wave: no row sees tokens from wave_to on, every row sees those up to wave_all.
+    const int32_t wrow = row0 + 32 * wave, wlast = wrow + 31 < job.rows ? wrow + 31 : job.rows - 1;
     const int64_t wave_to = wrow < job.rows ? job.kv - job.len + wlast / a.G + 1 : 0;
     const int64_t wave_all = job.kv - job.len + (wrow < job.rows ? wrow : 0) / a.G;
-    bf16x8 qf[NS][KS];
-    {
-        const TI* q = static_cast<const TI*>(a.q) + orow * DK + 8 * hf;
+    Eight<TI> q8[KS];
 #pragma unroll
-        for (int m = 0; m < KS; ++m)
+    for (int m = 0; m < KS; ++m) q8[m].load(static_cast<const TI*>(a.q) + orow * DK + 16 * m + 8 * hf);
+    bf16x8 qf[KS][NS];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                bf16 part[NS];
-                split_bf16<NS>(live ? to_f32(q[16 * m + j]) : 0.f, part);
-#pragma unroll
-                for (int s = 0; s < NS; ++s) qf[s][m][j] = part[s];
-            }
-    }
+    for (int m = 0; m < KS; ++m) q8[m].split(qf[m]);
 
     floatx16 O[DT];
 #pragma unroll
@@ -472,12 +545,11 @@ __global__ __launch_bounds__(64 * kWaves, sizeof(TI) == 4 ? 1 : 2) void attentio
     float mx = -kInf, ref = 0.f, sum = 0.f;  // ref: the maximum that O and sum are scaled by
     if (threadIdx.x < 2) s_nan[threadIdx.x] = 0;
     __syncthreads();
-    stage(job.from, 0);
-    load(job.from + kTile, next_page);
-    next_page = page_of(job.from + 2 * kTile);
+    stage(from, 0);
+    if (from < to) load(from + kTile);
     __syncthreads();
     int buf = 0;
-    for (int64_t base = job.from; base < job.to; base += kTile, buf ^= 1) {
+    for (int64_t base = from; base < to; base += kTile, buf ^= 1) {
         if (s_there[buf] && base < wave_to) {
             float s[32];
 #pragma unroll
@@ -487,7 +559,7 @@ __global__ __launch_bounds__(64 * kWaves, sizeof(TI) == 4 ? 1 : 2) void attentio
                 for (int m = 0; m < KS; ++m) {
                     const bf16x8 k8 = __builtin_bit_cast(bf16x8, s_k[buf][half * KS + m][lane ^ (m & 7)]);
 #pragma unroll
-                    for (int p = NS - 1; p >= 0; --p) x = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k8, qf[p][m], x, 0, 0, 0);
+                    for (int p = NS - 1; p >= 0; --p) x = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k8, qf[m][p], x, 0, 0, 0);
                 }
 #pragma unroll
                 for (int j = 0; j < 16; ++j) s[16 * half + j] = x[j] * a.scale2;
@@ -524,7 +596,7 @@ __global__ __launch_bounds__(64 * kWaves, sizeof(TI) == 4 ? 1 : 2) void attentio
             if (s_nan[buf]) {
                 // Some value of the tile is NaN (staged as 0): read the codes again
                 // and mark the outputs of the rows that see one.
-                const int32_t pg = job.table[base >> a.page_log2];
+                const int32_t pg = table[base >> a.page_log2];
                 const int64_t place = (((int64_t)pg * a.Hkv + h) << a.page_log2) + (base & page_mask);
 #pragma unroll 1
                 for (int half = 0; half < 2; ++half) {
@@ -555,156 +627,192 @@ __global__ __launch_bounds__(64 * kWaves, sizeof(TI) == 4 ? 1 : 2) void attentio
                     for (int p = NS - 1; p >= 0; --p) O[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v8, pf[p][k], O[d], 0, 0, 0);
                 }
         }
-        if (base + kTile < job.to) {
+        if (base + kTile < to) {
             // The other buffer's readers have met at the last barrier.
             if (threadIdx.x == 0) s_nan[buf ^ 1] = 0;
-            const bool may_be_nan = base + 2 * kTile - 1 > job.all_see;
+            const bool may_be_nan = base + 2 * kTile - 1 > all_see;
             if (may_be_nan) __syncthreads();  // the flag is cleared before it is set
             stage(base + kTile, buf ^ 1);
-            load(base + 2 * kTile, next_page);
-            next_page = page_of(base + 3 * kTile);
+            load(base + 2 * kTile);
             __syncthreads();
         }
     }
     sum += __shfl_xor(sum, 32);
     if (!live) return;
-    const float inv = !job.alone ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
-    const int64_t at = blockIdx.y * (a.T * a.H) + orow;
+    const bool alone = job.alone();
+    const float inv = !alone ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
+    const int64_t prow = blockIdx.y * part_rows(a, false) + orow;
 #pragma unroll
     for (int d = 0; d < DT; ++d)
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             const floatx4 x = {O[d][4 * q] * inv, O[d][4 * q + 1] * inv, O[d][4 * q + 2] * inv, O[d][4 * q + 3] * inv};
             const int ch = 32 * d + 8 * q + 4 * hf;
-            if (job.alone) store4(static_cast<TI*>(a.o) + orow * DV + ch, x);
-            else *reinterpret_cast<floatx4*>(a.ws_o + at * DV + ch) = x;
+            if (alone) store4(static_cast<TI*>(a.o) + orow * DV + ch, x);
+            else *reinterpret_cast<floatx4*>(a.ws_o[1] + prow * DV + ch) = x;
         }
-    if (!job.alone && hf == 0) {
-        a.ws_ml[2 * at] = sum == 0.f ? -kInf : ref;
-        a.ws_ml[2 * at + 1] = sum;
+    if (!alone && hf == 0) {
+        a.ws_ml[1][2 * prow] = sum == 0.f ? -kInf : ref;
+        a.ws_ml[1][2 * prow + 1] = sum;
     }
 }
 
 // ---------------------------------------------------------------- joining parts
 //
-// A workgroup per row: DV / 4 threads for the channels of a part, several parts
-// side by side.
-template <typename TI, int DV>
+// W waves per row, one or four as there are few or many parts: DV / 4 lanes for
+// the channels of a part, several parts side by side.
+template <typename TI, int DV, bool FEW, int W>
 __global__ __launch_bounds__(256) void attention_join_kernel(Attention a) {
-    constexpr int L = DV / 4, STEP = 256 / L;
-    __shared__ floatx4 s_o[STEP][L];
-    __shared__ float s_l[STEP], s_m[4];
-    const int lane = threadIdx.x & 63;
-    const int64_t row = blockIdx.x, t = row / a.H;
-    int32_t below = 0;
-    bool in = false;
-    for (int32_t n0 = 0; n0 <= a.num_seqs; n0 += 64) {
-        const int32_t n = n0 + lane;
-        const bool on = n <= a.num_seqs && a.cu[n] <= t;
-        below += __popcll(__ballot(on && n < a.num_seqs));
-        in |= __ballot(on && n == a.num_seqs) != 0;
+    constexpr int L = DV / 4, STEP = 64 * W / L, ROWS = kWaves / W;
+    __shared__ floatx4 s_o[STEP * ROWS][L];
+    __shared__ float s_l[STEP * ROWS], s_m[kWaves];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, thread = threadIdx.x % (64 * W);
+    const int64_t r = (int64_t)blockIdx.x * ROWS + wave / W;
+    int32_t n = -1;
+    int64_t orow = r;
+    bool mine = r < part_rows(a, FEW);
+    if (FEW) {
+        n = (int32_t)(r / ((int64_t)a.Hkv * a.few_rows));
+    } else if (mine) {
+        const int64_t t = r / a.H;
+        int32_t below = 0;
+        for (int32_t n0 = 0; n0 <= a.num_seqs; n0 += 64) below += __popcll(__ballot(n0 + lane <= a.num_seqs && a.cu[n0 + lane] <= t));
+        n = below - 1;
+        if (n >= a.num_seqs) n = -1;  // behind the last request
     }
-    const int32_t n = below - 1;
-    if (in || n < 0) return;  // behind the last request
-    const int64_t kv = held_tokens(a, n), chunk = chunk_of(a, kv);
-    if (kv <= chunk) return;  // written by its one workgroup
-    const int parts = (int)((kv + chunk - 1) / chunk);
-    const int64_t step = a.T * a.H;
+    int parts = 0;
+    if (mine && n >= 0) {
+        const Request q(a, n);
+        parts = q.few == FEW && !q.alone() ? (int)((q.kv + q.chunk - 1) / q.chunk) : 0;
+        if (FEW) {
+            const int32_t row = (int32_t)(r % a.few_rows), h = (int32_t)(r / a.few_rows % a.Hkv), i = row / a.G;
+            if (row >= q.rows) parts = 0;
+            orow = (q.t0 + i) * a.H + h * a.G + (row - i * a.G);
+        }
+    }
+    if (W == kWaves && parts == 0) return;  // the whole workgroup
+    const int64_t step = part_rows(a, FEW);
+    const float *ml = a.ws_ml[FEW ? 0 : 1], *wo = a.ws_o[FEW ? 0 : 1];
     float m = -kInf;
-    for (int s = threadIdx.x; s < parts; s += 256) m = fmaxf(m, a.ws_ml[2 * (s * step + row)]);
+    for (int s = thread; s < parts; s += 64 * W) m = fmaxf(m, ml[2 * (s * step + r)]);
 #pragma unroll
     for (int off = 32; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor(m, off));
-    if (lane == 0) s_m[threadIdx.x >> 6] = m;
-    __syncthreads();
-    m = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
+    if (W > 1) {
+        if (lane == 0) s_m[wave] = m;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) m = fmaxf(m, s_m[w]);
+    }
     const float ref = m == -kInf ? 0.f : m;
-    const int c = threadIdx.x % L, s0 = threadIdx.x / L;
+    const int c = thread % L, s0 = thread / L, at0 = wave / W * STEP;
     float l = 0.f;
     floatx4 out = zero4();
 #pragma unroll 4
     for (int s = s0; s < parts; s += STEP) {
-        const int64_t at = s * step + row;
-        const float f = __builtin_amdgcn_exp2f(a.ws_ml[2 * at] - ref);
-        l += f * a.ws_ml[2 * at + 1];
-        out += f * *reinterpret_cast<const floatx4*>(a.ws_o + at * DV + 4 * c);
+        const int64_t at = s * step + r;
+        const float f = __builtin_amdgcn_exp2f(ml[2 * at] - ref);
+        l += f * ml[2 * at + 1];
+        out += f * *reinterpret_cast<const floatx4*>(wo + at * DV + 4 * c);
     }
-    s_o[s0][c] = out;
-    if (c == 0) s_l[s0] = l;
+    s_o[at0 + s0][c] = out;
+    if (c == 0) s_l[at0 + s0] = l;
     __syncthreads();
-    if (s0 > 0) return;
+    if (s0 > 0 || parts == 0) return;
 #pragma unroll
     for (int s = 1; s < STEP; ++s) {
-        out += s_o[s][c];
-        l += s_l[s];
+        out += s_o[at0 + s][c];
+        l += s_l[at0 + s];
     }
     const float inv = l == 0.f && m == -kInf ? 0.f : 1.f / l;
-    store4(static_cast<TI*>(a.o) + row * DV + 4 * c, out * inv);
+    store4(static_cast<TI*>(a.o) + orow * DV + 4 * c, out * inv);
 }
 
 // ---------------------------------------------------------------- planning
 
+constexpr int64_t kAtOnce = 512;  // workgroups that the device holds: two on each compute unit
+
 struct Plan {
     bool few, many;  // kernels that the call needs
-    int32_t splits, min_chunk;
-    size_t ml_off, bytes;
+    int32_t few_rows, splits[2], min_chunk[2];
+    size_t off[4], bytes;  // ws_o and ws_ml of few, of the others
 };
 
 // The lengths are on the device, so the plan goes by sizes and bounds.  A
 // request has at most max_new (or T_total) new tokens: whether that is few rows
 // decides which kernels run.  Each request's cache is cut into at most `splits`
-// parts of at least min_chunk tokens: enough of them to fill the device when
-// every request is as long as the bound, and, for few rows, so that no part of
-// the longest request is above 8192 tokens.
+// parts of at least min_chunk tokens, so that there are enough workgroups when
+// every request is as long as the bound, and so that the lengths, which may
+// differ much, do not leave the device waiting for a few long parts.
 Plan plan(const CacheAttentionLaunch& p) {
     Plan r = {};
+    auto up = [](int64_t x, int64_t y) { return (x + y - 1) / y; };
     const int64_t room = (int64_t)p.max_blocks * p.page_size;
     const int64_t kv = p.max_kv > 0 && p.max_kv < room ? p.max_kv : room;
     const int64_t G = p.H / p.H_kv, all = p.T_total * G;
     const int64_t most = p.max_new > 0 && p.max_new < p.T_total ? p.max_new * G : all;
     r.many = most > kFewRows;
     r.few = !r.many || p.num_seqs > 1;
-    const int64_t per = r.many ? 32 * kWaves : 16, target = r.many ? 512 : 1024;
-    const int64_t tiles = (all + per - 1) / per > p.num_seqs ? (all + per - 1) / per : p.num_seqs;
-    const int64_t units = tiles * p.H_kv;
-    int64_t splits = units >= target ? 1 : (target + units - 1) / units;
-    r.min_chunk = units >= target ? 8192 : r.many ? 512 : 256;
-    if (r.few && splits < (kv + 8191) / 8192) splits = (kv + 8191) / 8192;
-    if (splits > (kv + r.min_chunk - 1) / r.min_chunk) splits = (kv + r.min_chunk - 1) / r.min_chunk;
-    if (splits < 1) splits = 1;
-    if (splits > 256) splits = 256;
-    r.splits = (int32_t)splits;
-    if (splits > 1) {
-        const size_t rows = (size_t)splits * p.T_total * p.H;
-        r.ml_off = (rows * p.dv * sizeof(float) + 255) & ~(size_t)255;
-        r.bytes = r.ml_off + ((rows * 2 * sizeof(float) + 255) & ~(size_t)255);
+    r.few_rows = (int32_t)(most < kFewRows ? most : kFewRows);
+    r.splits[0] = r.splits[1] = 1;
+    r.min_chunk[0] = r.min_chunk[1] = kTile;
+    if (r.few) {
+        const int64_t units = (int64_t)p.num_seqs * p.H_kv * up(r.few_rows, 16);
+        int64_t chunk = up(up(kv * units, kAtOnce), kTile) * kTile;
+        chunk = chunk < 512 ? 512 : chunk > 8192 ? 8192 : chunk;
+        const int64_t splits = up(kv, chunk);
+        r.splits[0] = (int32_t)(splits < 1 ? 1 : splits > 256 ? 256 : splits);
+        r.min_chunk[0] = (int32_t)chunk;
     }
+    if (r.many) {
+        const int64_t tiles = up(all, 32 * kWaves) > p.num_seqs ? up(all, 32 * kWaves) : p.num_seqs, units = tiles * p.H_kv;
+        int64_t splits = units >= kAtOnce ? 1 : up(kAtOnce, units);
+        if (splits > up(kv, 512)) splits = up(kv, 512);
+        r.splits[1] = (int32_t)(splits < 1 ? 1 : splits);
+        r.min_chunk[1] = 512;
+    }
+    auto take = [&](size_t bytes) {
+        const size_t at = r.bytes;
+        r.bytes += (bytes + 255) & ~(size_t)255;
+        return at;
+    };
+    for (int c = 0; c < 2; ++c)
+        if (r.splits[c] > 1) {
+            const size_t rows = (size_t)r.splits[c] * (c == 0 ? (size_t)p.num_seqs * p.H_kv * r.few_rows : (size_t)p.T_total * p.H);
+            r.off[2 * c] = take(rows * p.dv * sizeof(float));
+            r.off[2 * c + 1] = take(rows * 2 * sizeof(float));
+        }
     return r;
 }
 
 template <typename TI, int DK, int DV>
-hipError_t run(Attention a, const Plan& pl, hipStream_t s) {
-    const int64_t all = a.T * a.G;
+hipError_t run(const Attention& a, const Plan& pl, hipStream_t s) {
+    hipError_t e = hipSuccess;
     if (pl.many) {
-        a.more_rows = pl.few ? kFewRows : 0;
-        a.most_rows = INT64_MAX;
-        const int64_t tiles = all / (32 * kWaves) + a.num_seqs;
-        hipLaunchKernelGGL((attention_tile_kernel<TI, DK, DV>), dim3((unsigned)(tiles * a.Hkv), (unsigned)a.splits),
+        const int64_t tiles = a.T * a.G / (32 * kWaves) + a.num_seqs;
+        hipLaunchKernelGGL((attention_tile_kernel<TI, DK, DV>), dim3((unsigned)(tiles * a.Hkv), (unsigned)a.splits[1]),
                            dim3(64 * kWaves), 0, s, a);
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
+        if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     if (pl.few) {
-        a.more_rows = 0;
-        a.most_rows = pl.many ? kFewRows : INT64_MAX;
-        const int64_t tiles = all / 16 + a.num_seqs;
-        hipLaunchKernelGGL((attention_rows_kernel<TI, DK, DV>), dim3((unsigned)tiles, (unsigned)a.Hkv, (unsigned)a.splits),
-                           dim3(64 * kWaves), 0, s, a);
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
+        const dim3 grid((unsigned)(a.num_seqs * ((a.few_rows + 15) / 16)), (unsigned)a.Hkv, (unsigned)a.splits[0]);
+        hipLaunchKernelGGL((attention_rows_kernel<TI, DK, DV>), grid, dim3(64 * kWaves), 0, s, a);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
     }
-    if (a.splits == 1) return hipSuccess;
-    hipLaunchKernelGGL((attention_join_kernel<TI, DV>), dim3((unsigned)(a.T * a.H)), dim3(256), 0, s, a);
-    return hipGetLastError();
+    if (a.splits[0] > 1) {
+        const int64_t rows = (int64_t)a.num_seqs * a.Hkv * a.few_rows;
+        if (a.splits[0] > 16)
+            hipLaunchKernelGGL((attention_join_kernel<TI, DV, true, kWaves>), dim3((unsigned)rows), dim3(256), 0, s, a);
+        else
+            hipLaunchKernelGGL((attention_join_kernel<TI, DV, true, 1>), dim3((unsigned)((rows + kWaves - 1) / kWaves)),
+                               dim3(256), 0, s, a);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+    if (a.splits[1] > 1) {
+        const int64_t rows = a.T * a.H;
+        hipLaunchKernelGGL((attention_join_kernel<TI, DV, false, 1>), dim3((unsigned)((rows + kWaves - 1) / kWaves)), dim3(256), 0, s, a);
+        e = hipGetLastError();
+    }
+    return e;
 }
 template <typename TI>
 hipError_t run_t(const Attention& a, const CacheAttentionLaunch& p, const Plan& pl, hipStream_t s) {
@@ -728,9 +836,15 @@ hipError_t launch_cache_attention(const CacheAttentionLaunch& p, hipStream_t s) 
     a.page_log2 = p.page_size == 64 ? 6 : p.page_size == 128 ? 7 : 8;
     a.num_rows = p.num_rows; a.max_blocks = p.max_blocks;
     a.scale2 = p.scale * kLog2e; a.o = p.o; a.H = p.H; a.Hkv = p.H_kv; a.G = p.H / p.H_kv;
-    a.splits = pl.splits; a.min_chunk = pl.min_chunk;
-    a.ws_o = static_cast<float*>(p.workspace);
-    a.ws_ml = reinterpret_cast<float*>(static_cast<char*>(p.workspace) + pl.ml_off);
+    a.few_rows = pl.few_rows;
+    a.tiled = pl.many;
+    for (int c = 0; c < 2; ++c) {
+        a.splits[c] = pl.splits[c];
+        a.min_chunk[c] = pl.min_chunk[c];
+        a.ws_o[c] = reinterpret_cast<float*>(static_cast<char*>(p.workspace) + pl.off[2 * c]);
+        a.ws_ml[c] = reinterpret_cast<float*>(static_cast<char*>(p.workspace) + pl.off[2 * c + 1]);
+    }
+    if (!pl.few) a.few_rows = 0;  // every request goes to the tile kernel
     return p.bf16 ? run_t<bf16>(a, p, pl, s) : run_t<float>(a, p, pl, s);
 }
 
