@@ -20,6 +20,7 @@
 // as it is stored.  Codes are converted to bf16 exactly, and a page's scale, a
 // power of two, is applied exactly, to the scores and p or in the conversion.
 #include "gdn_e4m3.h"
+#include "gdn_lanes.h"
 #include "gdn_mfma.h"
 #include "gdn_serve_kernels.h"
 
@@ -307,8 +308,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_rows_kernel(Attentio
             float top = s[0];
 #pragma unroll
             for (int j = 1; j < 16; ++j) top = fmaxf(top, s[j]);
-            top = fmaxf(top, __shfl_xor(top, 16));
-            top = fmaxf(top, __shfl_xor(top, 32));
+            top = across<Max, 16>(top);
             const float now = fmaxf(mx, top);
             const float ref = now == -kInf ? 0.f : now;
             const float fade = __builtin_amdgcn_exp2f(mx - ref);
@@ -369,8 +369,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_rows_kernel(Attentio
         ks = Pages::lane_of(pages.ks, at);
         vs = Pages::lane_of(pages.vs, at);
     }
-    sum += __shfl_xor(sum, 16);
-    sum += __shfl_xor(sum, 32);
+    sum = across<Sum, 16>(sum);
     // The wave's output takes the place of its keys.
     float(*const s_o)[DV + 4] = reinterpret_cast<float(*)[DV + 4]>(s_k);
 #pragma unroll
@@ -573,7 +572,7 @@ __global__ __launch_bounds__(64 * kWaves, sizeof(TI) == 4 ? 1 : 2) void attentio
             float top = s[0];
 #pragma unroll
             for (int j = 1; j < 32; ++j) top = fmaxf(top, s[j]);
-            top = fmaxf(top, __shfl_xor(top, 32));
+            top = across<Max, 32>(top);
             mx = fmaxf(mx, top);
             if (__ballot(mx > ref + kSlack || (ref == 0.f && sum == 0.f))) {
                 const float now = mx == -kInf ? 0.f : mx;
@@ -637,7 +636,7 @@ __global__ __launch_bounds__(64 * kWaves, sizeof(TI) == 4 ? 1 : 2) void attentio
             __syncthreads();
         }
     }
-    sum += __shfl_xor(sum, 32);
+    sum = across<Sum, 32>(sum);
     if (!live) return;
     const bool alone = job.alone();
     const float inv = !alone ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
@@ -695,8 +694,7 @@ __global__ __launch_bounds__(256) void attention_join_kernel(Attention a) {
     const float *ml = a.ws_ml[FEW ? 0 : 1], *wo = a.ws_o[FEW ? 0 : 1];
     float m = -kInf;
     for (int s = thread; s < parts; s += 64 * W) m = fmaxf(m, ml[2 * (s * step + r)]);
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor(m, off));
+    m = across<Max>(m);
     if (W > 1) {
         if (lane == 0) s_m[wave] = m;
         __syncthreads();

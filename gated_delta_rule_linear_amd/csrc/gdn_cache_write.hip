@@ -15,6 +15,7 @@
 // Three operations per element: bound by the bytes read (2 or 4 for each) and
 // written (1).
 #include "gdn_e4m3.h"
+#include "gdn_lanes.h"
 #include "gdn_serve_kernels.h"
 
 namespace gdn {
@@ -81,12 +82,6 @@ __device__ __forceinline__ uintx2 eight_codes(const Eight<T>& e, float inv) {
     return uintx2{to_e4m3(f[0], f[1], f[2], f[3]), to_e4m3(f[4], f[5], f[6], f[7])};
 }
 
-__device__ __forceinline__ float wave_max(float x) {
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) x = fmaxf(x, __shfl_xor(x, off));
-    return x;
-}
-
 // The page's scale behind the run and what its older codes are multiplied by (0:
 // the page begins anew).
 struct Scales {
@@ -124,7 +119,7 @@ __device__ void write_keys(const Write& w, const Run& r, int h, int thread, floa
         if (i0 + u * STEP < len)
 #pragma unroll
             for (int j = 0; j < 8; ++j) top = fmaxf(top, finite_abs(to_f32(e[u].x[j])));
-    top = wave_max(top);
+    top = across<Max>(top);
     if constexpr (W > 1) {
         if (thread % 64 == 0) lds[thread / 64] = top;
         __syncthreads();  // every thread has read the scale, too
@@ -180,7 +175,7 @@ __device__ void write_values(const Write& w, const Run& r, int h, int thread, fl
     for (int u = 0; u < GROUPS; ++u)
 #pragma unroll
         for (int j = 0; j < 16; ++j) top = fmaxf(top, fmaxf(finite_abs(e[u][j].get(0)), finite_abs(e[u][j].get(1))));
-    top = wave_max(top);
+    top = across<Max>(top);
     if constexpr (W > 1) {
         if (thread % 64 == 0) lds[thread / 64] = top;
         __syncthreads();
@@ -241,7 +236,7 @@ __device__ void write_values_short(const Write& w, const Run& r, int h, int lane
     for (int j = 0; j < kShort; ++j)
 #pragma unroll
         for (int c = 0; c < C; ++c) top = fmaxf(top, finite_abs(e[j][c]));
-    const Scales s = new_scale(r, was, wave_max(top));
+    const Scales s = new_scale(r, was, across<Max>(top));
     const float inv = 1.f / s.now;
     if (lane == 0) *scale = s.now;
     uint8_t* to = w.vc + (r.page * w.H + h) * (int64_t)page * D + C * lane * 16;

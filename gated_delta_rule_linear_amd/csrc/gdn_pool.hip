@@ -10,10 +10,11 @@
 // A wave owns all d_k rows of kCols value columns of one (request, head), since
 // the columns of S evolve independently: a lane holds 4 neighbouring columns
 // (16 bytes) of d_k / kRowGroups neighbouring rows in registers for all the
-// tokens, and the sums over rows end in a butterfly over the lanes of the wave.
+// tokens, and the sums over rows end in exchanges between the lanes of the wave.
 // Tokens therefore need no barrier and no LDS.  The state is touched once: it
 // is read and written with non-temporal hints.
 #include "gdn_device.h"
+#include "gdn_lanes.h"
 #include "gdn_serve_kernels.h"
 
 namespace gdn {
@@ -35,35 +36,43 @@ struct Pool {
 };
 
 template <typename T, int N>
-__device__ __forceinline__ void load_row(const T* p, float* x) {
-    if constexpr (sizeof(T) == 4) {
+__device__ __forceinline__ void load_row(const T* p, T* x) {
+    constexpr int V = (int)(16 / sizeof(T)) < N ? (int)(16 / sizeof(T)) : N;  // a load of 16 bytes, or all of N
+    typedef T vec __attribute__((ext_vector_type(V)));
 #pragma unroll
-        for (int j = 0; j < N; j += 4) {
-            const floatx4 y = *reinterpret_cast<const floatx4*>(p + j);
-            x[j] = y[0]; x[j + 1] = y[1]; x[j + 2] = y[2]; x[j + 3] = y[3];
-        }
-    } else {
+    for (int j = 0; j < N; j += V) {
+        const vec y = *reinterpret_cast<const vec*>(p + j);
 #pragma unroll
-        for (int j = 0; j < N; j += 4) {
-            const bf16x4 y = *reinterpret_cast<const bf16x4*>(p + j);
-            x[j] = (float)y[0]; x[j + 1] = (float)y[1]; x[j + 2] = (float)y[2]; x[j + 3] = (float)y[3];
-        }
+        for (int i = 0; i < V; ++i) x[j + i] = y[i];
     }
 }
 
-__device__ __forceinline__ float rows_sum(float x) {
-#pragma unroll
-    for (int off = kColLanes; off < 64; off <<= 1) x += __shfl_xor(x, off);
-    return x;
-}
+__device__ __forceinline__ float rows_sum(float x) { return across<Sum, kColLanes>(x); }
 __device__ __forceinline__ floatx4 rows_sum(floatx4 x) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) x[i] = rows_sum(x[i]);
     return x;
 }
 
-template <typename TI, int DK, int DV, bool HEAD>
-__global__ __launch_bounds__(DV / kCols * 64) void pool_kernel(Pool a) {
+// A token's vectors, as a lane needs them.
+template <typename TI, int NR, bool HEAD>
+struct Token {
+    TI k[NR], q[NR], v[4];
+    float g[HEAD ? 1 : NR], beta;
+    __device__ __forceinline__ void load(const Pool& a, int64_t t, int32_t h, int32_t hk, int row, int dk, int col, int dv) {
+        const int64_t th = t * a.H + h, tk = (t * a.Hk + hk) * dk + row;
+        load_row<TI, NR>(static_cast<const TI*>(a.k) + tk, k);
+        load_row<TI, NR>(static_cast<const TI*>(a.q) + tk, q);
+        if constexpr (HEAD) g[0] = a.g[th];
+        else load_row<float, NR>(a.g + th * dk + row, g);
+        load_row<TI, 4>(static_cast<const TI*>(a.v) + th * dv + col, v);
+        beta = a.beta[th];
+    }
+};
+
+// MANY: a request may have more than one token.
+template <typename TI, int DK, int DV, bool HEAD, bool MANY>
+__global__ __launch_bounds__(DV / kCols * 64, MANY ? 2 : 4) void pool_kernel(Pool a) {
     constexpr int NR = DK / kRowGroups;  // rows of a lane
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t n = blockIdx.x / a.H;
@@ -71,7 +80,7 @@ __global__ __launch_bounds__(DV / kCols * 64) void pool_kernel(Pool a) {
     const int32_t slot = a.slots[n];
     if (slot < 0 || slot >= a.num_slots) return;
     int64_t t0 = n, t1 = n + 1;
-    if (a.cu) {
+    if (MANY) {
         t0 = a.cu[n]; t1 = a.cu[n + 1];
         if (t0 < 0) t0 = 0;
         if (t1 > a.T) t1 = a.T;
@@ -83,31 +92,26 @@ __global__ __launch_bounds__(DV / kCols * 64) void pool_kernel(Pool a) {
     const int rg = lane / kColLanes, col = wave * kCols + 4 * (lane % kColLanes);
     const int row = rg * NR;
     float* S = a.states + (((int64_t)slot * a.H + h) * DK + row) * DV + col;
+    Token<TI, NR, HEAD> next;
+    next.load(a, t0, h, hk, row, DK, col, DV);
     floatx4 s[NR];
 #pragma unroll
     for (int j = 0; j < NR; ++j) s[j] = __builtin_nontemporal_load(reinterpret_cast<const floatx4*>(S + j * DV));
     for (int64_t t = t0; t < t1; ++t) {
-        const int64_t th = t * a.H + h;
-        float k[NR], q[NR], al[NR];
-        load_row<TI, NR>(static_cast<const TI*>(a.k) + (t * a.Hk + hk) * DK + row, k);
-        load_row<TI, NR>(static_cast<const TI*>(a.q) + (t * a.Hk + hk) * DK + row, q);
-        if constexpr (HEAD) {
-            const float e = __expf(a.g[th]);
+        const Token<TI, NR, HEAD> x = next;
+        // the next token's vectors are on their way while this one is worked on
+        if (MANY && t + 1 < t1) next.load(a, t + 1, h, hk, row, DK, col, DV);
+        float k[NR], q[NR];
+        floatx4 v, r = {0.f, 0.f, 0.f, 0.f}, p = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int j = 0; j < NR; ++j) al[j] = e;
-        } else {
-            load_row<float, NR>(a.g + th * DK + row, al);
-#pragma unroll
-            for (int j = 0; j < NR; ++j) al[j] = __expf(al[j]);
-        }
-        floatx4 v;
-        load_row<TI, 4>(static_cast<const TI*>(a.v) + th * DV + col, reinterpret_cast<float*>(&v));
-        const float beta = a.beta[th];
-        floatx4 r = {0.f, 0.f, 0.f, 0.f}, p = {0.f, 0.f, 0.f, 0.f};
+        for (int j = 0; j < 4; ++j) v[j] = to_f32(x.v[j]);
+        const float head_decay = __expf(x.g[0]);  // with one gate per head
         float kq = 0.f, kk = 0.f, qq = 0.f;
 #pragma unroll
         for (int j = 0; j < NR; ++j) {
-            s[j] *= al[j];
+            k[j] = to_f32(x.k[j]);
+            q[j] = to_f32(x.q[j]);
+            s[j] *= HEAD ? head_decay : __expf(x.g[HEAD ? 0 : j]);
             r += s[j] * k[j];
             p += s[j] * q[j];
             kq += k[j] * q[j];
@@ -127,13 +131,13 @@ __global__ __launch_bounds__(DV / kCols * 64) void pool_kernel(Pool a) {
             ck = 1.f / sqrtf(rows_sum(kk) + a.eps);
             cq *= 1.f / sqrtf(rows_sum(qq) + a.eps);
         }
-        const floatx4 u = beta * (v - ck * r);
+        const floatx4 u = x.beta * (v - ck * r);
         const floatx4 out = cq * (p + (ck * kq) * u);
         const floatx4 w = ck * u;
 #pragma unroll
         for (int j = 0; j < NR; ++j) s[j] += w * k[j];
         if (rg == 0) {
-            TI* o = static_cast<TI*>(a.o) + th * DV + col;
+            TI* o = static_cast<TI*>(a.o) + (t * a.H + h) * DV + col;
             if constexpr (sizeof(TI) == 4) *reinterpret_cast<floatx4*>(o) = out;
             else *reinterpret_cast<bf16x4*>(o) = bf16x4{(bf16)out[0], (bf16)out[1], (bf16)out[2], (bf16)out[3]};
         }
@@ -145,8 +149,11 @@ __global__ __launch_bounds__(DV / kCols * 64) void pool_kernel(Pool a) {
 
 template <typename TI, int DK, int DV>
 hipError_t run(const Pool& a, bool head, unsigned units, hipStream_t s) {
-    if (head) hipLaunchKernelGGL((pool_kernel<TI, DK, DV, true>), dim3(units), dim3(DV / kCols * 64), 0, s, a);
-    else hipLaunchKernelGGL((pool_kernel<TI, DK, DV, false>), dim3(units), dim3(DV / kCols * 64), 0, s, a);
+    const dim3 grid(units), block(DV / kCols * 64);
+    if (head && a.cu) hipLaunchKernelGGL((pool_kernel<TI, DK, DV, true, true>), grid, block, 0, s, a);
+    else if (head) hipLaunchKernelGGL((pool_kernel<TI, DK, DV, true, false>), grid, block, 0, s, a);
+    else if (a.cu) hipLaunchKernelGGL((pool_kernel<TI, DK, DV, false, true>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((pool_kernel<TI, DK, DV, false, false>), grid, block, 0, s, a);
     return hipGetLastError();
 }
 template <typename TI>
