@@ -165,7 +165,7 @@ int32_t gdn_cache_write(const void* k, const void* v, const int32_t* slots, int6
     if (!supported_dtype(dtype) || !supported_d(d_k) || !supported_d(d_v) || !supported_page(page_size))
         return GDN_ERR_UNSUPPORTED;
     if (num_pages > ((int64_t)INT32_MAX + 1) / page_size) return GDN_ERR_UNSUPPORTED;  // slots are int32
-    if (T_total > ((int64_t)1 << 28)) return GDN_ERR_UNSUPPORTED;
+    if (T_total * H_kv > ((int64_t)1 << 28)) return GDN_ERR_UNSUPPORTED;  // a grid of less than 2^24 workgroups
     if (T_total == 0 || num_pages == 0) return GDN_OK;
     for (const void* x : {k, v, static_cast<const void*>(k_cache), static_cast<const void*>(v_cache)})
         if (!aligned(x, 16)) return GDN_ERR_INVALID_ARG;

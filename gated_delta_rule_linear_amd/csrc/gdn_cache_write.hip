@@ -284,46 +284,52 @@ __global__ __launch_bounds__(64 * kWaves) void cache_write_kernel(Write w) {
     __shared__ float lds[2][kWaves];
     constexpr int page = 64 * PG;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t t0 = (int64_t)blockIdx.x * w.tile;
-    const bool values = (int)blockIdx.y >= w.H;
-    const int h = values ? blockIdx.y - w.H : blockIdx.y;
-    // Runs that start in this tile: every wave finds them, a lane for each token.
-    bool leader = false;
-    if (lane < w.tile && t0 + lane < w.T) {
-        const int64_t t = t0 + lane, s = w.slots[t], before = t > 0 ? w.slots[t - 1] : -1;
-        leader = s >= 0 && s < w.places && (s % page == 0 || before != s - 1);
+    // The heads' keys and values of a tile of tokens are neighbours in memory and
+    // in the grid.
+    const int64_t t0 = (int64_t)(blockIdx.x / (2 * w.H)) * w.tile;
+    const int y = blockIdx.x % (2 * w.H), h = y >= w.H ? y - w.H : y;
+    const bool values = y >= w.H;
+    // Runs that start in this tile: every wave finds them, a lane for each of the
+    // 64 tokens from the tile's first.
+    int64_t slot = -1, before = -1;
+    if (t0 + lane < w.T) {
+        slot = w.slots[t0 + lane];
+        if (t0 + lane > 0) before = w.slots[t0 + lane - 1];
     }
-    uint64_t todo = __ballot(leader);
-    for (int turn = 0; todo; ++turn) {
+    const bool on = slot >= 0 && slot < w.places, first = on && (slot % page == 0 || before != slot - 1);
+    uint64_t todo = __ballot(first && lane < w.tile);
+    const uint64_t joined = __ballot(on && !first);  // tokens in a run with the one before
+    for (int shorts = 0, longs = 0; todo;) {
         const int at = __ffsll((unsigned long long)todo) - 1;
         todo &= todo - 1;
         Run r;
         r.t = t0 + at;
-        const int64_t s = w.slots[r.t];
+        const int64_t s = __builtin_amdgcn_readlane((int)slot, at);  // slots are int32
         r.page = s / page;
         r.a = (int)(s % page);
-        int len = 0;
-        for (int i0 = 0; i0 < page - r.a; i0 += 64) {
-            const int i = i0 + lane;
-            const bool on = i < page - r.a && r.t + i < w.T && w.slots[r.t + i] == s + i;
-            const uint64_t off = ~__ballot(on);
-            if (off) {
-                len = i0 + __ffsll((unsigned long long)off) - 1;
-                break;
+        const uint64_t stop = at == 63 ? 0 : ~joined >> (at + 1);
+        int len = stop ? __ffsll((unsigned long long)stop) : 64 - at;
+        if (at + len == 64)  // the run may go on behind these tokens
+            for (int i0 = len; i0 < page - r.a; i0 += 64) {
+                const int i = i0 + lane;
+                const bool more = i < page - r.a && r.t + i < w.T && w.slots[r.t + i] == s + i;
+                const uint64_t off = ~__ballot(more);
+                len += off ? __ffsll((unsigned long long)off) - 1 : 64;
+                if (off) break;
             }
-            len = i0 + 64;
-        }
         r.b = r.a + len;
         // All waves see the same runs in the same order, so they take the same
-        // branches here and meet at the same barriers; two sets of lds, taken in
-        // turn, keep a barrier between two uses of one.
+        // branches here and meet at the same barriers, one for each long run; two
+        // sets of lds, taken in turn by long runs, keep a barrier between two uses
+        // of one.
         if (len <= kShort) {
-            if (turn % kWaves != wave) continue;
+            if (shorts++ % kWaves != wave) continue;
             if (values) write_values_short<T, DV>(w, r, h, lane);
             else write_keys<T, DK, 1, (kShort * DK / 8 + 63) / 64>(w, r, h, lane, nullptr);
         } else {
-            if (values) write_values<T, DV, kWaves, (PG * DV / 32 + kWaves - 1) / kWaves>(w, r, h, threadIdx.x, lds[turn & 1]);
-            else write_keys<T, DK, kWaves, PG * DK / 8 / kWaves>(w, r, h, threadIdx.x, lds[turn & 1]);
+            float* const l = lds[longs++ & 1];
+            if (values) write_values<T, DV, kWaves, (PG * DV / 32 + kWaves - 1) / kWaves>(w, r, h, threadIdx.x, l);
+            else write_keys<T, DK, kWaves, PG * DK / 8 / kWaves>(w, r, h, threadIdx.x, l);
         }
     }
 }
@@ -351,7 +357,7 @@ hipError_t launch_cache_write(const CacheWriteLaunch& p, hipStream_t s) {
                p.page_size == 64 ? 6 : p.page_size == 128 ? 7 : 8, p.H_kv, kWaves};
     // Tokens of a tile: one for each wave while the grid is small, at most a wave's lanes.
     while (w.tile < 64 && (p.T_total + w.tile - 1) / w.tile * 2 * p.H_kv > 16384) w.tile *= 2;
-    const dim3 grid((unsigned)((p.T_total + w.tile - 1) / w.tile), (unsigned)(2 * p.H_kv));
+    const dim3 grid((unsigned)((p.T_total + w.tile - 1) / w.tile * 2 * p.H_kv));
     if (p.bf16) run<bf16>(w, p.dk, p.dv, grid, s);
     else run<float>(w, p.dk, p.dv, grid, s);
     return hipGetLastError();

@@ -128,8 +128,8 @@ __global__ __launch_bounds__(DV / kCols * 64, MANY ? 2 : 4) void pool_kernel(Poo
                 kk += k[j] * k[j];
                 qq += q[j] * q[j];
             }
-            ck = 1.f / sqrtf(rows_sum(kk) + a.eps);
-            cq *= 1.f / sqrtf(rows_sum(qq) + a.eps);
+            ck = __builtin_amdgcn_rsqf(rows_sum(kk) + a.eps);  // good to one step of fp32
+            cq *= __builtin_amdgcn_rsqf(rows_sum(qq) + a.eps);
         }
         const floatx4 u = x.beta * (v - ck * r);
         const floatx4 out = cq * (p + (ck * kq) * u);
