@@ -19,6 +19,10 @@
 // other operand, V^T, is 16 tokens of one channel: one 16-byte load of the cache
 // as it is stored.  Codes are converted to bf16 exactly, and a page's scale, a
 // power of two, is applied exactly, to the scores and p or in the conversion.
+#include <algorithm>
+#include <cmath>
+#include <limits>
+
 #include "gdn_e4m3.h"
 #include "gdn_lanes.h"
 #include "gdn_mfma.h"
@@ -42,7 +46,8 @@ struct Attention {
     int32_t num_seqs;
     int64_t T;
     int32_t num_pages, page_log2, num_rows, max_blocks;
-    float scale2;  // scale * log2(e): scores in units of log 2
+    float scale2;   // |scale| * log2(e), above 0: scores in units of log 2
+    bool negative;  // the scale is: q is negated
     void* o;
     int32_t H, Hkv, G;
     // Requests of few rows (at most few_rows) and the others: at most so many
@@ -268,7 +273,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_rows_kernel(Attentio
         const bool there = page >= 0;
         float s[16];
         if (there) {
-            const float c2 = ks * a.scale2;
+            const float c2 = a.negative ? -ks * a.scale2 : ks * a.scale2;
 #pragma unroll
             for (int j = 0; j < PR; ++j) {
                 const int row = (64 * j + lane) / PR, c = lane % PR;
@@ -536,7 +541,12 @@ __global__ __launch_bounds__(64 * kWaves, sizeof(TI) == 4 ? 1 : 2) void attentio
     for (int m = 0; m < KS; ++m) q8[m].load(static_cast<const TI*>(a.q) + orow * DK + 16 * m + 8 * hf);
     bf16x8 qf[KS][NS];
 #pragma unroll
-    for (int m = 0; m < KS; ++m) q8[m].split(qf[m]);
+    for (int m = 0; m < KS; ++m) {
+        q8[m].split(qf[m]);
+        if (a.negative)
+#pragma unroll
+            for (int p = 0; p < NS; ++p) qf[m][p] = -qf[m][p];
+    }
 
     floatx16 O[DT];
 #pragma unroll
@@ -550,29 +560,30 @@ __global__ __launch_bounds__(64 * kWaves, sizeof(TI) == 4 ? 1 : 2) void attentio
     int buf = 0;
     for (int64_t base = from; base < to; base += kTile, buf ^= 1) {
         if (s_there[buf] && base < wave_to) {
-            float s[32];
+            // Scores before the factor scale2 (the sign of the scale is in q).
+            floatx16 x[2] = {floatx16{}, floatx16{}};
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                floatx16 x = floatx16{};
+            for (int m = 0; m < KS; ++m)
 #pragma unroll
-                for (int m = 0; m < KS; ++m) {
+                for (int half = 0; half < 2; ++half) {
                     const bf16x8 k8 = __builtin_bit_cast(bf16x8, s_k[buf][half * KS + m][lane ^ (m & 7)]);
 #pragma unroll
-                    for (int p = NS - 1; p >= 0; --p) x = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k8, qf[m][p], x, 0, 0, 0);
+                    for (int p = NS - 1; p >= 0; --p)
+                        x[half] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k8, qf[m][p], x[half], 0, 0, 0);
                 }
+            // The lane's tokens that its row sees: those up to `see` of the first
+            // half-tile's 16, up to see - 32 of the second's.
+            const int64_t see_ = sees - (base + 16 * hf);
+            const int see = see_ < -1 ? -1 : see_ > 64 ? 64 : (int)see_;
+            if (base + kTile - 1 > wave_all) {  // some row does not see all of the tile
+                asm volatile("");  // a branch: most tiles are seen whole
 #pragma unroll
-                for (int j = 0; j < 16; ++j) s[16 * half + j] = x[j] * a.scale2;
+                for (int j = 0; j < 32; ++j) x[j >> 4][j & 15] = (j & 15) + 32 * (j >> 4) <= see ? x[j >> 4][j & 15] : -kInf;
             }
-            const bool edge = base + kTile - 1 > wave_all;
-            const int64_t see = sees - (base + 16 * hf);  // of the first half-tile's tokens; the second's are 32 further
-            if (edge) {
+            float top = x[0][0];
 #pragma unroll
-                for (int j = 0; j < 32; ++j) s[j] = (j & 15) + 32 * (j >> 4) <= see ? s[j] : -kInf;
-            }
-            float top = s[0];
-#pragma unroll
-            for (int j = 1; j < 32; ++j) top = fmaxf(top, s[j]);
-            top = across<Max, 32>(top);
+            for (int j = 1; j < 32; ++j) top = fmaxf(top, x[j >> 4][j & 15]);
+            top = across<Max, 32>(top) * a.scale2;
             mx = fmaxf(mx, top);
             if (__ballot(mx > ref + kSlack || (ref == 0.f && sum == 0.f))) {
                 const float now = mx == -kInf ? 0.f : mx;
@@ -585,12 +596,21 @@ __global__ __launch_bounds__(64 * kWaves, sizeof(TI) == 4 ? 1 : 2) void attentio
             bf16x8 pf[NS][4];
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
-                const float p = __builtin_amdgcn_exp2f(s[j] - ref);
-                sum += p;
+                const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(x[j >> 4][j & 15], a.scale2, -ref));
+                if constexpr (NS > 1) sum += p;
                 bf16 part[NS];
                 split_bf16<NS>(p, part);
 #pragma unroll
                 for (int q = 0; q < NS; ++q) pf[q][j >> 3][j & 7] = part[q];
+            }
+            if constexpr (NS == 1) {
+                // the sum of p as it is rounded for the product, two at a time
+                const bf16x2 one = {(bf16)1.f, (bf16)1.f};
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                    for (int j = 0; j < 8; j += 2)
+                        sum = __builtin_amdgcn_fdot2_f32_bf16(bf16x2{pf[0][k][j], pf[0][k][j + 1]}, one, sum, false);
             }
             if (s_nan[buf]) {
                 // Some value of the tile is NaN (staged as 0): read the codes again
@@ -833,7 +853,10 @@ hipError_t launch_cache_attention(const CacheAttentionLaunch& p, hipStream_t s) 
     a.num_seqs = p.num_seqs; a.T = p.T_total; a.num_pages = (int32_t)p.num_pages;
     a.page_log2 = p.page_size == 64 ? 6 : p.page_size == 128 ? 7 : 8;
     a.num_rows = p.num_rows; a.max_blocks = p.max_blocks;
-    a.scale2 = p.scale * kLog2e; a.o = p.o; a.H = p.H; a.Hkv = p.H_kv; a.G = p.H / p.H_kv;
+    // Scale 0 stands for the smallest factor: scores of masked tokens stay -Inf.
+    a.scale2 = std::max(std::fabs(p.scale) * kLog2e, std::numeric_limits<float>::min());
+    a.negative = p.scale < 0.f;
+    a.o = p.o; a.H = p.H; a.Hkv = p.H_kv; a.G = p.H / p.H_kv;
     a.few_rows = pl.few_rows;
     a.tiled = pl.many;
     for (int c = 0; c < 2; ++c) {

@@ -21,6 +21,11 @@
 namespace gdn {
 namespace {
 
+#ifdef NTW
+#define LDW(p) __builtin_nontemporal_load(p)
+#else
+#define LDW(p) (*(p))
+#endif
 constexpr int kWaves = 4;
 constexpr int kShort = 4;  // a run of so many tokens is one wave's
 
@@ -54,7 +59,9 @@ struct Pair<bf16> {
     __device__ __forceinline__ float get(int i) const { return (float)x[i]; }
 };
 template <typename T>
-__device__ __forceinline__ Pair<T> load_pair(const T* p) { return *reinterpret_cast<const Pair<T>*>(p); }
+__device__ __forceinline__ Pair<T> load_pair(const T* p) {
+    return Pair<T>{LDW(reinterpret_cast<const decltype(Pair<T>::x)*>(p))};
+}
 // Eight of them.
 template <typename T>
 struct Eight {
@@ -64,11 +71,11 @@ template <typename T>
 __device__ __forceinline__ Eight<T> load_eight(const T* p) {
     Eight<T> e;
     if constexpr (sizeof(T) == 4) {
-        const floatx4 a = *reinterpret_cast<const floatx4*>(p), b = *reinterpret_cast<const floatx4*>(p + 4);
+        const floatx4 a = LDW(reinterpret_cast<const floatx4*>(p)), b = LDW(reinterpret_cast<const floatx4*>(p + 4));
 #pragma unroll
         for (int i = 0; i < 4; ++i) { e.x[i] = a[i]; e.x[i + 4] = b[i]; }
     } else {
-        const bf16x8 a = *reinterpret_cast<const bf16x8*>(p);
+        const bf16x8 a = LDW(reinterpret_cast<const bf16x8*>(p));
 #pragma unroll
         for (int i = 0; i < 8; ++i) e.x[i] = a[i];
     }
@@ -137,7 +144,7 @@ __device__ void write_keys(const Write& w, const Run& r, int h, int thread, floa
     if (r.a > 0 && s.factor == 1.f) return;
     if (r.a == 0 && r.b == page) return;
     // the page's other places: cleared, or at the larger scale
-#pragma unroll 4
+#pragma unroll 8
     for (int i = i0; i < page; i += STEP) {
         if (i >= r.a && i < r.b) continue;
         uintx2* at = reinterpret_cast<uintx2*>(to + (int64_t)i * D);
@@ -256,7 +263,7 @@ __device__ void write_values_short(const Write& w, const Run& r, int h, int lane
         }
         return;
     }
-#pragma unroll 2
+#pragma unroll 4
     for (int p0 = 0; p0 < page; p0 += 16)
 #pragma unroll
         for (int c = 0; c < C; ++c) {
