@@ -430,14 +430,20 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_rows_kernel(Attentio
 // One workgroup: 32 rows for each of its waves.  The waves read the same keys
 // and values, so a tile's codes are converted once, by all of them, and staged
 // in LDS as bf16 in the order in which the matrix core takes them: a fragment is
-// 64 lanes x 16 bytes, read without conflicts.  Two tiles are held: while one is
-// worked on, the next is written and the one after it is on its way to
-// registers, with one barrier per tile.
+// 64 lanes x 16 bytes, read without conflicts.
 //
 // 32x32x16 products (lane l: c = l % 32, hf = l / 32; a result has rows
 // 8 q + 4 hf + i, q and i 0..3): row 8 q + 4 hf + i of K's half-tile is token
 // 16 hf + 4 q + i, so that a lane's 16 scores of a half-tile are those of tokens
 // 16 hf .. 16 hf + 15.
+//
+// A tile costs a wave about as long on the matrix core as on the vector units,
+// so both have to be busy at once, and a SIMD's two waves do not arrange that by
+// themselves: they drift into waiting for the same unit.  So a wave's products
+// run beside vector work that does not need them, in two blocks per tile: the
+// next tile's scores beside this tile's exponentials, and this tile's output
+// beside the next tile's maximum and the staging.  Of keys and of values two
+// tiles are held; keys are one tile ahead.
 //
 // Rescaling the output for a new maximum is put off while the maximum has grown
 // by at most 2^8: p stays below 2^8, its sum is in fp32, and its rounding to
@@ -447,20 +453,22 @@ __global__ __launch_bounds__(64 * kWaves, sizeof(TI) == 4 ? 1 : 2) void attentio
     constexpr int NS = sizeof(TI) == 4 ? 3 : 1;
     constexpr int BR = 32 * kWaves, KS = DK / 16, DT = DV / 32;
     constexpr float kSlack = 8.f;
-    __shared__ uintx4 s_k[2][2 * KS][64];      // [buffer][half-tile * KS + step][lane ^ step % 8]
-    __shared__ uintx4 s_v[2][2 * 2 * DT][64];  // [buffer][(half-tile * 2 + step) * DT + channels][lane]
-    __shared__ int32_t s_nan[2], s_there[2];
+    // A fragment's place is longer than the fragment: a wave writes pieces of the
+    // same lanes of several fragments at once, which so fall into different banks.
+    __shared__ uintx4 s_k[2][2 * KS][65];      // [tile % 2][half-tile * KS + step][lane]
+    __shared__ uintx4 s_v[2][2 * 2 * DT][64];  // [tile % 2][(half-tile * 2 + step) * DT + channels][lane]
+    __shared__ int32_t s_nan[2][kWaves];       // a wave's part of the tile's values had a NaN code
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), c = lane & 31, hf = lane >> 5;
     // Key/value heads are neighbours in the grid: workgroups go to the eight XCDs in
     // turn, so with eight heads the tiles of a head share one XCD's cache.  The
     // last rows, which see most, come first.
     const int h = blockIdx.x % a.Hkv;
     const int64_t id = blockIdx.x / a.Hkv, tiles = gridDim.x / a.Hkv;
-    const int64_t tile = tiles - 1 - id;
-    const int32_t n = request_of(a, tile, BR);
+    const int64_t rtile = tiles - 1 - id;
+    const int32_t n = request_of(a, rtile, BR);
     if (n < 0) return;
     const Request job(a, n);
-    const int64_t row0_ = (tile - first_tile(a, n, BR)) * BR;
+    const int64_t row0_ = (rtile - first_tile(a, n, BR)) * BR;
     if (job.few || row0_ < 0 || row0_ >= job.rows) return;
     const int32_t row0 = (int32_t)row0_, last_row = (row0 + BR < job.rows ? row0 + BR : job.rows) - 1;
     const int64_t from = blockIdx.y * job.chunk;
@@ -468,77 +476,98 @@ __global__ __launch_bounds__(64 * kWaves, sizeof(TI) == 4 ? 1 : 2) void attentio
     const int32_t* const table = table_of(a, n);
     int64_t to = job.kv - job.len + last_row / a.G + 1;  // no row of the tile sees more
     to = !table ? from : to < from + job.chunk ? to : from + job.chunk;
-    const int64_t all_see = job.kv - job.len + row0 / a.G;  // every row of the tile sees up to here
+    const int64_t all_see = job.kv - job.len + row0 / a.G;  // every row of the workgroup sees up to here
+    const int32_t count = to > from ? (int32_t)((to - from + kTile - 1) / kTile) : 0;  // tiles
     const int page_mask = (1 << a.page_log2) - 1;
+
+    // this lane's row; lanes behind the last one work on the first, unseen
+    const int32_t row = row0 + 32 * wave + c;
+    const bool live = row < job.rows;
+    const int32_t i = live ? row / a.G : 0, head = h * a.G + (live ? row - i * a.G : 0);
+    const int64_t orow = (job.t0 + i) * a.H + head;
+    const int64_t sees = live ? job.kv - job.len + i - from : -1;  // the last token of the part that the row sees
+    // Of this wave: no row sees tiles from wave_tiles on, every row sees the first wave_all.
+    const int32_t wrow = row0 + 32 * wave, wlast = wrow + 31 < job.rows ? wrow + 31 : job.rows - 1;
+    auto tiles_below = [&](int64_t tokens, int64_t up) {  // whole tiles, or tiles begun, of the part's first tokens
+        const int64_t t = tokens <= 0 ? 0 : (tokens + up) / kTile;
+        return (int32_t)(t < count ? t : count);
+    };
+    const int32_t wave_tiles = wrow < job.rows ? tiles_below(job.kv - job.len + wlast / a.G + 1 - from, kTile - 1) : 0;
+    const int32_t wave_all = wrow < job.rows ? tiles_below(job.kv - job.len + wrow / a.G + 1 - from, 0) : 0;
+    const int32_t group_all = tiles_below(all_see + 1 - from, 0);  // every row of the workgroup sees these tiles whole
+    Eight<TI> q8[KS];
+#pragma unroll
+    for (int m = 0; m < KS; ++m) q8[m].load(static_cast<const TI*>(a.q) + orow * DK + 16 * m + 8 * hf);
 
     // Staging: a thread takes 16-byte pieces of keys (a token's 16 channels) and
     // of values (a channel's 16 tokens).
     constexpr int NT = 64 * kWaves, KP = kTile * DK / 16 / NT, VP = kTile * DV / 16 / NT;
     uintx4 kr[KP], vr[VP];
-    float ks = 0.f, vs = 0.f;
-    int32_t page = -1;  // of the tile in kr and vr
     Pages pages;
-    int at = 0;  // the next tile's lane of `pages`
-    auto load = [&](int64_t base) {
-        if (at == 64) at = 0;
-        if (at == 0) pages.fetch(a, table, h, base, to, kTile);
-        page = __builtin_amdgcn_readlane(pages.page, at);
-        ks = Pages::lane_of(pages.ks, at);
-        vs = Pages::lane_of(pages.vs, at);
-        ++at;
-        const int64_t ph = (int64_t)(page < 0 ? 0 : page) * a.Hkv + h, place = (ph << a.page_log2) + (base & page_mask);
-        const uintx4* k = reinterpret_cast<const uintx4*>(a.kc + place * DK) + threadIdx.x;
-        const uintx4* v = reinterpret_cast<const uintx4*>(a.vc + place * DV) + threadIdx.x;
+    int32_t window = 0;  // the tile of lane 0 of `pages`; tiles from `count` on have no page
+    auto there = [&](int32_t tile) { return tile < count && __builtin_amdgcn_readlane(pages.page, tile - window) >= 0; };
+    // The loads have no branch: one would make the wait for the loads before it a
+    // wait for these too.  Where there is no tile they read page 0.
+    auto place_of = [&](int32_t tile) {
+        const int32_t p = __builtin_amdgcn_readlane(pages.page, tile - window);
+        return ((((int64_t)(p < 0 ? 0 : p) * a.Hkv + h) << a.page_log2) + ((from + (int64_t)tile * kTile) & page_mask));
+    };
+    auto load_keys = [&](int32_t tile) {
+        const uintx4* k = reinterpret_cast<const uintx4*>(a.kc + place_of(tile) * DK) + threadIdx.x;
 #pragma unroll
         for (int j = 0; j < KP; ++j) kr[j] = k[j * NT];
+    };
+    auto load_values = [&](int32_t tile) {
+        const uintx4* v = reinterpret_cast<const uintx4*>(a.vc + place_of(tile) * DV) + threadIdx.x;
 #pragma unroll
         for (int j = 0; j < VP; ++j) vr[j] = v[j * NT];
     };
-    auto stage = [&](int64_t base, int buf) {
-        if (threadIdx.x == 0) s_there[buf] = page >= 0;
-        if (page < 0) return;
+    // (Tiles without a page are staged all the same, from what the loads read.)
+    // A thread's pieces: of one half-tile each, or of one tile.
+    static_assert((KP == 2 && KS == 8) || (KP == 1 && KS == 4), "pieces of keys");
+    static_assert((VP == 2 && DV == 128) || (VP == 1 && DV == 64), "pieces of values");
+    const int ktoken = threadIdx.x / KS, kstep = threadIdx.x % KS;
+    uintx4* const kto = &s_k[0][(KP == 1 ? ktoken >> 5 : 0) * KS + kstep][8 * ((ktoken >> 2) & 3) + 4 * ((ktoken >> 4) & 1) + (ktoken & 3)];
+    const int vgroup = threadIdx.x / DV, vd = threadIdx.x % DV;
+    uintx4* const vto = &s_v[0][(VP == 1 ? vgroup >> 1 : 0) * 2 * DT + vd / 32][32 * (vgroup & 1) + (vd & 31)];
+    auto stage_keys = [&](int32_t tile, int buf) {
+        const float ks = Pages::lane_of(pages.ks, tile - window);
 #pragma unroll
         for (int j = 0; j < KP; ++j) {
-            const int piece = threadIdx.x + j * NT, token = piece / KS, step = piece % KS;
-            const int t = token & 31, row = 8 * ((t >> 2) & 3) + 4 * (t >> 4) + (t & 3);
-            uintx4* to = s_k[buf][(token >> 5) * KS + step];
-            to[row ^ (step & 7)] = __builtin_bit_cast(uintx4, e4m3_to_bf16x8(kr[j][0], kr[j][1], ks));
-            to[(row + 32) ^ (step & 7)] = __builtin_bit_cast(uintx4, e4m3_to_bf16x8(kr[j][2], kr[j][3], ks));
+            uintx4* const to_ = kto + (buf * 2 * KS + j * KS) * 65;
+            to_[0] = __builtin_bit_cast(uintx4, e4m3_to_bf16x8(kr[j][0], kr[j][1], ks));
+            to_[32] = __builtin_bit_cast(uintx4, e4m3_to_bf16x8(kr[j][2], kr[j][3], ks));
         }
-        const bool edge = base + kTile - 1 > all_see;
+    };
+    // Codes behind the last token, and NaN codes, as in the rows kernel.
+    auto clean_values = [&](int32_t tile, int buf) {
+        const int64_t base = from + (int64_t)tile * kTile;
         bool nan = false;
 #pragma unroll
         for (int j = 0; j < VP; ++j) {
-            const int piece = threadIdx.x + j * NT, group = piece / DV, d = piece % DV;
-            if (edge) {
-                // as in the rows kernel: codes behind the last token, and NaN codes
-                uintx4 ones;
-                keep_codes(vr[j], job.kv - (base + 16 * group));
-                nan |= has_nan_code(vr[j]);
-                split_nan(vr[j], ones);
-            }
-            const int half = group >> 1, at = 32 * (group & 1) + (d & 31);
-            s_v[buf][(half * 2 + 0) * DT + d / 32][at] = __builtin_bit_cast(uintx4, e4m3_to_bf16x8(vr[j][0], vr[j][1], vs));
-            s_v[buf][(half * 2 + 1) * DT + d / 32][at] = __builtin_bit_cast(uintx4, e4m3_to_bf16x8(vr[j][2], vr[j][3], vs));
+            uintx4 ones;
+            keep_codes(vr[j], job.kv - (base + 16 * ((int)(threadIdx.x + j * NT) / DV)));
+            nan |= has_nan_code(vr[j]);
+            split_nan(vr[j], ones);
         }
-        if (nan) s_nan[buf] = 1;
+        const bool any = __ballot(nan) != 0;
+        if (lane == 0) s_nan[buf][wave] = any;
+    };
+    auto stage_values = [&](int32_t tile, int buf) {
+        const float vs = Pages::lane_of(pages.vs, tile - window);
+#pragma unroll
+        for (int j = 0; j < VP; ++j) {
+            uintx4* const to_ = vto + (buf * 4 * DT + j * 2 * DT) * 64;
+            to_[0] = __builtin_bit_cast(uintx4, e4m3_to_bf16x8(vr[j][0], vr[j][1], vs));
+            to_[DT * 64] = __builtin_bit_cast(uintx4, e4m3_to_bf16x8(vr[j][2], vr[j][3], vs));
+        }
     };
 
-    if (from < to) load(from);
-
-    // this lane's row
-    const int32_t row = row0 + 32 * wave + c;
-    const bool live = row < job.rows;
-    const int32_t i = live ? row / a.G : 0, head = h * a.G + (live ? row - i * a.G : 0);
-    const int64_t sees = live ? job.kv - job.len + i : -1;  // the last token that the row sees
-    const int64_t orow = (job.t0 + i) * a.H + head;
-    // Of this wave: no row sees tokens from wave_to on, every row sees those up to wave_all.
-    const int32_t wrow = row0 + 32 * wave, wlast = wrow + 31 < job.rows ? wrow + 31 : job.rows - 1;
-    const int64_t wave_to = wrow < job.rows ? job.kv - job.len + wlast / a.G + 1 : 0;
-    const int64_t wave_all = job.kv - job.len + (wrow < job.rows ? wrow : 0) / a.G;
-    Eight<TI> q8[KS];
-#pragma unroll
-    for (int m = 0; m < KS; ++m) q8[m].load(static_cast<const TI*>(a.q) + orow * DK + 16 * m + 8 * hf);
+    if (count > 0) {
+        pages.fetch(a, table, h, from, to, kTile);
+        load_keys(0);
+        load_values(0);
+    }
     bf16x8 qf[KS][NS];
 #pragma unroll
     for (int m = 0; m < KS; ++m) {
@@ -547,115 +576,229 @@ __global__ __launch_bounds__(64 * kWaves, sizeof(TI) == 4 ? 1 : 2) void attentio
 #pragma unroll
             for (int p = 0; p < NS; ++p) qf[m][p] = -qf[m][p];
     }
+    if (count > 0) {
+        stage_keys(0, 0);
+        load_keys(1);
+        if (0 >= group_all) clean_values(0, 0);
+        stage_values(0, 0);
+        load_values(1);
+        stage_keys(1, 1);
+        load_keys(2);
+    }
+    __syncthreads();
 
-    floatx16 O[DT];
+    floatx16 O[DT], x[2], y[2];  // x and y: scores of a tile, before the factor scale2 (the sign of the scale is in q)
 #pragma unroll
     for (int d = 0; d < DT; ++d) O[d] = floatx16{};
     float mx = -kInf, ref = 0.f, sum = 0.f;  // ref: the maximum that O and sum are scaled by
-    if (threadIdx.x < 2) s_nan[threadIdx.x] = 0;
-    __syncthreads();
-    stage(from, 0);
-    if (from < to) load(from + kTile);
-    __syncthreads();
-    int buf = 0;
-    for (int64_t base = from; base < to; base += kTile, buf ^= 1) {
-        if (s_there[buf] && base < wave_to) {
-            // Scores before the factor scale2 (the sign of the scale is in q).
-            floatx16 x[2] = {floatx16{}, floatx16{}};
+    bf16x8 pf[NS][4];
+    auto scores = [&](int buf, floatx16* z) {
+        z[0] = z[1] = floatx16{};
 #pragma unroll
-            for (int m = 0; m < KS; ++m)
+        for (int m = 0; m < KS; ++m)
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const bf16x8 k8 = __builtin_bit_cast(bf16x8, s_k[buf][half * KS + m][lane ^ (m & 7)]);
+            for (int half = 0; half < 2; ++half) {
+                const bf16x8 k8 = __builtin_bit_cast(bf16x8, s_k[buf][half * KS + m][lane]);
 #pragma unroll
-                    for (int p = NS - 1; p >= 0; --p)
-                        x[half] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k8, qf[m][p], x[half], 0, 0, 0);
-                }
-            // The lane's tokens that its row sees: those up to `see` of the first
-            // half-tile's 16, up to see - 32 of the second's.
-            const int64_t see_ = sees - (base + 16 * hf);
-            const int see = see_ < -1 ? -1 : see_ > 64 ? 64 : (int)see_;
-            if (base + kTile - 1 > wave_all) {  // some row does not see all of the tile
-                asm volatile("");  // a branch: most tiles are seen whole
-#pragma unroll
-                for (int j = 0; j < 32; ++j) x[j >> 4][j & 15] = (j & 15) + 32 * (j >> 4) <= see ? x[j >> 4][j & 15] : -kInf;
+                for (int p = NS - 1; p >= 0; --p)
+                    z[half] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k8, qf[m][p], z[half], 0, 0, 0);
             }
-            float top = x[0][0];
+    };
+    // The lane's tokens that its row sees: those up to this of the first
+    // half-tile's 16, up to this - 32 of the second's.
+    auto see_of = [&](int32_t tile) {
+        const int64_t see = sees - ((int64_t)tile * kTile + 16 * hf);
+        return see < -1 ? -1 : see > 64 ? 64 : (int)see;
+    };
+    auto mask = [&](int32_t tile, floatx16* z) {
+        const int see = see_of(tile);
 #pragma unroll
-            for (int j = 1; j < 32; ++j) top = fmaxf(top, x[j >> 4][j & 15]);
-            top = across<Max, 32>(top) * a.scale2;
-            mx = fmaxf(mx, top);
-            if (__ballot(mx > ref + kSlack || (ref == 0.f && sum == 0.f))) {
-                const float now = mx == -kInf ? 0.f : mx;
-                const float fade = sum == 0.f ? 1.f : __builtin_amdgcn_exp2f(ref - now);
-                ref = now;
-                sum *= fade;
+        for (int j = 0; j < 32; ++j) z[j >> 4][j & 15] = (j & 15) + 32 * (j >> 4) <= see ? z[j >> 4][j & 15] : -kInf;
+    };
+    auto maximum = [&](const floatx16* z) {
+        float top = z[0][0];
 #pragma unroll
-                for (int d = 0; d < DT; ++d) O[d] *= fade;
-            }
-            bf16x8 pf[NS][4];
+        for (int j = 1; j < 32; ++j) top = fmaxf(top, z[j >> 4][j & 15]);
+        mx = fmaxf(mx, across<Max, 32>(top) * a.scale2);
+    };
+    auto rescale = [&]() {
+        if (__ballot(mx > ref + kSlack || (ref == 0.f && sum == 0.f))) {
+            const float now = mx == -kInf ? 0.f : mx;
+            const float fade = sum == 0.f ? 1.f : __builtin_amdgcn_exp2f(ref - now);
+            ref = now;
+            sum *= fade;
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-                const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(x[j >> 4][j & 15], a.scale2, -ref));
-                if constexpr (NS > 1) sum += p;
-                bf16 part[NS];
-                split_bf16<NS>(p, part);
+            for (int d = 0; d < DT; ++d) O[d] *= fade;
+        }
+    };
+    auto exponentials = [&](const floatx16* z) {
 #pragma unroll
-                for (int q = 0; q < NS; ++q) pf[q][j >> 3][j & 7] = part[q];
-            }
-            if constexpr (NS == 1) {
-                // the sum of p as it is rounded for the product, two at a time
-                const bf16x2 one = {(bf16)1.f, (bf16)1.f};
+        for (int j = 0; j < 32; ++j) {
+            const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(z[j >> 4][j & 15], a.scale2, -ref));
+            if constexpr (NS > 1) sum += p;
+            bf16 part[NS];
+            split_bf16<NS>(p, part);
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-#pragma unroll
-                    for (int j = 0; j < 8; j += 2)
-                        sum = __builtin_amdgcn_fdot2_f32_bf16(bf16x2{pf[0][k][j], pf[0][k][j + 1]}, one, sum, false);
-            }
-            if (s_nan[buf]) {
-                // Some value of the tile is NaN (staged as 0): read the codes again
-                // and mark the outputs of the rows that see one.
-                const int32_t pg = table[base >> a.page_log2];
-                const int64_t place = (((int64_t)pg * a.Hkv + h) << a.page_log2) + (base & page_mask);
-#pragma unroll 1
-                for (int half = 0; half < 2; ++half) {
-                    bf16x8 see8[2];
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) see8[j >> 3][j & 7] = (bf16)(j + 32 * half <= see ? 1.f : 0.f);
-#pragma unroll
-                    for (int d = 0; d < DT; ++d) {
-                        const int group = 2 * half + hf;
-                        uintx4 code = *reinterpret_cast<const uintx4*>(a.vc + place * DV + ((int64_t)group * DV + 32 * d + c) * 16), ones;
-                        keep_codes(code, job.kv - (base + 16 * group));
-                        split_nan(code, ones);
-                        floatx16 hits = floatx16{};
-                        hits = __builtin_amdgcn_mfma_f32_32x32x16_bf16(e4m3_to_bf16x8(ones[0], ones[1]), see8[0], hits, 0, 0, 0);
-                        hits = __builtin_amdgcn_mfma_f32_32x32x16_bf16(e4m3_to_bf16x8(ones[2], ones[3]), see8[1], hits, 0, 0, 0);
-#pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            if (hits[j] > 0.f) O[d][j] = __builtin_nanf("");
-                    }
-                }
-            }
+            for (int q = 0; q < NS; ++q) pf[q][j >> 3][j & 7] = part[q];
+        }
+        if constexpr (NS == 1) {
+            const bf16x2 one = {(bf16)1.f, (bf16)1.f};
 #pragma unroll
             for (int k = 0; k < 4; ++k)
 #pragma unroll
-                for (int d = 0; d < DT; ++d) {
-                    const bf16x8 v8 = __builtin_bit_cast(bf16x8, s_v[buf][k * DT + d][lane]);
+                for (int j = 0; j < 8; j += 2)
+                    sum = __builtin_amdgcn_fdot2_f32_bf16(bf16x2{pf[0][k][j], pf[0][k][j + 1]}, one, sum, false);
+        }
+    };
+    auto output = [&](int buf) {
 #pragma unroll
-                    for (int p = NS - 1; p >= 0; --p) O[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v8, pf[p][k], O[d], 0, 0, 0);
-                }
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int d = 0; d < DT; ++d) {
+                const bf16x8 v8 = __builtin_bit_cast(bf16x8, s_v[buf][k * DT + d][lane]);
+#pragma unroll
+                for (int p = NS - 1; p >= 0; --p) O[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v8, pf[p][k], O[d], 0, 0, 0);
+            }
+    };
+    // Some value of a tile may be NaN (staged as 0): reads the codes again and
+    // marks the outputs of the rows that see one.
+    auto mark_nan = [&](int32_t tile, int buf) {
+        int32_t nan = 0;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) nan |= s_nan[buf][w];
+        if (!__builtin_amdgcn_readfirstlane(nan)) return;
+        const int64_t place = place_of(tile);
+        const int see = see_of(tile);
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+            bf16x8 see8[2];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) see8[j >> 3][j & 7] = (bf16)(j + 32 * half <= see ? 1.f : 0.f);
+#pragma unroll
+            for (int d = 0; d < DT; ++d) {
+                const int group = 2 * half + hf;
+                uintx4 code = *reinterpret_cast<const uintx4*>(a.vc + place * DV + ((int64_t)group * DV + 32 * d + c) * 16), ones;
+                keep_codes(code, job.kv - (from + (int64_t)tile * kTile + 16 * group));
+                split_nan(code, ones);
+                floatx16 hits = floatx16{};
+                hits = __builtin_amdgcn_mfma_f32_32x32x16_bf16(e4m3_to_bf16x8(ones[0], ones[1]), see8[0], hits, 0, 0, 0);
+                hits = __builtin_amdgcn_mfma_f32_32x32x16_bf16(e4m3_to_bf16x8(ones[2], ones[3]), see8[1], hits, 0, 0, 0);
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    if (hits[j] > 0.f) O[d][j] = __builtin_nanf("");
+            }
         }
-        if (base + kTile < to) {
-            // The other buffer's readers have met at the last barrier.
-            if (threadIdx.x == 0) s_nan[buf ^ 1] = 0;
-            const bool may_be_nan = base + 2 * kTile - 1 > all_see;
-            if (may_be_nan) __syncthreads();  // the flag is cleared before it is set
-            stage(base + kTile, buf ^ 1);
-            load(base + 2 * kTile);
-            __syncthreads();
+    };
+    auto fetch_pages = [&](int32_t tile) {
+        window = tile;
+        pages.fetch(a, table, h, from + (int64_t)window * kTile, to, kTile);
+    };
+    // One tile that every row sees whole, as it sees the one after it: `now` holds
+    // its scores, in the maximum already; `next` receives those of the tile after
+    // it.  buf: tile % 2.
+    auto step = [&](int32_t tile, int buf, const floatx16* now, floatx16* next) {
+        rescale();
+        // The order is the one written, so that what is read ahead fits the
+        // registers: a step's operands are read one step before their products.
+        next[0] = next[1] = floatx16{};
+        const auto key = [&](int m, int half) { return __builtin_bit_cast(bf16x8, s_k[buf ^ 1][half * KS + m][lane]); };
+        bf16x8 k0 = key(0, 0), k1 = key(0, 1);
+        const bf16x2 one = {(bf16)1.f, (bf16)1.f};
+#pragma unroll
+        for (int m = 0; m < KS; ++m) {
+            const bf16x8 u0 = k0, u1 = k1;
+            if (m + 1 < KS) {
+                k0 = key(m + 1, 0);
+                k1 = key(m + 1, 1);
+            }
+            next[0] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(u0, qf[m][0], next[0], 0, 0, 0);
+            next[1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(u1, qf[m][0], next[1], 0, 0, 0);
+#pragma unroll
+            for (int j = 32 / KS * m; j < 32 / KS * (m + 1); j += 2) {
+                const bf16x2 p = {(bf16)__builtin_amdgcn_exp2f(__builtin_fmaf(now[j >> 4][j & 15], a.scale2, -ref)),
+                                  (bf16)__builtin_amdgcn_exp2f(__builtin_fmaf(now[j >> 4][(j & 15) + 1], a.scale2, -ref))};
+                // the sum of p as it is rounded for the product, two at a time
+                sum = __builtin_amdgcn_fdot2_f32_bf16(p, one, sum, false);
+                pf[0][j >> 3][j & 7] = p[0];
+                pf[0][j >> 3][(j & 7) + 1] = p[1];
+            }
+            __builtin_amdgcn_sched_barrier(0);
         }
+        const auto value = [&](int k, int d) { return __builtin_bit_cast(bf16x8, s_v[buf][k * DT + d][lane]); };
+        bf16x8 v8[DT];
+#pragma unroll
+        for (int d = 0; d < DT; ++d) v8[d] = value(0, d);
+        float top = -kInf;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            bf16x8 u[DT];
+#pragma unroll
+            for (int d = 0; d < DT; ++d) {
+                u[d] = v8[d];
+                if (k < 3) v8[d] = value(k + 1, d);
+            }
+#pragma unroll
+            for (int d = 0; d < DT; ++d) O[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(u[d], pf[0][k], O[d], 0, 0, 0);
+#pragma unroll
+            for (int j = 8 * k; j < 8 * (k + 1); ++j) top = fmaxf(top, next[j >> 4][j & 15]);
+            if (k == 0) stage_values(tile + 1, buf ^ 1);
+            if (k == 1) load_values(tile + 2);
+            if (k == 2) stage_keys(tile + 2, buf);
+            if (k == 3) load_keys(tile + 3);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        mx = fmaxf(mx, across<Max, 32>(top) * a.scale2);
+        __syncthreads();
+    };
+    // Any tile; the scores change in x.
+    auto last_step = [&](int32_t tile, int buf) {
+        if (tile + 3 >= window + 64) fetch_pages(tile);
+        const bool mine = tile < wave_tiles && there(tile), more = tile + 1 < wave_tiles;
+        if (mine) {
+            rescale();
+            exponentials(x);
+        }
+        if (more) {
+            scores(buf ^ 1, x);
+            if (tile + 1 >= wave_all) mask(tile + 1, x);
+            if (there(tile + 1)) maximum(x);
+        }
+        if (mine) {
+            if (tile >= group_all) mark_nan(tile, buf);
+            output(buf);
+        }
+        if (tile + 1 < count) {
+            if (tile + 1 >= group_all) clean_values(tile + 1, buf ^ 1);
+            stage_values(tile + 1, buf ^ 1);
+            load_values(tile + 2);
+            stage_keys(tile + 2, buf);
+            load_keys(tile + 3);
+        }
+        __syncthreads();
+    };
+    if (wave_tiles > 0) {
+        scores(0, x);
+        if (0 >= wave_all) mask(0, x);
+        if (there(0)) maximum(x);
     }
+    // The first scores' keys may be overwritten in the first step.
+    __syncthreads();
+    int32_t tile = 0;
+    if constexpr (NS == 1)  // (three bf16 parts leave no room for two tiles' scores)
+        for (;;) {
+            if (tile >= window + 60) fetch_pages(tile);
+            // Pairs of steps, up to a tile without a page or the window's end.
+            const uint64_t gone = __ballot(pages.page < 0);
+            const int32_t present = window + (gone ? __ffsll((unsigned long long)gone) - 1 : 64);
+            int32_t stop = (present < group_all ? present : group_all) - 2;
+            stop = stop < window + 60 ? stop : window + 60;
+            if (tile >= stop) break;
+            for (; tile < stop; tile += 2) {
+                step(tile, 0, x, y);
+                step(tile + 1, 1, y, x);
+            }
+        }
+    for (; tile < count; ++tile) last_step(tile, tile & 1);
     sum = across<Sum, 32>(sum);
     if (!live) return;
     const bool alone = job.alone();
@@ -665,10 +808,10 @@ __global__ __launch_bounds__(64 * kWaves, sizeof(TI) == 4 ? 1 : 2) void attentio
     for (int d = 0; d < DT; ++d)
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            const floatx4 x = {O[d][4 * q] * inv, O[d][4 * q + 1] * inv, O[d][4 * q + 2] * inv, O[d][4 * q + 3] * inv};
+            const floatx4 z = {O[d][4 * q] * inv, O[d][4 * q + 1] * inv, O[d][4 * q + 2] * inv, O[d][4 * q + 3] * inv};
             const int ch = 32 * d + 8 * q + 4 * hf;
-            if (alone) store4(static_cast<TI*>(a.o) + orow * DV + ch, x);
-            else *reinterpret_cast<floatx4*>(a.ws_o[1] + prow * DV + ch) = x;
+            if (alone) store4(static_cast<TI*>(a.o) + orow * DV + ch, z);
+            else *reinterpret_cast<floatx4*>(a.ws_o[1] + prow * DV + ch) = z;
         }
     if (!alone && hf == 0) {
         a.ws_ml[1][2 * prow] = sum == 0.f ? -kInf : ref;
