@@ -631,23 +631,24 @@ __global__ __launch_bounds__(64 * kWaves, sizeof(TI) == 4 ? 1 : 2) void attentio
             for (int d = 0; d < DT; ++d) O[d] *= fade;
         }
     };
-    auto exponentials = [&](const floatx16* z) {
+    // p of the lane's scores j0 .. j1 - 1 (whole pairs)
+    auto exponentials = [&](const floatx16* z, int j0, int j1) {
+        const bf16x2 one = {(bf16)1.f, (bf16)1.f};
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-            const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(z[j >> 4][j & 15], a.scale2, -ref));
-            if constexpr (NS > 1) sum += p;
-            bf16 part[NS];
-            split_bf16<NS>(p, part);
+        for (int j = j0; j < j1; j += 2) {
+            const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(z[j >> 4][j & 15], a.scale2, -ref)),
+                        p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(z[j >> 4][(j & 15) + 1], a.scale2, -ref));
+            bf16 part0[NS], part1[NS];
+            split_bf16<NS>(p0, part0);
+            split_bf16<NS>(p1, part1);
+            // with one part, the sum is of p as it is rounded for the product
+            if constexpr (NS == 1) sum = __builtin_amdgcn_fdot2_f32_bf16(bf16x2{part0[0], part1[0]}, one, sum, false);
+            else sum += p0 + p1;
 #pragma unroll
-            for (int q = 0; q < NS; ++q) pf[q][j >> 3][j & 7] = part[q];
-        }
-        if constexpr (NS == 1) {
-            const bf16x2 one = {(bf16)1.f, (bf16)1.f};
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-#pragma unroll
-                for (int j = 0; j < 8; j += 2)
-                    sum = __builtin_amdgcn_fdot2_f32_bf16(bf16x2{pf[0][k][j], pf[0][k][j + 1]}, one, sum, false);
+            for (int q = 0; q < NS; ++q) {
+                pf[q][j >> 3][j & 7] = part0[q];
+                pf[q][j >> 3][(j & 7) + 1] = part1[q];
+            }
         }
     };
     auto output = [&](int buf) {
@@ -703,7 +704,6 @@ __global__ __launch_bounds__(64 * kWaves, sizeof(TI) == 4 ? 1 : 2) void attentio
         next[0] = next[1] = floatx16{};
         const auto key = [&](int m, int half) { return __builtin_bit_cast(bf16x8, s_k[buf ^ 1][half * KS + m][lane]); };
         bf16x8 k0 = key(0, 0), k1 = key(0, 1);
-        const bf16x2 one = {(bf16)1.f, (bf16)1.f};
 #pragma unroll
         for (int m = 0; m < KS; ++m) {
             const bf16x8 u0 = k0, u1 = k1;
@@ -711,19 +711,16 @@ __global__ __launch_bounds__(64 * kWaves, sizeof(TI) == 4 ? 1 : 2) void attentio
                 k0 = key(m + 1, 0);
                 k1 = key(m + 1, 1);
             }
-            next[0] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(u0, qf[m][0], next[0], 0, 0, 0);
-            next[1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(u1, qf[m][0], next[1], 0, 0, 0);
 #pragma unroll
-            for (int j = 32 / KS * m; j < 32 / KS * (m + 1); j += 2) {
-                const bf16x2 p = {(bf16)__builtin_amdgcn_exp2f(__builtin_fmaf(now[j >> 4][j & 15], a.scale2, -ref)),
-                                  (bf16)__builtin_amdgcn_exp2f(__builtin_fmaf(now[j >> 4][(j & 15) + 1], a.scale2, -ref))};
-                // the sum of p as it is rounded for the product, two at a time
-                sum = __builtin_amdgcn_fdot2_f32_bf16(p, one, sum, false);
-                pf[0][j >> 3][j & 7] = p[0];
-                pf[0][j >> 3][(j & 7) + 1] = p[1];
+            for (int p = NS - 1; p >= 0; --p) {
+                next[0] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(u0, qf[m][p], next[0], 0, 0, 0);
+                next[1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(u1, qf[m][p], next[1], 0, 0, 0);
             }
-            __builtin_amdgcn_sched_barrier(0);
+            exponentials(now, 32 / KS * m, 32 / KS * (m + 1));
+            // (With 128 channels of keys the compiler's own order is 2% faster.)
+            if (NS > 1 || KS < 8) __builtin_amdgcn_sched_barrier(0);
         }
+        __builtin_amdgcn_sched_barrier(0);
         const auto value = [&](int k, int d) { return __builtin_bit_cast(bf16x8, s_v[buf][k * DT + d][lane]); };
         bf16x8 v8[DT];
 #pragma unroll
@@ -738,7 +735,9 @@ __global__ __launch_bounds__(64 * kWaves, sizeof(TI) == 4 ? 1 : 2) void attentio
                 if (k < 3) v8[d] = value(k + 1, d);
             }
 #pragma unroll
-            for (int d = 0; d < DT; ++d) O[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(u[d], pf[0][k], O[d], 0, 0, 0);
+            for (int p = NS - 1; p >= 0; --p)
+#pragma unroll
+                for (int d = 0; d < DT; ++d) O[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(u[d], pf[p][k], O[d], 0, 0, 0);
 #pragma unroll
             for (int j = 8 * k; j < 8 * (k + 1); ++j) top = fmaxf(top, next[j >> 4][j & 15]);
             if (k == 0) stage_values(tile + 1, buf ^ 1);
@@ -756,7 +755,7 @@ __global__ __launch_bounds__(64 * kWaves, sizeof(TI) == 4 ? 1 : 2) void attentio
         const bool mine = tile < wave_tiles && there(tile), more = tile + 1 < wave_tiles;
         if (mine) {
             rescale();
-            exponentials(x);
+            exponentials(x, 0, 32);
         }
         if (more) {
             scores(buf ^ 1, x);
@@ -784,7 +783,7 @@ __global__ __launch_bounds__(64 * kWaves, sizeof(TI) == 4 ? 1 : 2) void attentio
     // The first scores' keys may be overwritten in the first step.
     __syncthreads();
     int32_t tile = 0;
-    if constexpr (NS == 1)  // (three bf16 parts leave no room for two tiles' scores)
+    if constexpr (NS == 1 || DK == 64 || DV == 64)  // (else three bf16 parts leave no room for two tiles' scores)
         for (;;) {
             if (tile >= window + 60) fetch_pages(tile);
             // Pairs of steps, up to a tile without a page or the window's end.
