@@ -783,20 +783,19 @@ __global__ __launch_bounds__(64 * kWaves, sizeof(TI) == 4 ? 1 : 2) void attentio
     // The first scores' keys may be overwritten in the first step.
     __syncthreads();
     int32_t tile = 0;
-    if constexpr (NS == 1 || DK == 64 || DV == 64)  // (else three bf16 parts leave no room for two tiles' scores)
-        for (;;) {
-            if (tile >= window + 60) fetch_pages(tile);
-            // Pairs of steps, up to a tile without a page or the window's end.
-            const uint64_t gone = __ballot(pages.page < 0);
-            const int32_t present = window + (gone ? __ffsll((unsigned long long)gone) - 1 : 64);
-            int32_t stop = (present < group_all ? present : group_all) - 2;
-            stop = stop < window + 60 ? stop : window + 60;
-            if (tile >= stop) break;
-            for (; tile < stop; tile += 2) {
-                step(tile, 0, x, y);
-                step(tile + 1, 1, y, x);
-            }
+    for (;;) {
+        if (tile >= window + 60) fetch_pages(tile);
+        // Pairs of steps, up to a tile without a page or the window's end.
+        const uint64_t gone = __ballot(pages.page < 0);
+        const int32_t present = window + (gone ? __ffsll((unsigned long long)gone) - 1 : 64);
+        int32_t stop = (present < group_all ? present : group_all) - 2;
+        stop = stop < window + 60 ? stop : window + 60;
+        if (tile >= stop) break;
+        for (; tile < stop; tile += 2) {
+            step(tile, 0, x, y);
+            step(tile + 1, 1, y, x);
         }
+    }
     for (; tile < count; ++tile) last_step(tile, tile & 1);
     sum = across<Sum, 32>(sum);
     if (!live) return;

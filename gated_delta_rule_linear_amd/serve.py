@@ -8,7 +8,6 @@ on the device of its tensors, which all have to be on one device.
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
 
 import torch
@@ -56,33 +55,6 @@ def _refuse(t, name, dtype, shape):
     raise ValueError(f"{name} must be on the device of the call's first tensor")
 
 
-def _dims(t, name, dims):
-    if t.dim() != dims:
-        raise ValueError(f"{name} must have {dims} dimensions, got {list(t.shape)}")
-    return t.shape
-
-
-class _Device:
-    """The device and the stream of a call while it allocates and enqueues.  Entered only where they are not the
-    current ones: a context manager costs as much as several checks."""
-
-    def __init__(self, device, stream):
-        self.device, self.stream = torch.cuda.device(device), None if stream is None else torch.cuda.stream(stream)
-
-    def __enter__(self):
-        self.device.__enter__()
-        if self.stream is not None:
-            self.stream.__enter__()
-
-    def __exit__(self, *exc):
-        if self.stream is not None:
-            self.stream.__exit__(*exc)
-        self.device.__exit__(*exc)
-
-
-_HERE_ALREADY = contextlib.nullcontext()
-
-
 def _device_of(t, name):
     device = t.get_device()
     if device < 0:
@@ -90,14 +62,27 @@ def _device_of(t, name):
     return device
 
 
-def _on(device, stream):
-    if stream is None and device == torch.cuda.current_device():
-        return _HERE_ALREADY
-    return _Device(device, stream)
+def _elsewhere(device, stream):
+    """Whether a call has to change the current device or stream first."""
+    return stream is not None or device != torch.cuda.current_device()
 
 
-def _stream(device, stream):
-    return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+class _On:
+    """The device and the stream of a call, while it allocates and enqueues."""
+
+    def __init__(self, device, stream):
+        self.entered = [torch.cuda.device(device)] + ([] if stream is None else [torch.cuda.stream(stream)])
+
+    def __enter__(self):
+        for c in self.entered:
+            c.__enter__()
+
+    def __exit__(self, *exc):
+        for c in reversed(self.entered):
+            c.__exit__(*exc)
+
+
+_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _bytes(t):
@@ -117,9 +102,11 @@ def gdn_batch_tables(context_lens, new_lens, T_total: int, page_size: int, block
     context_lens and new_lens are int32 [num_seqs] on the device (new_lens < 0: the request has ended); rows int32
     [num_seqs] names each request's row (None: row n)."""
     lib, dev, i32 = _gdn._load(), _device_of(context_lens, "context_lens"), torch.int32
-    (n,) = _dims(context_lens, "context_lens", 1)
-    num_rows, max_blocks = _dims(block_table, "block_table", 2)
-    (pages,) = _dims(free_pages, "free_pages", 1)
+    if _elsewhere(dev, stream):
+        with _On(dev, stream):
+            return gdn_batch_tables(context_lens, new_lens, T_total, page_size, block_table, page_counts, free_pages,
+                                    free_state, rows, workspace)
+    (n,), (num_rows, max_blocks), (pages,) = context_lens.shape, block_table.shape, free_pages.shape
     cp, np = _take(context_lens, "context_lens", i32, (n,), dev), _take(new_lens, "new_lens", i32, (n,), dev)
     rp = None if rows is None else _take(rows, "rows", i32, (n,), dev)
     table = _take(block_table, "block_table", i32, (num_rows, max_blocks), dev)
@@ -128,23 +115,21 @@ def gdn_batch_tables(context_lens, new_lens, T_total: int, page_size: int, block
     T = int(T_total)
     if T < 0:
         raise ValueError("T_total must be >= 0")
-    need = 0 if workspace is not None else lib.gdn_batch_tables_workspace_bytes(n, T) // 4
-    with _on(dev, stream):
-        # one block for the four results and the workspace
-        cu, kv, slots, pos, own = torch.empty(2 * n + 1 + 2 * T + need, dtype=i32,
-                                              device=context_lens.device).split((n + 1, n, T, T, need))
-        base = cu.data_ptr()
-        wp, wb = (own.data_ptr(), 4 * need) if workspace is None else (workspace.data_ptr(), _bytes(workspace))
-        st = lib.gdn_batch_tables(cp, np, rp, n, T, page_size, table, num_rows, max_blocks, counts, ring, pages, state,
-                                  base, base + 4 * (n + 1), base + 4 * (2 * n + 1), base + 4 * (2 * n + 1 + T), wp, wb,
-                                  _stream(dev, stream))
-    _gdn._check(st, "gdn_batch_tables")
+    need = lib.gdn_batch_tables_workspace_bytes(n, T) // 4 if workspace is None else 0
+    # one block for the four results and the workspace
+    cu, kv, slots, pos, own = torch.split_with_sizes(context_lens.new_empty(2 * n + 1 + 2 * T + need),
+                                                     (n + 1, n, T, T, need))
+    base = cu.data_ptr()
+    wp, wb = (own.data_ptr(), 4 * need) if workspace is None else (workspace.data_ptr(), _bytes(workspace))
+    st = lib.gdn_batch_tables(cp, np, rp, n, T, page_size, table, num_rows, max_blocks, counts, ring, pages, state, base,
+                              base + 4 * (n + 1), base + 4 * (2 * n + 1), base + 4 * (2 * n + 1 + T), wp, wb, _stream(dev))
+    if st:
+        _gdn._check(st, "gdn_batch_tables")
     return cu, kv, slots, pos
 
 
 def _cache(k_cache, v_cache, k_scale, v_scale, dev):
-    pages, hkv, page, dk = _dims(k_cache, "k_cache", 4)
-    dv = _dims(v_cache, "v_cache", 5)[3]
+    (pages, hkv, page, dk), (_, _, _, dv, _) = k_cache.shape, v_cache.shape
     return (pages, page, hkv, dk, dv, _take(k_cache, "k_cache", E4M3, (pages, hkv, page, dk), dev),
             _take(v_cache, "v_cache", E4M3, (pages, hkv, page // 16, dv, 16), dev),
             _take(k_scale, "k_scale", torch.float32, (pages, hkv), dev),
@@ -156,13 +141,16 @@ def gdn_cache_write(k, v, slots, k_cache, v_cache, k_scale, v_scale, stream=None
     k_cache [pages, H_kv, page, dk] and v_cache [pages, H_kv, page / 16, dv, 16] (torch.float8_e4m3fn), k_scale and
     v_scale [pages, H_kv] (fp32 powers of two), updated in place."""
     lib, dt, dev = _gdn._load(), _gdn._dtype_code(k), _device_of(k, "k")
+    if _elsewhere(dev, stream):
+        with _On(dev, stream):
+            return gdn_cache_write(k, v, slots, k_cache, v_cache, k_scale, v_scale)
     pages, page, hkv, dk, dv, kc, vc, ks, vs = _cache(k_cache, v_cache, k_scale, v_scale, dev)
-    T = _dims(k, "k", 3)[0]
+    T = k.shape[0]
     kp, vp = _take(k, "k", k.dtype, (T, hkv, dk), dev), _take(v, "v", k.dtype, (T, hkv, dv), dev)
     sp = _take(slots, "slots", torch.int32, (T,), dev)
-    with _on(dev, stream):
-        st = lib.gdn_cache_write(kp, vp, sp, T, kc, vc, ks, vs, pages, page, hkv, dk, dv, dt, _stream(dev, stream))
-    _gdn._check(st, "gdn_cache_write")
+    st = lib.gdn_cache_write(kp, vp, sp, T, kc, vc, ks, vs, pages, page, hkv, dk, dv, dt, _stream(dev))
+    if st:
+        _gdn._check(st, "gdn_cache_write")
 
 
 def gdn_cache_attention_workspace_bytes(num_seqs: int, T_total: int, max_new: int, max_kv: int, page_size: int,
@@ -178,29 +166,31 @@ def gdn_cache_attention(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_l
     kv_lens[n] tokens that row rows[n] (None: row n) of block_table holds.  scale: 1 / sqrt(dk) by default.  max_new
     and max_kv, host-side bounds on a request's new tokens and on kv_lens, help to plan (0: unknown)."""
     lib, dt, dev, i32 = _gdn._load(), _gdn._dtype_code(q), _device_of(q, "q"), torch.int32
+    if _elsewhere(dev, stream):
+        with _On(dev, stream):
+            return gdn_cache_attention(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, cu_seqlens, rows, scale,
+                                       max_new, max_kv, o, workspace)
     pages, page, hkv, dk, dv, kc, vc, ks, vs = _cache(k_cache, v_cache, k_scale, v_scale, dev)
-    T, H, _ = _dims(q, "q", 3)
-    (n,) = _dims(kv_lens, "kv_lens", 1)
-    num_rows, max_blocks = _dims(block_table, "block_table", 2)
+    (T, H, _), (n,), (num_rows, max_blocks) = q.shape, kv_lens.shape, block_table.shape
     qp = _take(q, "q", q.dtype, (T, H, dk), dev)
     table = _take(block_table, "block_table", i32, (num_rows, max_blocks), dev)
     rp = None if rows is None else _take(rows, "rows", i32, (n,), dev)
     kv, cu = _take(kv_lens, "kv_lens", i32, (n,), dev), _take(cu_seqlens, "cu_seqlens", i32, (n + 1,), dev)
-    with _on(dev, stream):
-        if o is None:
-            o = torch.empty((T, H, dv), dtype=q.dtype, device=q.device)
-            op = o.data_ptr()
-        else:
-            op = _take(o, "o", q.dtype, (T, H, dv), dev)
-        if workspace is None:
-            need = lib.gdn_cache_attention_workspace_bytes(n, T, max_new, max_kv, page, max_blocks, H, hkv, dk, dv)
-            if need:
-                workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-        wp, wb = (None, 0) if workspace is None else (workspace.data_ptr(), _bytes(workspace))
-        st = lib.gdn_cache_attention(qp, kc, vc, ks, vs, table, rp, kv, cu, n, T, max_new, max_kv, pages, page, num_rows,
-                                     max_blocks, dk ** -0.5 if scale is None else scale, op, H, hkv, dk, dv, dt, wp, wb,
-                                     _stream(dev, stream))
-    _gdn._check(st, "gdn_cache_attention")
+    if o is None:
+        o = q.new_empty((T, H, dv))
+        op = o.data_ptr()
+    else:
+        op = _take(o, "o", q.dtype, (T, H, dv), dev)
+    if workspace is None:
+        need = lib.gdn_cache_attention_workspace_bytes(n, T, max_new, max_kv, page, max_blocks, H, hkv, dk, dv)
+        if need:
+            workspace = k_scale.new_empty((need + 3) // 4)  # fp32
+    wp, wb = (None, 0) if workspace is None else (workspace.data_ptr(), _bytes(workspace))
+    st = lib.gdn_cache_attention(qp, kc, vc, ks, vs, table, rp, kv, cu, n, T, max_new, max_kv, pages, page, num_rows,
+                                 max_blocks, dk ** -0.5 if scale is None else scale, op, H, hkv, dk, dv, dt, wp, wb,
+                                 _stream(dev))
+    if st:
+        _gdn._check(st, "gdn_cache_attention")
     return o
 
 
@@ -212,9 +202,10 @@ def gdn_decode_pool(q, k, v, g, beta, states, slots, cu_seqlens=None, commit=Non
     [num_seqs + 1] (None: one token each); commit int32 [num_seqs]: the tokens whose update is kept (None: all);
     l2_eps > 0: q and k are L2-normalised in the kernel."""
     lib, dt, dev, i32, f32 = _gdn._load(), _gdn._dtype_code(q), _device_of(q, "q"), torch.int32, torch.float32
-    T, hk, dk = _dims(q, "q", 3)
-    num_slots, H, _, dv = _dims(states, "states", 4)
-    (n,) = _dims(slots, "slots", 1)
+    if _elsewhere(dev, stream):
+        with _On(dev, stream):
+            return gdn_decode_pool(q, k, v, g, beta, states, slots, cu_seqlens, commit, q_scale, l2_eps, o)
+    (T, hk, dk), (num_slots, H, _, dv), (n,) = q.shape, states.shape, slots.shape
     head_gate = g.dim() == 2
     qp, kp = _take(q, "q", q.dtype, (T, hk, dk), dev), _take(k, "k", q.dtype, (T, hk, dk), dev)
     vp = _take(v, "v", q.dtype, (T, H, dv), dev)
@@ -222,15 +213,15 @@ def gdn_decode_pool(q, k, v, g, beta, states, slots, cu_seqlens=None, commit=Non
     sp, lp = _take(states, "states", f32, (num_slots, H, dk, dv), dev), _take(slots, "slots", i32, (n,), dev)
     cp = None if cu_seqlens is None else _take(cu_seqlens, "cu_seqlens", i32, (n + 1,), dev)
     mp = None if commit is None else _take(commit, "commit", i32, (n,), dev)
-    with _on(dev, stream):
-        if o is None:
-            o = torch.empty((T, H, dv), dtype=q.dtype, device=q.device)
-            op = o.data_ptr()
-        else:
-            op = _take(o, "o", q.dtype, (T, H, dv), dev)
-        st = lib.gdn_decode_pool(qp, kp, vp, gp, head_gate, bp, sp, lp, cp, mp, n, T, num_slots, q_scale, l2_eps, op, H,
-                                 hk, dk, dv, dt, _stream(dev, stream))
-    _gdn._check(st, "gdn_decode_pool")
+    if o is None:
+        o = v.new_empty((T, H, dv))
+        op = o.data_ptr()
+    else:
+        op = _take(o, "o", q.dtype, (T, H, dv), dev)
+    st = lib.gdn_decode_pool(qp, kp, vp, gp, head_gate, bp, sp, lp, cp, mp, n, T, num_slots, q_scale, l2_eps, op, H, hk, dk,
+                             dv, dt, _stream(dev))
+    if st:
+        _gdn._check(st, "gdn_decode_pool")
     return o
 
 
