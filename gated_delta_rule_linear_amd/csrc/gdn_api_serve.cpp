@@ -161,7 +161,7 @@ int32_t gdn_batch_tables(const int32_t* context_lens, const int32_t* new_lens, c
 int32_t gdn_cache_write(const void* k, const void* v, const int32_t* slots, int64_t T_total, void* k_cache,
                         void* v_cache, float* k_scale, float* v_scale, int64_t num_pages, int32_t page_size,
                         int32_t H_kv, int32_t d_k, int32_t d_v, int32_t dtype, void* stream) {
-    if (T_total < 0 || T_total > INT32_MAX || num_pages < 0 || H_kv < 1 || H_kv > 32767) return GDN_ERR_INVALID_ARG;
+    if (T_total < 0 || T_total > INT32_MAX || num_pages < 0 || H_kv < 1 || H_kv > 8191) return GDN_ERR_INVALID_ARG;
     if (!supported_dtype(dtype) || !supported_d(d_k) || !supported_d(d_v) || !supported_page(page_size))
         return GDN_ERR_UNSUPPORTED;
     if (num_pages > ((int64_t)INT32_MAX + 1) / page_size) return GDN_ERR_UNSUPPORTED;  // slots are int32

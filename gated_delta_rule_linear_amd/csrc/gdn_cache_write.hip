@@ -21,11 +21,6 @@
 namespace gdn {
 namespace {
 
-#ifdef NTW
-#define LDW(p) __builtin_nontemporal_load(p)
-#else
-#define LDW(p) (*(p))
-#endif
 constexpr int kWaves = 4;
 constexpr int kShort = 4;  // a run of so many tokens is one wave's
 
@@ -45,48 +40,81 @@ struct Run {
     int a, b;      // places a .. b-1 of the page
 };
 
-// Two neighbouring values of a token.
-template <typename T>
-struct Pair;
-template <>
-struct Pair<float> {
-    floatx2 x;
-    __device__ __forceinline__ float get(int i) const { return x[i]; }
-};
-template <>
-struct Pair<bf16> {
-    bf16x2 x;
-    __device__ __forceinline__ float get(int i) const { return (float)x[i]; }
-};
-template <typename T>
-__device__ __forceinline__ Pair<T> load_pair(const T* p) {
-    return Pair<T>{LDW(reinterpret_cast<const decltype(Pair<T>::x)*>(p))};
-}
-// Eight of them.
-template <typename T>
-struct Eight {
-    T x[8];
-};
-template <typename T>
-__device__ __forceinline__ Eight<T> load_eight(const T* p) {
-    Eight<T> e;
-    if constexpr (sizeof(T) == 4) {
-        const floatx4 a = LDW(reinterpret_cast<const floatx4*>(p)), b = LDW(reinterpret_cast<const floatx4*>(p + 4));
+// N neighbouring values of a token, as they are in memory, and the largest
+// magnitude among such as bits: magnitudes order as the integers of their bits,
+// Inf and NaN above all, and two bf16 are compared at once.
+template <typename T, int N>
+struct Values {
+    static constexpr int WORDS = N * sizeof(T) / 4;
+    typedef uint32_t words __attribute__((ext_vector_type(WORDS > 4 ? 4 : WORDS)));
+    uint32_t w[WORDS];
+    __device__ __forceinline__ void load(const T* p) {
+        constexpr int V = WORDS > 4 ? 4 : WORDS;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) { e.x[i] = a[i]; e.x[i + 4] = b[i]; }
-    } else {
-        const bf16x8 a = LDW(reinterpret_cast<const bf16x8*>(p));
+        for (int i = 0; i < WORDS; i += V) {
+            const words x = __builtin_nontemporal_load(reinterpret_cast<const words*>(p) + i / V);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) e.x[i] = a[i];
+            for (int j = 0; j < V; ++j) w[i + j] = x[j];
+        }
     }
-    return e;
-}
-template <typename T>
-__device__ __forceinline__ uintx2 eight_codes(const Eight<T>& e, float inv) {
-    float f[8];
+    __device__ __forceinline__ void clear() {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = finite_or_nan(to_f32(e.x[i])) * inv;
-    return uintx2{to_e4m3(f[0], f[1], f[2], f[3]), to_e4m3(f[4], f[5], f[6], f[7])};
+        for (int i = 0; i < WORDS; ++i) w[i] = 0;
+    }
+    __device__ __forceinline__ float get(int i) const {
+        if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
+        else return __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+    }
+    // The largest magnitude so far, as `top_bits` undoes it.
+    __device__ __forceinline__ uint32_t top(uint32_t t) const {
+        typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i) {
+            if constexpr (sizeof(T) == 4) t = max(t, w[i] & 0x7fffffffu);
+            else
+                t = __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, t),
+                                                                           __builtin_bit_cast(u16x2, w[i] & 0x7fff7fffu)));
+        }
+        return t;
+    }
+    __device__ __forceinline__ float finite_top(float t) const {
+#pragma unroll
+        for (int i = 0; i < N; ++i) t = fmaxf(t, finite_abs(get(i)));
+        return t;
+    }
+};
+template <typename T>
+__device__ __forceinline__ float top_bits(uint32_t t) {  // as the bits of an fp32
+    if constexpr (sizeof(T) == 4) return __uint_as_float(t);
+    else return __uint_as_float(max(t << 16, t & 0xffff0000u));
+}
+struct MaxBits {
+    __device__ __forceinline__ static float of(float a, float b) { return __uint_as_float(max(__float_as_uint(a), __float_as_uint(b))); }
+};
+__device__ __forceinline__ bool is_finite(float bits) { return __float_as_uint(bits) < 0x7f800000u; }
+
+// Over W waves; one barrier, after which every thread has done what is before.
+template <typename OP, int W>
+__device__ __forceinline__ float over_waves(float x, float* lds) {
+    x = across<OP>(x);
+    if constexpr (W > 1) {
+        if (threadIdx.x % 64 == 0) lds[threadIdx.x / 64] = x;
+        __syncthreads();
+#pragma unroll
+        for (int v = 0; v < W; ++v) x = OP::of(x, lds[v]);
+    }
+    return x;
+}
+// The largest finite magnitude; *odd: there are others.
+template <typename T, int W, typename F>
+__device__ __forceinline__ float largest(uint32_t top, float* lds, bool* odd, F finite_top) {
+    float amax = over_waves<MaxBits, W>(top_bits<T>(top), lds);
+    *odd = !is_finite(amax);
+    if (*odd) {  // the same for all threads
+        if constexpr (W > 1) __syncthreads();
+        amax = over_waves<Max, W>(finite_top(), lds);
+    }
+    return amax;
 }
 
 // The page's scale behind the run and what its older codes are multiplied by (0:
@@ -106,122 +134,167 @@ __device__ __forceinline__ Scales new_scale(const Run& r, float was, float amax)
 }
 
 // Keys of a run, W waves.  A thread takes 8 neighbouring channels of a token;
-// UNROLL tokens (one for each pass over the run) stay in registers.
-template <typename T, int D, int W, int UNROLL>
+// UNROLL tokens (one for each pass over the run) stay in registers.  FULL: the
+// run is a whole page.
+template <typename T, int D, int W, int UNROLL, bool FULL>
 __device__ void write_keys(const Write& w, const Run& r, int h, int thread, float* lds) {
     constexpr int L = D / 8, STEP = 64 * W / L;
     const int32_t page = 1 << w.page_log2;
     const int c = thread % L * 8, i0 = thread / L;
-    const T* x = static_cast<const T*>(w.k) + (r.t * w.H + h) * D + c;
+    // A run's first token is the wave's, a thread's part of an address is below
+    // 2^31 bytes (256 tokens of at most 8191 heads).
+    const T* x = static_cast<const T*>(w.k) + (r.t * w.H + h) * D;
+    const uint32_t mine = (uint32_t)i0 * w.H * D + c;
     const int len = r.b - r.a;
-    Eight<T> e[UNROLL];
-    float top = 0.f;
+    Values<T, 8> e[UNROLL];
 #pragma unroll
-    for (int u = 0; u < UNROLL; ++u)
-        if (i0 + u * STEP < len) e[u] = load_eight(x + (int64_t)(i0 + u * STEP) * w.H * D);
+    for (int u = 0; u < UNROLL; ++u) {
+        if (!FULL) e[u].clear();
+        if (FULL || i0 + u * STEP < len) e[u].load(x + (int64_t)(u * STEP) * w.H * D + mine);
+    }
     float* scale = w.ks + r.page * w.H + h;
     const float was = *scale;
+    uint32_t top = 0;
 #pragma unroll
-    for (int u = 0; u < UNROLL; ++u)
-        if (i0 + u * STEP < len)
+    for (int u = 0; u < UNROLL; ++u) top = e[u].top(top);
+    bool odd;
+    const float amax = largest<T, W>(top, lds, &odd, [&]() {
+        float t = 0.f;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) top = fmaxf(top, finite_abs(to_f32(e[u].x[j])));
-    top = across<Max>(top);
-    if constexpr (W > 1) {
-        if (thread % 64 == 0) lds[thread / 64] = top;
-        __syncthreads();  // every thread has read the scale, too
-#pragma unroll
-        for (int v = 0; v < W; ++v) top = fmaxf(top, lds[v]);
-    }
-    const Scales s = new_scale(r, was, top);
+        for (int u = 0; u < UNROLL; ++u) t = e[u].finite_top(t);
+        return t;
+    });
+    const Scales s = new_scale(r, was, amax);
     const float inv = 1.f / s.now;
     if (thread == 0) *scale = s.now;
     uint8_t* to = w.kc + (r.page * w.H + h) * (int64_t)page * D + c;
+    auto write = [&](auto value) {
 #pragma unroll
-    for (int u = 0; u < UNROLL; ++u)
-        if (i0 + u * STEP < len)
-            *reinterpret_cast<uintx2*>(to + (int64_t)(r.a + i0 + u * STEP) * D) = eight_codes(e[u], inv);
-    if (r.a > 0 && s.factor == 1.f) return;
-    if (r.a == 0 && r.b == page) return;
-    // the page's other places: cleared, or at the larger scale
-#pragma unroll 8
-    for (int i = i0; i < page; i += STEP) {
-        if (i >= r.a && i < r.b) continue;
-        uintx2* at = reinterpret_cast<uintx2*>(to + (int64_t)i * D);
-        uintx2 old = {0u, 0u};
-        if (r.a > 0) {
-            old = *at;
-            old[0] = e4m3_rescaled(old[0], s.factor);
-            old[1] = e4m3_rescaled(old[1], s.factor);
+        for (int u = 0; u < UNROLL; ++u)
+            if (FULL || i0 + u * STEP < len) {
+                float f[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) f[i] = value(e[u].get(i)) * inv;
+                *reinterpret_cast<uintx2*>(to + (int64_t)(r.a + i0 + u * STEP) * D) =
+                    uintx2{to_e4m3(f[0], f[1], f[2], f[3]), to_e4m3(f[4], f[5], f[6], f[7])};
+            }
+    };
+    if (odd) write([](float v) { return finite_or_nan(v); });
+    else write([](float v) { return v; });
+    if (FULL || (r.a > 0 && s.factor == 1.f)) return;
+    // The page's other places: cleared, or at the larger scale.  Some are read
+    // before the first of them is written: a load behind a store that might be to
+    // the same place would wait for it.
+    constexpr int MANY = W == 1 ? 16 : 4;
+    for (int i1 = i0; i1 < page; i1 += MANY * STEP) {
+        uintx2 old[MANY];
+#pragma unroll
+        for (int u = 0; u < MANY; ++u) {
+            const int i = i1 + u * STEP;
+            old[u] = uintx2{0u, 0u};
+            if (r.a > 0 && i < page) old[u] = *reinterpret_cast<const uintx2*>(to + (int64_t)i * D);
         }
-        *at = old;
+#pragma unroll
+        for (int u = 0; u < MANY; ++u) {
+            const int i = i1 + u * STEP;
+            if (i < page && (i < r.a || i >= r.b))
+                *reinterpret_cast<uintx2*>(to + (int64_t)i * D) =
+                    uintx2{e4m3_rescaled(old[u][0], s.factor), e4m3_rescaled(old[u][1], s.factor)};
+        }
     }
 }
 
 // Values of a run, W waves.  A thread takes 2 neighbouring channels of the 16
 // places of a group, GROUPS groups of the page.
-template <typename T, int D, int W, int GROUPS>
+template <typename T, int D, int W, int GROUPS, bool FULL>
 __device__ void write_values(const Write& w, const Run& r, int h, int thread, float* lds) {
     constexpr int L = D / 2, STEP = 64 * W / L;  // threads of a group; groups side by side
     const int32_t page = 1 << w.page_log2;
     const int d = thread % L * 2, g0 = thread / L;
-    const T* x = static_cast<const T*>(w.v) + (r.t * w.H + h) * D + d;
-    Pair<T> e[GROUPS][16];
+    const T* x = static_cast<const T*>(w.v) + ((r.t - r.a) * w.H + h) * D;
+    const uint32_t mine = (uint32_t)(16 * g0) * w.H * D + d;
+    Values<T, 2> e[GROUPS][16];
 #pragma unroll
-    for (int u = 0; u < GROUPS; ++u)
+    for (int u = 0; u < GROUPS; ++u) {
+        const int p0 = 16 * (g0 + u * STEP);  // (with 64 channels, groups side by side may be more than a page's)
+        const bool in = p0 < page;
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
-            const int i = 16 * (g0 + u * STEP) + j - r.a;
-            e[u][j] = Pair<T>{};
-            if (i >= 0 && i < r.b - r.a) e[u][j] = load_pair(x + (int64_t)i * w.H * D);
+            const int i = p0 + j - r.a;
+            if (!FULL || D == 64) e[u][j].clear();
+            if (FULL ? D == 128 || in : i >= 0 && i < r.b - r.a) e[u][j].load(x + (int64_t)(16 * u * STEP + j) * w.H * D + mine);
         }
+    }
     float* scale = w.vs + r.page * w.H + h;
     const float was = *scale;
-    float top = 0.f;
+    uint32_t top = 0;
 #pragma unroll
     for (int u = 0; u < GROUPS; ++u)
 #pragma unroll
-        for (int j = 0; j < 16; ++j) top = fmaxf(top, fmaxf(finite_abs(e[u][j].get(0)), finite_abs(e[u][j].get(1))));
-    top = across<Max>(top);
-    if constexpr (W > 1) {
-        if (thread % 64 == 0) lds[thread / 64] = top;
-        __syncthreads();
+        for (int j = 0; j < 16; ++j) top = e[u][j].top(top);
+    bool odd;
+    const float amax = largest<T, W>(top, lds, &odd, [&]() {
+        float t = 0.f;
 #pragma unroll
-        for (int v = 0; v < W; ++v) top = fmaxf(top, lds[v]);
-    }
-    const Scales s = new_scale(r, was, top);
+        for (int u = 0; u < GROUPS; ++u)
+#pragma unroll
+            for (int j = 0; j < 16; ++j) t = e[u][j].finite_top(t);
+        return t;
+    });
+    const Scales s = new_scale(r, was, amax);
     const float inv = 1.f / s.now;
     if (thread == 0) *scale = s.now;
     const bool whole = r.a == 0 || s.factor != 1.f;
     uint8_t* to = w.vc + (r.page * w.H + h) * (int64_t)page * D;
+    auto write = [&](auto value) {
 #pragma unroll
-    for (int u = 0; u < GROUPS; ++u) {
-        const int p0 = 16 * (g0 + u * STEP);
-        if (p0 >= page || (!whole && (p0 >= r.b || p0 + 16 <= r.a))) continue;
-        uintx4* at = reinterpret_cast<uintx4*>(to + (int64_t)p0 * D + d * 16);
-        const bool full = p0 >= r.a && p0 + 16 <= r.b;
+        for (int u = 0; u < GROUPS; ++u) {
+            const int p0 = 16 * (g0 + u * STEP);
+            if (p0 >= page || (!whole && (p0 >= r.b || p0 + 16 <= r.a))) continue;
+            uintx4* at = reinterpret_cast<uintx4*>(to + (int64_t)p0 * D + d * 16);
+            const bool full = FULL || (p0 >= r.a && p0 + 16 <= r.b);
 #pragma unroll
-        for (int ch = 0; ch < 2; ++ch) {
-            uintx4 code = {0u, 0u, 0u, 0u};
-            if (!full && r.a > 0) code = at[ch];
+            for (int ch = 0; ch < 2; ++ch) {
+                uintx4 code = {0u, 0u, 0u, 0u};
+                if (!full && r.a > 0) code = at[ch];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                float f[4];
-                uint32_t run = 0;  // bytes of the run
+                for (int q = 0; q < 4; ++q) {
+                    float f[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    f[j] = finite_or_nan(e[u][4 * q + j].get(ch)) * inv;
-                    const int i = p0 + 4 * q + j;
-                    if (i >= r.a && i < r.b) run |= 0xffu << (8 * j);
+                    for (int j = 0; j < 4; ++j) f[j] = value(e[u][4 * q + j].get(ch)) * inv;
+                    const uint32_t fresh = to_e4m3(f[0], f[1], f[2], f[3]);
+                    if (full) {
+                        code[q] = fresh;
+                        continue;
+                    }
+                    uint32_t run = 0;  // bytes of the run
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int i = p0 + 4 * q + j;
+                        if (i >= r.a && i < r.b) run |= 0xffu << (8 * j);
+                    }
+                    // the others: at the page's new scale, or 0 in a page that begins anew
+                    code[q] = (fresh & run) | (e4m3_rescaled(code[q], s.factor) & ~run);
                 }
-                const uint32_t fresh = to_e4m3(f[0], f[1], f[2], f[3]);
-                // the others: at the page's new scale, or 0 in a page that begins anew
-                if (full) code[q] = fresh;
-                else code[q] = (fresh & run) | (e4m3_rescaled(code[q], s.factor) & ~run);
+                at[ch] = code;
             }
-            at[ch] = code;
         }
-    }
+    };
+    if (odd) write([](float v) { return finite_or_nan(v); });
+    else write([](float v) { return v; });
+}
+
+// A group's 16 codes with the run's, which begin `at` places in front of it, in
+// their places: byte i of `code` is that of the run's token i.
+__device__ __forceinline__ uintx4 with_new(uintx4 x, uint32_t code, int at, int len) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int i = at + 4 * q + j;
+            if (i >= 0 && i < len) x[q] = (x[q] & ~(0xffu << (8 * j))) | (((code >> (8 * i)) & 0xffu) << (8 * j));
+        }
+    return x;
 }
 
 // Values of a short run inside a page whose scale stays: single bytes; else the
@@ -232,11 +305,15 @@ __device__ void write_values_short(const Write& w, const Run& r, int h, int lane
     const int32_t page = 1 << w.page_log2;
     const T* x = static_cast<const T*>(w.v) + (r.t * w.H + h) * D + C * lane;
     const int len = r.b - r.a;
+    typedef T mine __attribute__((ext_vector_type(C)));
     float e[kShort][C], top = 0.f;
 #pragma unroll
-    for (int j = 0; j < kShort; ++j)
+    for (int j = 0; j < kShort; ++j) {
+        mine y = {};
+        if (j < len) y = *reinterpret_cast<const mine*>(x + (int64_t)j * w.H * D);
 #pragma unroll
-        for (int c = 0; c < C; ++c) e[j][c] = j < len ? to_f32(x[(int64_t)j * w.H * D + c]) : 0.f;
+        for (int c = 0; c < C; ++c) e[j][c] = to_f32(y[c]);
+    }
     float* scale = w.vs + r.page * w.H + h;
     const float was = *scale;
 #pragma unroll
@@ -263,25 +340,26 @@ __device__ void write_values_short(const Write& w, const Run& r, int h, int lane
         }
         return;
     }
-#pragma unroll 4
-    for (int p0 = 0; p0 < page; p0 += 16)
+    constexpr int MANY = 4;  // groups that are read before the first is written
+    for (int p1 = 0; p1 < page; p1 += 16 * MANY) {
+        uintx4 old[MANY][C];
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
-            uintx4* at = reinterpret_cast<uintx4*>(to + (int64_t)p0 * D + c * 16);
-            uintx4 old = {0u, 0u, 0u, 0u};
-            if (r.a > 0) old = *at;
+        for (int u = 0; u < MANY; ++u)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                old[q] = e4m3_rescaled(old[q], s.factor);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int i = p0 + 4 * q + j - r.a;  // the run's token here
-                    if (i >= 0 && i < len)
-                        old[q] = (old[q] & ~(0xffu << (8 * j))) | (((code[c] >> (8 * i)) & 0xffu) << (8 * j));
-                }
+            for (int c = 0; c < C; ++c) {
+                old[u][c] = uintx4{0u, 0u, 0u, 0u};
+                if (r.a > 0) old[u][c] = *reinterpret_cast<const uintx4*>(to + (int64_t)(p1 + 16 * u) * D + c * 16);
             }
-            *at = old;
-        }
+#pragma unroll
+        for (int u = 0; u < MANY; ++u)
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                uintx4 x16 = old[u][c];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) x16[q] = e4m3_rescaled(x16[q], s.factor);
+                *reinterpret_cast<uintx4*>(to + (int64_t)(p1 + 16 * u) * D + c * 16) = with_new(x16, code[c], p1 + 16 * u - r.a, len);
+            }
+    }
 }
 static_assert(kShort == 4, "a lane's new codes are one word");
 
@@ -332,11 +410,18 @@ __global__ __launch_bounds__(64 * kWaves) void cache_write_kernel(Write w) {
         if (len <= kShort) {
             if (shorts++ % kWaves != wave) continue;
             if (values) write_values_short<T, DV>(w, r, h, lane);
-            else write_keys<T, DK, 1, (kShort * DK / 8 + 63) / 64>(w, r, h, lane, nullptr);
+            else write_keys<T, DK, 1, (kShort * DK / 8 + 63) / 64, false>(w, r, h, lane, nullptr);
         } else {
             float* const l = lds[longs++ & 1];
-            if (values) write_values<T, DV, kWaves, (PG * DV / 32 + kWaves - 1) / kWaves>(w, r, h, threadIdx.x, l);
-            else write_keys<T, DK, kWaves, PG * DK / 8 / kWaves>(w, r, h, threadIdx.x, l);
+            constexpr int KU = PG * DK / 8 / kWaves, VG = (PG * DV / 32 + kWaves - 1) / kWaves;
+            if (len == page) {
+                if (values) write_values<T, DV, kWaves, VG, true>(w, r, h, threadIdx.x, l);
+                else write_keys<T, DK, kWaves, KU, true>(w, r, h, threadIdx.x, l);
+            } else if (values) {
+                write_values<T, DV, kWaves, VG, false>(w, r, h, threadIdx.x, l);
+            } else {
+                write_keys<T, DK, kWaves, KU, false>(w, r, h, threadIdx.x, l);
+            }
         }
     }
 }
