@@ -79,6 +79,37 @@ int32_t validate_slots(const gdn::CacheWriteLaunch& p, hipStream_t s) {
     return GDN_OK;
 }
 
+int32_t validate_attention(const gdn::CacheAttentionLaunch& p, hipStream_t s) {
+    std::vector<int32_t> cu, kv, rows, table;
+    if (!to_host(cu, p.cu_seqlens, (int64_t)p.num_seqs + 1, s) || !to_host(kv, p.kv_lens, p.num_seqs, s)) return GDN_ERR_HIP;
+    if (cu.front() != 0 || cu.back() > p.T_total) return GDN_ERR_DOMAIN;
+    for (size_t n = 1; n < cu.size(); ++n)
+        if (cu[n] < cu[n - 1]) return GDN_ERR_DOMAIN;
+    for (const int32_t x : kv)
+        if (x < 0 || x > (int64_t)p.max_blocks * p.page_size) return GDN_ERR_DOMAIN;
+    if (p.rows && !to_host(rows, p.rows, p.num_seqs, s)) return GDN_ERR_HIP;
+    if (p.num_pages == 0) return GDN_OK;
+    std::vector<float> scale[2];
+    if (!to_host(table, p.block_table, (int64_t)p.num_rows * p.max_blocks, s) ||
+        !to_host(scale[0], p.k_scale, p.num_pages * p.H_kv, s) || !to_host(scale[1], p.v_scale, p.num_pages * p.H_kv, s))
+        return GDN_ERR_HIP;
+    for (int32_t n = 0; n < p.num_seqs; ++n) {
+        const int64_t row = p.rows ? rows[(size_t)n] : n;
+        if (row < 0 || row >= p.num_rows) continue;
+        for (int64_t b = 0; b * p.page_size < kv[(size_t)n]; ++b) {
+            const int64_t page = table[(size_t)(row * p.max_blocks + b)];
+            if (page < 0 || page >= p.num_pages) continue;
+            int e;
+            for (const auto& x : scale)
+                for (int32_t h = 0; h < p.H_kv; ++h) {
+                    const float f = x[(size_t)(page * p.H_kv + h)];
+                    if (!(f > 0.f) || std::isinf(f) || std::frexp(f, &e) != 0.5f) return GDN_ERR_DOMAIN;
+                }
+        }
+    }
+    return GDN_OK;
+}
+
 int32_t validate_pool(const gdn::DecodePoolLaunch& p, hipStream_t s) {
     std::vector<int32_t> slots, cu;
     std::vector<float> g;
@@ -213,7 +244,12 @@ int32_t gdn_cache_attention(const void* q, const void* k_cache, const void* v_ca
         return GDN_ERR_INVALID_ARG;
     const size_t need = gdn::cache_attention_workspace_bytes(p);
     if (need > 0 && (!aligned(workspace, 16) || workspace_bytes < need)) return GDN_ERR_INVALID_ARG;
-    return status_of(gdn::launch_cache_attention(p, static_cast<hipStream_t>(stream)));
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (validate_mode()) {
+        const int32_t v = validated(validate_attention, p, s);
+        if (v != GDN_OK) return v;
+    }
+    return status_of(gdn::launch_cache_attention(p, s));
 }
 
 int32_t gdn_decode_pool(const void* q, const void* k, const void* v, const float* g, int32_t head_gate,

@@ -279,7 +279,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_rows_kernel(Attentio
                 const int row = (64 * j + lane) / PR, c = lane % PR;
                 s_k[row * PR + (c ^ turn(row))] = kr[j];
             }
-            __builtin_amdgcn_wave_barrier();  // the wave's own writes and reads of s_k stay in this order
+            asm volatile("" ::: "memory");  // the wave's writes and reads of s_k stay in this order
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 floatx4 x = zero4();
@@ -297,6 +297,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_rows_kernel(Attentio
                 for (int j = 0; j < 4; ++j) s[4 * c + j] = x[j] * c2;
             }
         }
+        asm volatile("" ::: "memory");  // (and the next tile's writes behind them)
         if (++at == 64) {
             pages.fetch(a, table, h, base + STEP, to, STEP);
             at = 0;
@@ -915,12 +916,13 @@ Plan plan(const CacheAttentionLaunch& p) {
     r.splits[0] = r.splits[1] = 1;
     r.min_chunk[0] = r.min_chunk[1] = kTile;
     if (r.few) {
+        // Enough parts to fill the device, none of the longest request above 8192
+        // tokens; but, for the workspace's sake, not more parts than 16384 in all.
         const int64_t units = (int64_t)p.num_seqs * p.H_kv * up(r.few_rows, 16);
-        int64_t chunk = up(up(kv * units, kAtOnce), kTile) * kTile;
-        chunk = chunk < 512 ? 512 : chunk > 8192 ? 8192 : chunk;
-        const int64_t splits = up(kv, chunk);
-        r.splits[0] = (int32_t)(splits < 1 ? 1 : splits > 256 ? 256 : splits);
-        r.min_chunk[0] = (int32_t)chunk;
+        int64_t splits = std::max(up(kAtOnce, units), up(kv, 8192));
+        splits = std::min(splits, std::min<int64_t>(up(kv, 512), std::max<int64_t>(16384 / units, 1)));
+        r.splits[0] = (int32_t)std::max<int64_t>(std::min<int64_t>(splits, 256), 1);
+        r.min_chunk[0] = units >= kAtOnce ? 2048 : 512;  // a shorter part costs more to begin than it saves
     }
     if (r.many) {
         const int64_t tiles = up(all, 32 * kWaves) > p.num_seqs ? up(all, 32 * kWaves) : p.num_seqs, units = tiles * p.H_kv;

@@ -12,7 +12,8 @@
  * work enqueued on `stream` without waiting, status codes, argument errors
  * reported before any memory is touched, no allocation, no state kept between
  * calls, calls on different streams independent of each other, every call
- * capturable into a graph.  Contents of index arrays are checked in the
+ * capturable into a graph (GDN_VALIDATE=1 aside, which waits for the stream).
+ * Contents of index arrays are checked in the
  * kernels where a bad value could address memory outside the arrays given, as
  * stated at each call.  Floating inputs with NaN or Inf are not masked: they
  * propagate, and only where the definition lets them.
@@ -80,7 +81,9 @@ extern "C" {
  * has no room (max_blocks), when it owns fewer pages than context_lens needs,
  * or when rows[n] is outside [0, num_rows).  A refused request keeps its pages and its kv_lens entry is context_lens[n]; its
  * tokens stay in cu_seqlens.  Pages given back in a call are free for the next
- * call.  Calling again with the same lengths changes nothing.
+ * call.  Calling again with the same lengths changes nothing.  A call reads and
+ * updates the tables and the ring: calls on the same ones are ordered by the
+ * caller, as on one stream.
  * GDN_VALIDATE=1 copies the lengths, the rows, the counts and the ring to the
  * host and returns GDN_ERR_DOMAIN for negative context_lens, rows that repeat
  * or lie outside, and a ring that does not fit its array. */
@@ -141,7 +144,12 @@ int32_t gdn_cache_write(const void* k, const void* v, const int32_t* slots, int6
  * token's own position.  Tokens whose block table entry is outside
  * [0, num_pages) or whose row is outside [0, num_rows) are left out; a row that
  * sees no token (kv_lens 0, or more new tokens than kv_lens) is 0.  A NaN in a
- * key or value reaches only the rows that see its token.
+ * key or value reaches only the rows that see its token.  Scales that are not
+ * powers of two are not supported (they are exact factors of bf16 operands).
+ * Two calls in flight at once need two workspaces.
+ * GDN_VALIDATE=1 returns GDN_ERR_DOMAIN for offsets that decrease or end behind
+ * T_total, lengths below 0 or past the table, and scales of held pages that are
+ * not positive powers of two.
  *
  * GDN_BF16: products on bf16 matrix cores (e4m3 codes are exact in bf16) with
  * fp32 accumulation, softmax in fp32, p rounded to bf16 for the second

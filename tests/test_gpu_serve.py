@@ -278,6 +278,15 @@ def test_attention_prompts(lens, kv, dtype, dk, dv):
     _attention_check(ref.Server(kv, 64, 2, dk, dv, seed=kv[0]), lens, 8, dtype, max_new=max(lens), max_kv=max(kv))
 
 
+@pytest.mark.parametrize("lens,kv,hints", [([2, 1, 70, 0], [9000, 5, 300, 7], dict(max_new=1, max_kv=64)),
+                                           ([2, 3], [9000, 40000], dict(max_new=1)),
+                                           ([1, 1], [9000, 40000], dict(max_new=500)),
+                                           ([300], [700], dict(max_new=1, max_kv=1)), ([5], [70000], dict())])
+def test_attention_hints_are_only_hints(lens, kv, hints):
+    log(f"attention new={lens} kv={kv} hints {hints}")
+    _attention_check(ref.Server(kv, 128, 2, 64, 64, seed=11), lens, 8, torch.bfloat16, **hints)
+
+
 @pytest.mark.parametrize("lens", [[1, 1, 1, 1], [3, 70, 1, 200]])
 def test_attention_rows_that_see_nothing(lens):
     # more new tokens than tokens held, an empty cache, a padded batch
@@ -623,6 +632,18 @@ def test_validation_mode(monkeypatch):
     for slots in ([5, 7], [6, 5], [5, 5]):
         with pytest.raises(gdn.GdnError) as e:
             gdn.gdn_cache_write(one, one, i32(slots), *cache)
+        assert e.value.status == gdn.GDN_ERR_DOMAIN
+    s = ref.Server([100, 30], 64, 2, 64, 64)
+    kc, vc, ks, vs, tab, kv, _ = s.to("cuda")
+    q = torch.zeros((3, 4, 64), device="cuda")
+    gdn.gdn_cache_attention(q, kc, vc, ks, vs, tab, kv, i32([0, 2, 3]))
+    odd = ks.clone()
+    odd[int(s.table[0, 1])] *= 1.5
+    for bad in (dict(ks=odd), dict(kv=i32([-1, 30])), dict(kv=i32([100, 300])), dict(cu=i32([0, 2, 4])),
+                dict(cu=i32([0, 2, 1])), dict(cu=i32([1, 2, 3]))):
+        a = dict(q=q, kc=kc, vc=vc, ks=ks, vs=vs, tab=tab, kv=kv, cu=i32([0, 2, 3])) | bad
+        with pytest.raises(gdn.GdnError) as e:
+            gdn.gdn_cache_attention(*a.values())
         assert e.value.status == gdn.GDN_ERR_DOMAIN
     args = [t.cuda() for t in _pool_inputs([1, 1], 2, 2, 64, 64, torch.float32, True, [0, 1], 0, 1, True)]
     gdn.gdn_decode_pool(*args, i32([1, -1]))
