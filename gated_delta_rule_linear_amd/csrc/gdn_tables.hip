@@ -10,7 +10,9 @@
 // waves' through LDS).  The tokens, each of which only has to find its request,
 // are filled by that workgroup in the same launch when there are few of them
 // and of the requests, whose data then stays in LDS, and otherwise by a second
-// launch over the whole device.
+// launch over the whole device.  Measured in a graph, where a launch that does
+// nothing is 3.5 us: 512 requests of one token 8.8 us, 64 prompts of 512 to 16,384
+// tokens (4.3 MB written) 9.2 us.
 #include "gdn_device.h"
 #include "gdn_serve_kernels.h"
 
@@ -21,7 +23,9 @@ constexpr int kScan = 512;       // threads of the summing workgroup
 constexpr int kFill = 256;       // threads of a fill workgroup
 constexpr int kPerThread = 4;    // tokens per thread of the fill step
 constexpr int kCuLds = 4096;     // offsets held in LDS by the fill step
-constexpr int64_t kOneLaunch = 4096;  // up to so many tokens (and kScan requests) one launch does all
+// Up to so many tokens (and kScan requests) one launch does all.  64 requests,
+// one launch / two: 2,048 tokens 6.6 / 8.5 us, 4,096 tokens 9.0 / 8.4, 8,192 13.6 / 8.5.
+constexpr int64_t kOneLaunch = 2048;
 
 struct Tables {
     const int32_t *ctx, *nw, *rows;
