@@ -10,10 +10,14 @@
 // A workgroup looks at the runs that start in a tile of tokens: of few tokens
 // where there are few (each token of a decode step is a run, and each wave takes
 // its own, without a barrier), of more where there are many (a prompt's runs are
-// whole pages, which the four waves share).
+// whole pages, which all waves share).
 //
 // Three operations per element: bound by the bytes read (2 or 4 for each) and
-// written (1).
+// written (1).  Measured with 8 heads of 128 + 128 channels, bf16, pages of 64:
+// 65,536 tokens of whole pages, 403 MB, in 83 us: 4.8 TB/s, what a large copy
+// reaches (4.9).  512 single tokens move 3.2 MB and what growing scales make of
+// their pages: 12 us, of which a launch is 3.5 and the rest a chain of slot,
+// values, old scale, old codes, each behind the one before.
 #include "gdn_e4m3.h"
 #include "gdn_lanes.h"
 #include "gdn_serve_kernels.h"
@@ -21,8 +25,21 @@
 namespace gdn {
 namespace {
 
+// Waves of a workgroup for each 64 places of a page, so that a thread's part of a
+// whole page is 16 words at every page size and four waves fit a SIMD.  (Four
+// waves for pages of 256 need 64 words, one wave fits: 32,768 tokens with the
+// grid below took 115 us and take 64.)
 constexpr int kWaves = 4;
-constexpr int kShort = 4;  // a run of so many tokens is one wave's
+// Tiles grow, from a token for each wave up to a page, while the grid has more
+// workgroups than this (of 4 waves): twice what the card holds at once
+// shares out uneven runs, and more are mostly workgroups in which no run starts.
+// 1024 / 2048 / 4096 / 16384: 2,048 tokens of a prompt 5.8 / 7.0 / 8.1 / 10.0 us,
+// 8,192 tokens 13.6 / 13.6 / 20.4 / 27.5, 64 requests of 1 to 64 tokens
+// 16.5 / 13.1 / 13.4 / 16.6, 4,096 single tokens 60 / 61 / 61 / 73.
+constexpr int kGrid = 2048;
+// A run of so many tokens is one wave's: these fit a lane's word of new codes, and
+// a wave needs no barrier.
+constexpr int kShort = 4;
 
 struct Write {
     const void *k, *v;
@@ -365,70 +382,77 @@ static_assert(kShort == 4, "a lane's new codes are one word");
 
 // PG: page_size / 64.
 template <typename T, int DK, int DV, int PG>
-__global__ __launch_bounds__(64 * kWaves) void cache_write_kernel(Write w) {
-    __shared__ float lds[2][kWaves];
-    constexpr int page = 64 * PG;
+__global__ __launch_bounds__(64 * kWaves * PG) void cache_write_kernel(Write w) {
+    constexpr int page = 64 * PG, W = kWaves * PG;
+    __shared__ float lds[2][W];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     // The heads' keys and values of a tile of tokens are neighbours in memory and
     // in the grid.
-    const int64_t t0 = (int64_t)(blockIdx.x / (2 * w.H)) * w.tile;
+    const int64_t begin = (int64_t)(blockIdx.x / (2 * w.H)) * w.tile, end = min(begin + w.tile, w.T);
     const int y = blockIdx.x % (2 * w.H), h = y >= w.H ? y - w.H : y;
     const bool values = y >= w.H;
-    // Runs that start in this tile: every wave finds them, a lane for each of the
-    // 64 tokens from the tile's first.
-    int64_t slot = -1, before = -1;
-    if (t0 + lane < w.T) {
-        slot = w.slots[t0 + lane];
-        if (t0 + lane > 0) before = w.slots[t0 + lane - 1];
-    }
-    const bool on = slot >= 0 && slot < w.places, first = on && (slot % page == 0 || before != slot - 1);
-    uint64_t todo = __ballot(first && lane < w.tile);
-    const uint64_t joined = __ballot(on && !first);  // tokens in a run with the one before
-    for (int shorts = 0, longs = 0; todo;) {
-        const int at = __ffsll((unsigned long long)todo) - 1;
-        todo &= todo - 1;
-        Run r;
-        r.t = t0 + at;
-        const int64_t s = __builtin_amdgcn_readlane((int)slot, at);  // slots are int32
-        r.page = s / page;
-        r.a = (int)(s % page);
-        const uint64_t stop = at == 63 ? 0 : ~joined >> (at + 1);
-        int len = stop ? __ffsll((unsigned long long)stop) : 64 - at;
-        if (at + len == 64)  // the run may go on behind these tokens
-            for (int i0 = len; i0 < page - r.a; i0 += 64) {
-                const int i = i0 + lane;
-                const bool more = i < page - r.a && r.t + i < w.T && w.slots[r.t + i] == s + i;
-                const uint64_t off = ~__ballot(more);
-                len += off ? __ffsll((unsigned long long)off) - 1 : 64;
-                if (off) break;
-            }
-        r.b = r.a + len;
-        // All waves see the same runs in the same order, so they take the same
-        // branches here and meet at the same barriers, one for each long run; two
-        // sets of lds, taken in turn by long runs, keep a barrier between two uses
-        // of one.
-        if (len <= kShort) {
-            if (shorts++ % kWaves != wave) continue;
-            if (values) write_values_short<T, DV>(w, r, h, lane);
-            else write_keys<T, DK, 1, (kShort * DK / 8 + 63) / 64, false>(w, r, h, lane, nullptr);
-        } else {
-            float* const l = lds[longs++ & 1];
-            constexpr int KU = PG * DK / 8 / kWaves, VG = (PG * DV / 32 + kWaves - 1) / kWaves;
-            if (len == page) {
-                if (values) write_values<T, DV, kWaves, VG, true>(w, r, h, threadIdx.x, l);
-                else write_keys<T, DK, kWaves, KU, true>(w, r, h, threadIdx.x, l);
-            } else if (values) {
-                write_values<T, DV, kWaves, VG, false>(w, r, h, threadIdx.x, l);
+    // Runs that start in this tile: every wave finds them, a lane for each of 64
+    // tokens.
+    int shorts = 0, longs = 0;
+    int64_t t0 = begin, next;
+    do {
+        next = t0 + 64;  // or behind the last run
+        int64_t slot = -1, before = -1;
+        if (t0 + lane < w.T) {
+            slot = w.slots[t0 + lane];
+            if (t0 + lane > 0) before = w.slots[t0 + lane - 1];
+        }
+        const bool on = slot >= 0 && slot < w.places, first = on && (slot % page == 0 || before != slot - 1);
+        uint64_t todo = __ballot(first && t0 + lane < end);
+        const uint64_t joined = __ballot(on && !first);  // tokens in a run with the one before
+        while (todo) {
+            const int at = __ffsll((unsigned long long)todo) - 1;
+            todo &= todo - 1;
+            Run r;
+            r.t = t0 + at;
+            const int64_t s = __builtin_amdgcn_readlane((int)slot, at);  // slots are int32
+            r.page = s / page;
+            r.a = (int)(s % page);
+            const uint64_t stop = at == 63 ? 0 : ~joined >> (at + 1);
+            int len = stop ? __ffsll((unsigned long long)stop) : 64 - at;
+            if (at + len == 64)  // the run may go on behind these tokens
+                for (int i0 = len; i0 < page - r.a; i0 += 64) {
+                    const int i = i0 + lane;
+                    const bool more = i < page - r.a && r.t + i < w.T && w.slots[r.t + i] == s + i;
+                    const uint64_t off = ~__ballot(more);
+                    len += off ? __ffsll((unsigned long long)off) - 1 : 64;
+                    if (off) break;
+                }
+            r.b = r.a + len;
+            next = max(next, r.t + len);
+            // All waves see the same runs in the same order, so they take the same
+            // branches here and meet at the same barriers, one for each long run; two
+            // sets of lds, taken in turn by long runs, keep a barrier between two uses
+            // of one.
+            if (len <= kShort) {
+                if (shorts++ % W != wave) continue;
+                if (values) write_values_short<T, DV>(w, r, h, lane);
+                else write_keys<T, DK, 1, (kShort * DK / 8 + 63) / 64, false>(w, r, h, lane, nullptr);
             } else {
-                write_keys<T, DK, kWaves, KU, false>(w, r, h, threadIdx.x, l);
+                float* const l = lds[longs++ & 1];
+                constexpr int KU = DK / 8 / kWaves, VG = (DV / 32 + kWaves - 1) / kWaves;
+                if (len == page) {
+                    if (values) write_values<T, DV, W, VG, true>(w, r, h, threadIdx.x, l);
+                    else write_keys<T, DK, W, KU, true>(w, r, h, threadIdx.x, l);
+                } else if (values) {
+                    write_values<T, DV, W, VG, false>(w, r, h, threadIdx.x, l);
+                } else {
+                    write_keys<T, DK, W, KU, false>(w, r, h, threadIdx.x, l);
+                }
             }
         }
-    }
+        t0 = next;
+    } while (PG > 1 && t0 < end);  // (a tile is at most a page)
 }
 
 template <typename T, int DK, int DV>
 void run_d(const Write& w, dim3 grid, hipStream_t s) {
-    const dim3 b(64 * kWaves);
+    const dim3 b(kWaves << w.page_log2);
     if (w.page_log2 == 6) hipLaunchKernelGGL((cache_write_kernel<T, DK, DV, 1>), grid, b, 0, s, w);
     else if (w.page_log2 == 7) hipLaunchKernelGGL((cache_write_kernel<T, DK, DV, 2>), grid, b, 0, s, w);
     else hipLaunchKernelGGL((cache_write_kernel<T, DK, DV, 4>), grid, b, 0, s, w);
@@ -446,9 +470,10 @@ void run(const Write& w, int32_t dk, int32_t dv, dim3 grid, hipStream_t s) {
 hipError_t launch_cache_write(const CacheWriteLaunch& p, hipStream_t s) {
     if (p.T_total == 0 || p.num_pages == 0) return hipSuccess;
     Write w = {p.k, p.v, p.slots, p.T_total, p.k_cache, p.v_cache, p.k_scale, p.v_scale, p.num_pages * p.page_size,
-               p.page_size == 64 ? 6 : p.page_size == 128 ? 7 : 8, p.H_kv, kWaves};
-    // Tokens of a tile: one for each wave while the grid is small, at most a wave's lanes.
-    while (w.tile < 64 && (p.T_total + w.tile - 1) / w.tile * 2 * p.H_kv > 16384) w.tile *= 2;
+               p.page_size == 64 ? 6 : p.page_size == 128 ? 7 : 8, p.H_kv, 0};
+    // Tokens of a tile: one for each wave while the grid is small, at most a page's.
+    w.tile = kWaves * (int)(p.page_size / 64);
+    while (w.tile < p.page_size && (p.T_total + w.tile - 1) / w.tile * 2 * p.H_kv > kGrid / (p.page_size / 64)) w.tile *= 2;
     const dim3 grid((unsigned)((p.T_total + w.tile - 1) / w.tile * 2 * p.H_kv));
     if (p.bf16) run<bf16>(w, p.dk, p.dv, grid, s);
     else run<float>(w, p.dk, p.dv, grid, s);

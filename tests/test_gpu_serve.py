@@ -167,6 +167,27 @@ def test_write_sizes(T, hkv):
     _write_check(k, v, slots, *cache)
 
 
+@pytest.mark.parametrize("page", [64, 128, 256])
+@pytest.mark.parametrize("longest", [6, 90, 700])
+def test_write_many_runs(page, longest):
+    # runs of all lengths, some over several pages, so many that a workgroup takes more than one of them
+    gen = torch.Generator().manual_seed(page + longest)
+    hkv, slots = 8, []
+    T, pages = (1500, 640) if longest == 6 else (2900, 150)
+    order = torch.randperm(pages, generator=gen).tolist()
+    while len(slots) < T:
+        n = int(torch.randint(1, longest + 1, (1,), generator=gen))
+        at = int(torch.randint(0, page, (1,), generator=gen))
+        while n:
+            m = min(n, page - at)
+            p = order.pop()
+            slots += [p * page + at + i for i in range(m)]
+            n, at = n - m, 0
+    cache = _pool_of_pages(gen, pages, hkv, page, 64, 64)
+    k, v = (torch.randn((len(slots), hkv, 64), generator=gen).bfloat16().cuda() for _ in range(2))
+    _write_check(k, v, slots, *cache)
+
+
 def test_write_values_at_the_borders():
     # zeros, subnormals, the largest values, Inf and NaN, ties between codes, a scale that grows by 2^200
     gen = torch.Generator().manual_seed(4)
