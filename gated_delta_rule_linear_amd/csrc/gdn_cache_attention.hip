@@ -35,6 +35,7 @@ typedef float floatx16 __attribute__((ext_vector_type(16)));
 
 constexpr int kTile = 64;      // tokens of a tile
 constexpr int kFewRows = 32;   // a request with up to so many rows is one of few rows
+constexpr int kMinPart = 512;  // tokens of a part of a request's cache, at least
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kInf = __builtin_inff();
 
@@ -51,9 +52,9 @@ struct Attention {
     void* o;
     int32_t H, Hkv, G;
     // Requests of few rows (at most few_rows) and the others: at most so many
-    // parts of a request's cache, of at least so many tokens.
+    // parts of a request's cache.
     int32_t few_rows;
-    int32_t splits[2], min_chunk[2];
+    int32_t splits[2];
     bool tiled;  // the others go to the tile kernel
     // Parts before they are joined, [part][row][d_v] and [part][row][2] (maximum
     // and sum).  Rows: for few, (n * Hkv + h) * few_rows + row; else those of q.
@@ -96,7 +97,7 @@ struct Request {
         few = rows <= a.few_rows;
         const int c = few ? 0 : 1;
         chunk = ((kv + a.splits[c] - 1) / a.splits[c] + kTile - 1) / kTile * kTile;
-        if (chunk < a.min_chunk[c]) chunk = a.min_chunk[c];
+        if (chunk < kMinPart) chunk = kMinPart;
         if (!few && !a.tiled && chunk < kv) chunk = (kv + kTile - 1) / kTile * kTile;  // there is no room for its parts
     }
     __device__ __forceinline__ bool alone() const { return kv <= chunk; }
@@ -194,7 +195,7 @@ constexpr int kWaves = 4;
 // asked for when the last keys have become scores, values when the last values
 // have been used.
 //
-// Bound by reading the cache: 5.4 TB/s over 64 requests of 512 to 16384 tokens
+// Bound by reading the cache: 5.6 TB/s over 64 requests of 512 to 16384 tokens
 // (8 heads of 128 channels, 8 KB of a page at a time in random order), which the
 // same kernel with the loads alone does not exceed by more than 3%; 4.8 over one
 // request of 65536.  Keys' loads that take half a line of each row instead ran
@@ -911,14 +912,14 @@ constexpr int64_t kAtOnce = 512;  // workgroups that the device holds: two on ea
 
 struct Plan {
     bool few, many;  // kernels that the call needs
-    int32_t few_rows, splits[2], min_chunk[2];
+    int32_t few_rows, splits[2];
     size_t off[4], bytes;  // ws_o and ws_ml of few, of the others
 };
 
 // The lengths are on the device, so the plan goes by sizes and bounds.  A
 // request has at most max_new (or T_total) new tokens: whether that is few rows
 // decides which kernels run.  Each request's cache is cut into at most `splits`
-// parts of at least min_chunk tokens, so that there are enough workgroups when
+// parts of at least kMinPart tokens, so that there are enough workgroups when
 // every request is as long as the bound, and so that the lengths, which may
 // differ much, do not leave the device waiting for a few long parts.
 Plan plan(const CacheAttentionLaunch& p) {
@@ -932,22 +933,28 @@ Plan plan(const CacheAttentionLaunch& p) {
     r.few = !r.many || p.num_seqs > 1;
     r.few_rows = (int32_t)(most < kFewRows ? most : kFewRows);
     r.splits[0] = r.splits[1] = 1;
-    r.min_chunk[0] = r.min_chunk[1] = kTile;
     if (r.few) {
-        // Enough parts to fill the device, none of the longest request above 8192
-        // tokens; but, for the workspace's sake, not more parts than 16384 in all.
+        // From a workgroup for each compute unit on, a part for each request (32
+        // requests over 4096, 256 workgroups: 44.6 us, in two parts 49.3); below,
+        // enough parts to fill the device, since the lengths may differ much (23
+        // over 1 to 4097, 92 units: 15.0 us with 512 at once, 18.2 with 256), none
+        // below 512 tokens (with 256, 4 over 100 to 500 take 9.2 us instead of 7.0,
+        // 1 over 1000 takes 9.0 instead of 9.8).  A long request beside many short
+        // ones should not be waited for: at most 16384 tokens to a part (which is no
+        // cut for 64 over 512 to 16384: 206 us; with 8192, 212).  For the
+        // workspace's sake, not more parts than 16384 in all.
         const int64_t units = (int64_t)p.num_seqs * p.H_kv * up(r.few_rows, 16);
-        int64_t splits = std::max(up(kAtOnce, units), up(kv, 8192));
-        splits = std::min(splits, std::min<int64_t>(up(kv, 512), std::max<int64_t>(16384 / units, 1)));
+        int64_t splits = std::max(units >= kAtOnce / 2 ? 1 : up(kAtOnce, units), up(kv, 16384));
+        splits = std::min(splits, std::min<int64_t>(up(kv, kMinPart), std::max<int64_t>(16384 / units, 1)));
         r.splits[0] = (int32_t)std::max<int64_t>(std::min<int64_t>(splits, 256), 1);
-        r.min_chunk[0] = units >= kAtOnce ? 2048 : 512;  // a shorter part costs more to begin than it saves
     }
     if (r.many) {
         const int64_t tiles = up(all, 32 * kWaves) > p.num_seqs ? up(all, 32 * kWaves) : p.num_seqs, units = tiles * p.H_kv;
-        int64_t splits = units >= kAtOnce ? 1 : up(kAtOnce, units);
-        if (splits > up(kv, 512)) splits = up(kv, 512);
+        // 128 tokens over 32000, 64 units: 84.8 us, with 256 at once 121 and with
+        // 1024 94.6.
+        int64_t splits = up(kAtOnce, units);
+        if (splits > up(kv, kMinPart)) splits = up(kv, kMinPart);
         r.splits[1] = (int32_t)(splits < 1 ? 1 : splits);
-        r.min_chunk[1] = 512;
     }
     auto take = [&](size_t bytes) {
         const size_t at = r.bytes;
@@ -1022,7 +1029,6 @@ hipError_t launch_cache_attention(const CacheAttentionLaunch& p, hipStream_t s) 
     a.tiled = pl.many;
     for (int c = 0; c < 2; ++c) {
         a.splits[c] = pl.splits[c];
-        a.min_chunk[c] = pl.min_chunk[c];
         a.ws_o[c] = reinterpret_cast<float*>(static_cast<char*>(p.workspace) + pl.off[2 * c]);
         a.ws_ml[c] = reinterpret_cast<float*>(static_cast<char*>(p.workspace) + pl.off[2 * c + 1]);
     }
