@@ -85,8 +85,11 @@ class _On:
 _stream = torch._C._cuda_getCurrentRawStream
 
 
-def _bytes(t):
-    return t.numel() * t.element_size()
+def _space(t, device):
+    """Address and size of a caller's workspace."""
+    if t.get_device() != device or not t.is_contiguous():
+        raise ValueError("workspace must be contiguous and on the device of the call's first tensor")
+    return t.data_ptr(), t.numel() * t.element_size()
 
 
 def gdn_batch_tables_workspace_bytes(num_seqs: int, T_total: int) -> int:
@@ -120,7 +123,7 @@ def gdn_batch_tables(context_lens, new_lens, T_total: int, page_size: int, block
     cu, kv, slots, pos, own = torch.split_with_sizes(context_lens.new_empty(2 * n + 1 + 2 * T + need),
                                                      (n + 1, n, T, T, need))
     base = cu.data_ptr()
-    wp, wb = (own.data_ptr(), 4 * need) if workspace is None else (workspace.data_ptr(), _bytes(workspace))
+    wp, wb = (own.data_ptr(), 4 * need) if workspace is None else _space(workspace, dev)
     st = lib.gdn_batch_tables(cp, np, rp, n, T, page_size, table, num_rows, max_blocks, counts, ring, pages, state, base,
                               base + 4 * (n + 1), base + 4 * (2 * n + 1), base + 4 * (2 * n + 1 + T), wp, wb, _stream(dev))
     if st:
@@ -182,10 +185,12 @@ def gdn_cache_attention(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_l
     else:
         op = _take(o, "o", q.dtype, (T, H, dv), dev)
     if workspace is None:
-        need = lib.gdn_cache_attention_workspace_bytes(n, T, max_new, max_kv, page, max_blocks, H, hkv, dk, dv)
-        if need:
-            workspace = k_scale.new_empty((need + 3) // 4)  # fp32
-    wp, wb = (None, 0) if workspace is None else (workspace.data_ptr(), _bytes(workspace))
+        wp, wb = None, lib.gdn_cache_attention_workspace_bytes(n, T, max_new, max_kv, page, max_blocks, H, hkv, dk, dv)
+        if wb:
+            workspace = k_scale.new_empty((wb + 3) // 4)  # fp32
+            wp = workspace.data_ptr()
+    else:
+        wp, wb = _space(workspace, dev)
     st = lib.gdn_cache_attention(qp, kc, vc, ks, vs, table, rp, kv, cu, n, T, max_new, max_kv, pages, page, num_rows,
                                  max_blocks, dk ** -0.5 if scale is None else scale, op, H, hkv, dk, dv, dt, wp, wb,
                                  _stream(dev))

@@ -643,6 +643,11 @@ def test_binding_refusals():
     long = torch.zeros((1, 2000), dtype=torch.int32, device="cuda")
     with pytest.raises(gdn.GdnError):
         gdn.gdn_cache_attention(q, kc, vc, ks, vs, long, kv_lens, i32([0, 1]), workspace=torch.empty(16, device="cuda"))
+    for bad in (torch.empty(1 << 20), torch.empty((2048, 512), device="cuda").t()):  # not on the device; not in one piece
+        with pytest.raises(ValueError):
+            gdn.gdn_cache_attention(q, kc, vc, ks, vs, long, kv_lens, i32([0, 1]), workspace=bad)
+        with pytest.raises(ValueError):
+            gdn.gdn_batch_tables(i32([0]), i32([1]), 1, 64, long, i32([0]), i32([0]), i32([0, 1, 0]), workspace=bad)
 
 
 def test_validation_mode(monkeypatch):
