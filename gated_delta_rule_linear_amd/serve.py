@@ -64,7 +64,7 @@ def _device_of(t, name):
 
 def _elsewhere(device, stream):
     """Whether a call has to change the current device or stream first."""
-    return stream is not None or device != torch.cuda.current_device()
+    return stream is not None or device != _current_device()
 
 
 class _On:
@@ -83,6 +83,7 @@ class _On:
 
 
 _stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice  # of a process that has device tensors
 
 
 def _space(t, device):
@@ -180,7 +181,7 @@ def gdn_cache_attention(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_l
     rp = None if rows is None else _take(rows, "rows", i32, (n,), dev)
     kv, cu = _take(kv_lens, "kv_lens", i32, (n,), dev), _take(cu_seqlens, "cu_seqlens", i32, (n + 1,), dev)
     if o is None:
-        o = q.new_empty((T, H, dv))
+        o = torch.empty_like(q) if dv == dk else q.new_empty((T, H, dv))
         op = o.data_ptr()
     else:
         op = _take(o, "o", q.dtype, (T, H, dv), dev)
@@ -219,7 +220,7 @@ def gdn_decode_pool(q, k, v, g, beta, states, slots, cu_seqlens=None, commit=Non
     cp = None if cu_seqlens is None else _take(cu_seqlens, "cu_seqlens", i32, (n + 1,), dev)
     mp = None if commit is None else _take(commit, "commit", i32, (n,), dev)
     if o is None:
-        o = v.new_empty((T, H, dv))
+        o = torch.empty_like(v)
         op = o.data_ptr()
     else:
         op = _take(o, "o", q.dtype, (T, H, dv), dev)
