@@ -365,6 +365,29 @@ def test_attention_scale(scale):
     _attention_check(ref.Server([150, 20], 64, 2, 64, 64, seed=1), [1, 20], 4, torch.float32, scale=scale)
 
 
+@pytest.mark.parametrize("max_kv", [0, 40000])
+def test_attention_one_long_request_among_many(max_kv):
+    # enough workgroups without parts, and one cache of several parts beside short ones
+    log(f"attention: 40000 tokens beside 35 short requests, max_kv={max_kv}")
+    kv = [1 + 7 * i for i in range(35)] + [40000]
+    _attention_check(ref.Server(kv, 256, 8, 64, 64, seed=19), [1] * 36, 8, torch.bfloat16, max_new=1, max_kv=max_kv)
+
+
+def test_attention_of_nothing():
+    # no tokens, no requests, no pages, no table: rows that are there are 0
+    def call(T, n, pages, rows, blocks, cu):
+        kc = torch.zeros((pages, 2, 64, 64), dtype=torch.uint8, device="cuda").view(ref.E4M3)
+        vc = torch.zeros((pages, 2, 4, 64, 16), dtype=torch.uint8, device="cuda").view(ref.E4M3)
+        ks, vs = (torch.ones((pages, 2), device="cuda") for _ in range(2))
+        table = torch.zeros((rows, blocks), dtype=torch.int32, device="cuda")
+        return gdn.gdn_cache_attention(torch.ones((T, 4, 64), device="cuda"), kc, vc, ks, vs, table, i32([7] * n), i32(cu))
+
+    assert call(0, 0, 2, 1, 1, [0]).shape == (0, 4, 64)
+    assert call(0, 2, 2, 2, 1, [0, 0, 0]).shape == (0, 4, 64)
+    for T, pages, rows, blocks in ((1, 0, 1, 1), (40, 0, 1, 1), (1, 2, 0, 1), (40, 2, 0, 1), (1, 2, 1, 0), (40, 2, 1, 0)):
+        assert torch.count_nonzero(call(T, 1, pages, rows, blocks, [0, T])) == 0
+
+
 def test_attention_many_requests():
     r = np.random.RandomState(0)
     kv = [int(x) for x in r.randint(0, 200, 300)]
@@ -438,6 +461,23 @@ def test_pool_many_tokens():
     # longer than a server's steps: the same recurrence
     args = _pool_inputs([200, 33], 2, 1, 64, 64, torch.float32, True, [1, 0], 0, 7, False)
     _pool_check(args, [1, 0], [0, 200, 233], [150, 33], 1e-6)
+
+
+def test_pool_and_write_of_nothing():
+    f = torch.ones
+    q, v, g, b = (f((2, 2, 64), device="cuda") for _ in range(4))
+    states, kept = (f((1, 2, 64, 64), device="cuda") for _ in range(2))
+    o = torch.full((2, 2, 64), 7.0, device="cuda")
+    gdn.gdn_decode_pool(q, q, v, -g, b[:, :, 0].contiguous(), states, i32([-1, 5]), o=o)  # no such states
+    gdn.gdn_decode_pool(q, q, v, -g, b[:, :, 0].contiguous(), states[:0], i32([0, 0]), o=o)
+    gdn.gdn_decode_pool(q[:0], q[:0], v[:0], -g[:0], b[:0, :, 0].contiguous(), states, i32([0]), cu_seqlens=i32([0, 0]))
+    gdn.gdn_decode_pool(q, q, v, -g, b[:, :, 0].contiguous(), states, i32([0]), cu_seqlens=i32([0, 0]), o=o)
+    assert torch.equal(states, kept) and torch.all(o == 7.0)
+    cache = _pool_of_pages(torch.Generator().manual_seed(1), 2, 2, 64, 64, 64)
+    before = [t.clone() for t in cache]
+    gdn.gdn_cache_write(q[:0], v[:0], i32([]), *cache)
+    gdn.gdn_cache_write(q, v, i32([0, 1]), *(t[:0] for t in cache))
+    assert all(torch.equal(x.view(torch.uint8), y.view(torch.uint8)) for x, y in zip(cache, before))
 
 
 def test_pool_equals_decode():
