@@ -56,8 +56,12 @@ struct Attention {
     int32_t few_rows;
     int32_t splits[2];
     bool tiled;  // the others go to the tile kernel
+    // The tile kernel's tiles of rows for each key/value head, and those of them,
+    // the first, whose cache is cut into parts.
+    int32_t tiles, tail;
     // Parts before they are joined, [part][row][d_v] and [part][row][2] (maximum
-    // and sum).  Rows: for few, (n * Hkv + h) * few_rows + row; else those of q.
+    // and sum).  Rows: for few, (n * Hkv + h) * few_rows + row; else the first of q.
+    int64_t part_rows[2];
     float *ws_o[2], *ws_ml[2];
 };
 
@@ -112,10 +116,6 @@ __device__ __forceinline__ int64_t part_row(const Attention& a, const Request& q
                                             int64_t orow) {
     return q.few ? ((int64_t)n * a.Hkv + h) * a.few_rows + row : orow;
 }
-__device__ __forceinline__ int64_t part_rows(const Attention& a, bool few) {
-    return few ? (int64_t)a.num_seqs * a.Hkv * a.few_rows : a.T * a.H;
-}
-
 // Pages and scales of 64 tiles, `step` tokens apart, a lane for each: fetched
 // ahead in one go, since a load in the tiles' loop whose result is needed at
 // once would wait for every load before it, the keys and values among them.
@@ -422,7 +422,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_rows_kernel(Attentio
                 store4(static_cast<TI*>(a.o) + orow * DV + c0 + k,
                        floatx4{out[k] * inv, out[k + 1] * inv, out[k + 2] * inv, out[k + 3] * inv});
         } else {
-            const int64_t prow = blockIdx.z * part_rows(a, true) + part_row(a, job, n, h, row0 + jr, orow);
+            const int64_t prow = blockIdx.z * a.part_rows[0] + part_row(a, job, n, h, row0 + jr, orow);
 #pragma unroll
             for (int k = 0; k < C; k += 4)
                 *reinterpret_cast<floatx4*>(a.ws_o[0] + prow * DV + c0 + k) = floatx4{out[k], out[k + 1], out[k + 2], out[k + 3]};
@@ -481,18 +481,19 @@ __global__ __launch_bounds__(64 * kWaves, sizeof(TI) == 4 ? 1 : 2) void attentio
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), c = lane & 31, hf = lane >> 5;
     // Key/value heads are neighbours in the grid: workgroups go to the eight XCDs in
     // turn, so with eight heads the tiles of a head share one XCD's cache.  The
-    // last rows, which see most, come first.
+    // last rows, which see most, come first, and the parts of the first last.
     const int h = blockIdx.x % a.Hkv;
-    const int64_t id = blockIdx.x / a.Hkv, tiles = gridDim.x / a.Hkv;
-    const int64_t rtile = tiles - 1 - id;
+    const int32_t id = blockIdx.x / a.Hkv, over = id - a.tiles, part = over < 0 ? 0 : 1 + over / a.tail;
+    const int32_t rtile = over < 0 ? a.tiles - 1 - id : a.tail - 1 - over % a.tail;
     const int32_t n = request_of(a, rtile, BR);
     if (n < 0) return;
-    const Request job(a, n);
+    Request job(a, n);
+    if (rtile >= a.tail) job.chunk = job.kv;
     const int64_t row0_ = (rtile - first_tile(a, n, BR)) * BR;
     if (job.few || row0_ < 0 || row0_ >= job.rows) return;
     const int32_t row0 = (int32_t)row0_, last_row = (row0 + BR < job.rows ? row0 + BR : job.rows) - 1;
-    const int64_t from = blockIdx.y * job.chunk;
-    if (blockIdx.y > 0 && from >= job.kv) return;
+    const int64_t from = part * job.chunk;
+    if (part > 0 && from >= job.kv) return;
     const int32_t* const table = table_of(a, n);
     int64_t to = job.kv - job.len + last_row / a.G + 1;  // no row of the tile sees more
     to = !table ? from : to < from + job.chunk ? to : from + job.chunk;
@@ -821,7 +822,8 @@ __global__ __launch_bounds__(64 * kWaves, sizeof(TI) == 4 ? 1 : 2) void attentio
     if (!live) return;
     const bool alone = job.alone();
     const float inv = !alone ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
-    const int64_t prow = blockIdx.y * part_rows(a, false) + orow;
+    if (!alone && orow >= a.part_rows[1]) return;  // (with offsets that are no offsets)
+    const int64_t prow = part * a.part_rows[1] + orow;
 #pragma unroll
     for (int d = 0; d < DT; ++d)
 #pragma unroll
@@ -850,7 +852,7 @@ __global__ __launch_bounds__(256) void attention_join_kernel(Attention a) {
     const int64_t r = (int64_t)blockIdx.x * ROWS + wave / W;
     int32_t n = -1;
     int64_t orow = r;
-    bool mine = r < part_rows(a, FEW);
+    bool mine = r < a.part_rows[FEW ? 0 : 1];
     if (FEW) {
         n = (int32_t)(r / ((int64_t)a.Hkv * a.few_rows));
     } else if (mine) {
@@ -868,10 +870,12 @@ __global__ __launch_bounds__(256) void attention_join_kernel(Attention a) {
             const int32_t row = (int32_t)(r % a.few_rows), h = (int32_t)(r / a.few_rows % a.Hkv), i = row / a.G;
             if (row >= q.rows) parts = 0;
             orow = (q.t0 + i) * a.H + h * a.G + (row - i * a.G);
+        } else if (first_tile(a, n, 32 * kWaves) + ((r / a.H - q.t0) * a.G + r % a.H % a.G) / (32 * kWaves) >= a.tail) {
+            parts = 0;
         }
     }
     if (W == kWaves && parts == 0) return;  // the whole workgroup
-    const int64_t step = part_rows(a, FEW);
+    const int64_t step = a.part_rows[FEW ? 0 : 1];
     const float *ml = a.ws_ml[FEW ? 0 : 1], *wo = a.ws_o[FEW ? 0 : 1];
     float m = -kInf;
     for (int s = thread; s < parts; s += 64 * W) m = fmaxf(m, ml[2 * (s * step + r)]);
@@ -909,16 +913,18 @@ __global__ __launch_bounds__(256) void attention_join_kernel(Attention a) {
 // ---------------------------------------------------------------- planning
 
 constexpr int64_t kAtOnce = 512;  // workgroups that the device holds: two on each compute unit
+constexpr int64_t kTailCache = 2048;  // tokens in front of a call's last tiles, from which on they are cut
 
 struct Plan {
     bool few, many;  // kernels that the call needs
-    int32_t few_rows, splits[2];
+    int32_t few_rows, splits[2], tiles, tail;
+    int64_t part_rows[2];
     size_t off[4], bytes;  // ws_o and ws_ml of few, of the others
 };
 
 // The lengths are on the device, so the plan goes by sizes and bounds.  A
 // request has at most max_new (or T_total) new tokens: whether that is few rows
-// decides which kernels run.  Each request's cache is cut into at most `splits`
+// decides which kernels run.  A request's cache is cut into at most `splits`
 // parts of at least kMinPart tokens, so that there are enough workgroups when
 // every request is as long as the bound, and so that the lengths, which may
 // differ much, do not leave the device waiting for a few long parts.
@@ -947,14 +953,25 @@ Plan plan(const CacheAttentionLaunch& p) {
         int64_t splits = std::max(units >= kAtOnce / 2 ? 1 : up(kAtOnce, units), up(kv, 16384));
         splits = std::min(splits, std::min<int64_t>(up(kv, kMinPart), std::max<int64_t>(16384 / units, 1)));
         r.splits[0] = (int32_t)std::max<int64_t>(std::min<int64_t>(splits, 256), 1);
+        r.part_rows[0] = (int64_t)p.num_seqs * p.H_kv * r.few_rows;
     }
     if (r.many) {
-        const int64_t tiles = up(all, 32 * kWaves) > p.num_seqs ? up(all, 32 * kWaves) : p.num_seqs, units = tiles * p.H_kv;
-        // 128 tokens over 32000, 64 units: 84.8 us, with 256 at once 121 and with
-        // 1024 94.6.
-        int64_t splits = up(kAtOnce, units);
-        if (splits > up(kv, kMinPart)) splits = up(kv, kMinPart);
-        r.splits[1] = (int32_t)(splits < 1 ? 1 : splits);
+        // With fewer tiles than the device holds, all are cut (128 tokens over 32000,
+        // 64 units: 83 us, with 256 at once 121 and with 1024 94.6).  Else the last
+        // that start, where they would leave the device more than half empty and
+        // each has a long cache before it.  2,100 tokens, 536 units, over 1024: 89.2 us
+        // uncut, 92.6 cut; over 2048 134.8 and 125.1; over 8192, 176 units past 512
+        // 442 and 432, 240 past it 458 and 471.
+        constexpr int32_t BR = 32 * kWaves;
+        r.tiles = (int32_t)(all / BR + p.num_seqs);
+        const int64_t units = std::max<int64_t>(up(all, BR), p.num_seqs) * p.H_kv, rest = r.tiles * (int64_t)p.H_kv % kAtOnce;
+        if (units < kAtOnce) r.tail = r.tiles;
+        else if (rest <= kAtOnce * 3 / 8 && kv - most / G >= kTailCache) r.tail = (int32_t)up(rest, p.H_kv);
+        const int64_t cut = std::min(up(kAtOnce, units < kAtOnce ? units : std::max<int64_t>(rest, 1)), up(kv, kMinPart));
+        if (r.tail > 0) r.splits[1] = (int32_t)std::max<int64_t>(cut, 1);
+        if (r.splits[1] == 1) r.tail = 0;
+        // Rows of the first `tail` tiles are among the first (tail + 1) * BR: see first_tile.
+        r.part_rows[1] = std::min(p.T_total, up((int64_t)(r.tail + 1) * BR, G)) * p.H;
     }
     auto take = [&](size_t bytes) {
         const size_t at = r.bytes;
@@ -963,7 +980,7 @@ Plan plan(const CacheAttentionLaunch& p) {
     };
     for (int c = 0; c < 2; ++c)
         if (r.splits[c] > 1) {
-            const size_t rows = (size_t)r.splits[c] * (c == 0 ? (size_t)p.num_seqs * p.H_kv * r.few_rows : (size_t)p.T_total * p.H);
+            const size_t rows = (size_t)r.splits[c] * (size_t)r.part_rows[c];
             r.off[2 * c] = take(rows * p.dv * sizeof(float));
             r.off[2 * c + 1] = take(rows * 2 * sizeof(float));
         }
@@ -974,9 +991,8 @@ template <typename TI, int DK, int DV>
 hipError_t run(const Attention& a, const Plan& pl, hipStream_t s) {
     hipError_t e = hipSuccess;
     if (pl.many) {
-        const int64_t tiles = a.T * a.G / (32 * kWaves) + a.num_seqs;
-        hipLaunchKernelGGL((attention_tile_kernel<TI, DK, DV>), dim3((unsigned)(tiles * a.Hkv), (unsigned)a.splits[1]),
-                           dim3(64 * kWaves), 0, s, a);
+        const int64_t tiles = a.tiles + (int64_t)a.tail * (a.splits[1] - 1);
+        hipLaunchKernelGGL((attention_tile_kernel<TI, DK, DV>), dim3((unsigned)(tiles * a.Hkv)), dim3(64 * kWaves), 0, s, a);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     if (pl.few) {
@@ -985,7 +1001,7 @@ hipError_t run(const Attention& a, const Plan& pl, hipStream_t s) {
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     if (a.splits[0] > 1) {
-        const int64_t rows = (int64_t)a.num_seqs * a.Hkv * a.few_rows;
+        const int64_t rows = a.part_rows[0];
         if (a.splits[0] > 16)
             hipLaunchKernelGGL((attention_join_kernel<TI, DV, true, kWaves>), dim3((unsigned)rows), dim3(256), 0, s, a);
         else
@@ -994,7 +1010,7 @@ hipError_t run(const Attention& a, const Plan& pl, hipStream_t s) {
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     if (a.splits[1] > 1) {
-        const int64_t rows = a.T * a.H;
+        const int64_t rows = a.part_rows[1];
         hipLaunchKernelGGL((attention_join_kernel<TI, DV, false, 1>), dim3((unsigned)((rows + kWaves - 1) / kWaves)), dim3(256), 0, s, a);
         e = hipGetLastError();
     }
@@ -1027,8 +1043,11 @@ hipError_t launch_cache_attention(const CacheAttentionLaunch& p, hipStream_t s) 
     a.o = p.o; a.H = p.H; a.Hkv = p.H_kv; a.G = p.H / p.H_kv;
     a.few_rows = pl.few_rows;
     a.tiled = pl.many;
+    a.tiles = pl.tiles;
+    a.tail = pl.tail;
     for (int c = 0; c < 2; ++c) {
         a.splits[c] = pl.splits[c];
+        a.part_rows[c] = pl.part_rows[c];
         a.ws_o[c] = reinterpret_cast<float*>(static_cast<char*>(p.workspace) + pl.off[2 * c]);
         a.ws_ml[c] = reinterpret_cast<float*>(static_cast<char*>(p.workspace) + pl.off[2 * c + 1]);
     }

@@ -299,6 +299,30 @@ def test_attention_prompts(lens, kv, dtype, dk, dv):
     _attention_check(ref.Server(kv, 64, 2, dk, dv, seed=kv[0]), lens, 8, dtype, max_new=max(lens), max_kv=max(kv))
 
 
+@pytest.mark.parametrize("lens,kv,hints", [
+    ([1027], [4000], {}), ([500, 1, 530, 3], [3100, 5000, 3700, 40], dict(max_new=530, max_kv=5000)),
+    # few held tokens in front of them, and none
+    ([1027], [4000], dict(max_new=1027, max_kv=1027)), ([1040], [1040], dict(max_new=1, max_kv=9000))])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_attention_last_tiles_in_parts(lens, kv, hints, dtype):
+    # a few more tiles of rows than the device holds at once, over a long cache
+    log(f"attention: last tiles in parts new={lens} kv={kv} {hints} {dtype}")
+    _attention_check(ref.Server(kv, 64, 16, 64, 64, seed=23), lens, 64, dtype, T_extra=3, **hints)
+
+
+def test_attention_last_tiles_with_offsets_that_are_none():
+    # offsets that start below 0 or decrease: nothing outside o is written, and the workspace is enough
+    s = ref.Server([4000, 300], 64, 16, 64, 64, seed=23)
+    kc, vc, ks, vs, table, kv_lens, _ = s.to("cuda")
+    q = torch.randn((1030, 64, 64)).bfloat16().cuda()
+    need = gdn.gdn_cache_attention_workspace_bytes(2, 1030, 0, 0, 64, table.shape[1], 64, 16, 64, 64)
+    for cu in ([-5000, 1030, 1030], [0, 1030, 7], [900, 20, 1030], [-3, 10 ** 9, -7], [2000, 2000, 2000]):
+        ws = torch.full((need + 4096,), 77, dtype=torch.uint8, device="cuda")
+        room = torch.full((1030 + 64, 64, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+        gdn.gdn_cache_attention(q, kc, vc, ks, vs, table, kv_lens, i32(cu), o=room[:1030], workspace=ws[:need])
+        assert torch.all(ws[need:] == 77) and torch.all(room[1030:] == 7.0)
+
+
 @pytest.mark.parametrize("lens,kv,hints", [([2, 1, 70, 0], [9000, 5, 300, 7], dict(max_new=1, max_kv=64)),
                                            ([2, 3], [9000, 40000], dict(max_new=1)),
                                            ([1, 1], [9000, 40000], dict(max_new=500)),
