@@ -111,11 +111,7 @@ __device__ __forceinline__ const int32_t* table_of(const Attention& a, int32_t n
     const int32_t row = a.rows ? a.rows[n] : n;
     return row >= 0 && row < a.num_rows && a.num_pages > 0 ? a.table + (int64_t)row * a.max_blocks : nullptr;
 }
-// Where row `row` of request n and head h stands among the rows of parts.
-__device__ __forceinline__ int64_t part_row(const Attention& a, const Request& q, int32_t n, int32_t h, int32_t row,
-                                            int64_t orow) {
-    return q.few ? ((int64_t)n * a.Hkv + h) * a.few_rows + row : orow;
-}
+
 // Pages and scales of 64 tiles, `step` tokens apart, a lane for each: fetched
 // ahead in one go, since a load in the tiles' loop whose result is needed at
 // once would wait for every load before it, the keys and values among them.
@@ -422,7 +418,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_rows_kernel(Attentio
                 store4(static_cast<TI*>(a.o) + orow * DV + c0 + k,
                        floatx4{out[k] * inv, out[k + 1] * inv, out[k + 2] * inv, out[k + 3] * inv});
         } else {
-            const int64_t prow = blockIdx.z * a.part_rows[0] + part_row(a, job, n, h, row0 + jr, orow);
+            const int64_t prow = blockIdx.z * a.part_rows[0] + ((int64_t)n * a.Hkv + h) * a.few_rows + row0 + jr;
 #pragma unroll
             for (int k = 0; k < C; k += 4)
                 *reinterpret_cast<floatx4*>(a.ws_o[0] + prow * DV + c0 + k) = floatx4{out[k], out[k + 1], out[k + 2], out[k + 3]};
@@ -464,7 +460,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_rows_kernel(Attentio
 // rounding.
 //
 // Bound by the matrix cores and the power they draw: 1.05 PFLOP/s over two
-// prompts of 8192 tokens (32 heads, 8 for keys, 128 channels), where a plain
+// prompts of 8192 tokens (32 heads, 8 for keys, 128 channels), 1.07 over chunks
+// of 1021 to 2048 tokens behind 16384, where a plain
 // product of 8192 x 8192 matrices reaches 1.24; with 64 channels, where a tile's
 // products are half and its exponentials the same, 0.85.  In full precision
 // (three products for one) 0.36.
