@@ -8,8 +8,9 @@
 // running maximum and sum of the softmax.  Requests with few rows (decode,
 // verifying drafted tokens) go to attention_rows_kernel, which is bound by
 // reading the cache; the others to attention_tile_kernel, which is bound by the
-// matrix cores.  Where rows are few in all, a request's cache is cut into parts
-// that workgroups take side by side and attention_join_kernel joins.
+// matrix cores.  Where rows are few in all, and for the last of many, a request's
+// cache is cut into parts that workgroups take side by side and
+// attention_join_kernel joins.
 //
 // Scores are formed transposed, S^T = K Q^T, so that a lane holds scores of one
 // row and the softmax statistics of a row are scalars of its lanes, and so that

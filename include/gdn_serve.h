@@ -13,10 +13,10 @@
  * reported before any memory is touched, no allocation, no state kept between
  * calls, calls on different streams independent of each other, every call
  * capturable into a graph (GDN_VALIDATE=1 aside, which waits for the stream).
- * Contents of index arrays are checked in the
- * kernels where a bad value could address memory outside the arrays given, as
- * stated at each call.  Floating inputs with NaN or Inf are not masked: they
- * propagate, and only where the definition lets them.
+ * Contents of index arrays are checked in the kernels where a bad value could
+ * address memory outside the arrays given, as stated at each call.  Floating
+ * inputs with NaN or Inf are not masked: they propagate, and only where the
+ * definition lets them.
  *
  * The paged cache.  A page holds page_size consecutive tokens of one request
  * for every key/value head:
@@ -76,14 +76,14 @@ extern "C" {
  * Pages are taken from the ring's start in the order of the requests and pages
  * that come back go to its end, so the result does not depend on timing.  A
  * request needs the pages behind those it owns up to the block of its last new
- * token; it is refused, and gets nothing, when its need and the
- * need of the requests before it do not fit in the free pages, when its row
- * has no room (max_blocks), when it owns fewer pages than context_lens needs,
- * or when rows[n] is outside [0, num_rows).  A refused request keeps its pages and its kv_lens entry is context_lens[n]; its
- * tokens stay in cu_seqlens.  Pages given back in a call are free for the next
- * call.  Calling again with the same lengths changes nothing.  A call reads and
- * updates the tables and the ring: calls on the same ones are ordered by the
- * caller, as on one stream.
+ * token; it is refused, and gets nothing, when its need and the need of the
+ * requests before it do not fit in the free pages, when its row has no room
+ * (max_blocks), when it owns fewer pages than context_lens needs, or when
+ * rows[n] is outside [0, num_rows).  A refused request keeps its pages and its
+ * kv_lens entry is context_lens[n]; its tokens stay in cu_seqlens.  Pages given
+ * back in a call are free for the next call.  Calling again with the same
+ * lengths changes nothing.  A call reads and updates the tables and the ring:
+ * calls on the same ones are ordered by the caller, as on one stream.
  * GDN_VALIDATE=1 copies the lengths, the rows, the counts and the ring to the
  * host and returns GDN_ERR_DOMAIN for negative context_lens, rows that repeat
  * or lie outside, and a ring that does not fit its array. */
@@ -155,8 +155,8 @@ int32_t gdn_cache_write(const void* k, const void* v, const int32_t* slots, int6
  * fp32 accumulation, softmax in fp32, p rounded to bf16 for the second
  * product.  GDN_F32: q and p are split into three bf16 parts, whose products
  * with the codes are exact, so that the arithmetic is fp32's.
- * A long cache with few rows is cut into parts computed side by side and
- * joined by a second launch. */
+ * The cache of few rows, or of the last of many, may be cut into parts computed
+ * side by side and joined by another launch. */
 int32_t gdn_cache_attention(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
                             const float* v_scale, const int32_t* block_table, const int32_t* rows,
                             const int32_t* kv_lens, const int32_t* cu_seqlens, int32_t num_seqs, int64_t T_total,
