@@ -643,7 +643,9 @@ __global__ __launch_bounds__(64 * kWaves, sizeof(TI) == 4 ? 1 : 2) void attentio
     auto rescale = [&]() {
         if (__ballot(mx > ref + kSlack || (ref == 0.f && sum == 0.f))) {
             const float now = mx == -kInf ? 0.f : mx;
-            const float fade = sum == 0.f ? 1.f : __builtin_amdgcn_exp2f(ref - now);
+            // (At most 1: a row without a score yet has ref 0, whatever its maximum.
+            // `sum` says nothing of that: it is of this lane's tokens, O of the row's.)
+            const float fade = fminf(__builtin_amdgcn_exp2f(ref - now), 1.f);
             ref = now;
             sum *= fade;
 #pragma unroll

@@ -384,6 +384,24 @@ def test_attention_nan(dtype, lens):
     assert torch.equal(torch.isnan(o).cpu(), want)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("dk,dv", [(64, 64), (128, 128)])
+@pytest.mark.parametrize("kv,rise", [(200, 1), (200, 2), (700, 1), (700, 4), (3000, 1), (3000, 3)])
+def test_attention_far_apart_scores(dtype, dk, dv, kv, rise):
+    # Up to tile `rise` of 64 tokens, scores of every other 16 tokens are so far below the others' that their
+    # exponentials are 0 (they are all the tokens that one lane has of a row); then the maximum rises, once.
+    log(f"attention: scores far apart kv={kv} rise={rise} {dtype} dk={dk} dv={dv}")
+    s = ref.Server([kv], 64, 1, dk, dv, seed=kv)
+    s.ks[:] = 1.0
+    k = torch.zeros((s.k.shape[0], 1, 64, dk))
+    low = (torch.arange(64) // 16) % 2 == 1
+    for b, page in enumerate(s.table[0, :-(-kv // 64)].tolist()):
+        k[page, 0, :, 0] = torch.where(low, -448.0, 0.0) if b < rise else 8.0   # rows with q0 > 0
+        k[page, 0, :, 1] = torch.where(low, 0.0, -448.0) if b < rise else 8.0   # q1 > 0: the other 16 tokens
+    s.k = k.to(ref.E4M3)
+    _attention_check(s, [60], 4, dtype, scale=1.0)
+
+
 @pytest.mark.parametrize("scale", [0.0, -0.3, 4.0])
 def test_attention_scale(scale):
     _attention_check(ref.Server([150, 20], 64, 2, 64, 64, seed=1), [1, 20], 4, torch.float32, scale=scale)
