@@ -113,14 +113,22 @@ __device__ __forceinline__ const int32_t* table_of(const Attention& a, int32_t n
     return row >= 0 && row < a.num_rows && a.num_pages > 0 ? a.table + (int64_t)row * a.max_blocks : nullptr;
 }
 
+// The lane's number where it is needed: what is made of threadIdx.x is kept in
+// registers from the kernel's start, through loops that need them all.
+__device__ __forceinline__ int late_lane() {
+    uint32_t all = ~0u;
+    asm volatile("" : "+s"(all));
+    return (int)__builtin_amdgcn_mbcnt_hi(all, __builtin_amdgcn_mbcnt_lo(all, 0));
+}
+
 // Pages and scales of 64 tiles, `step` tokens apart, a lane for each: fetched
 // ahead in one go, since a load in the tiles' loop whose result is needed at
 // once would wait for every load before it, the keys and values among them.
 struct Pages {
     int32_t page;  // -1: left out
     float ks, vs;
-    __device__ __forceinline__ void fetch(const Attention& a, const int32_t* table, int32_t h, int64_t base, int64_t to, int step) {
-        const int64_t at = base + (int64_t)(threadIdx.x & 63) * step;
+    __device__ __forceinline__ void fetch(const Attention& a, const int32_t* table, int32_t h, int64_t base, int64_t to, int step, int lane) {
+        const int64_t at = base + (int64_t)lane * step;
         page = table && at < to ? table[at >> a.page_log2] : -1;
         if (page >= a.num_pages) page = -1;
         ks = vs = 0.f;
@@ -134,6 +142,32 @@ struct Pages {
         return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), i));
     }
 };
+
+// Whether a row that sees the tokens up to `sees` sees one of the tiles at base,
+// base + step, ... below `to`: some of them may have no page.  For rows whose
+// maximum is -Inf: without a token their output is 0, with scores that are all
+// -Inf it is NaN.
+__device__ __forceinline__ bool sees_some(const Attention& a, const int32_t* table, int64_t base, int64_t to, int step,
+                                          int64_t sees) {
+    const int lane = late_lane();
+    for (; base < to; base += 64 * (int64_t)step) {
+        const int64_t at = base + (int64_t)lane * step;
+        const int32_t page = table && at < to ? table[at >> a.page_log2] : -1;
+        const uint64_t there = __ballot(page >= 0 && page < a.num_pages);
+        if (there) return base + (__ffsll((unsigned long long)there) - 1) * (int64_t)step <= sees;
+    }
+    return false;
+}
+// Statistics of a part of a row are joined with those of the others by this
+// factor, `all` the largest maximum.  Parts whose scores are all -Inf have a sum
+// above 0, those without a token 0, and the factor keeps that apart: 1, where
+// the exponential's argument is no number.
+__device__ __forceinline__ float joined(float part, float all) {
+    return part == all ? 1.f : __builtin_amdgcn_exp2f(part - all);
+}
+__device__ __forceinline__ float reciprocal_sum(float sum, float top) {
+    return sum == 0.f ? 0.f : top == -kInf ? __builtin_nanf("") : 1.f / sum;
+}
 
 // A value split into NS bf16 parts: one rounds it, three hold all of an fp32.
 template <int NS>
@@ -259,7 +293,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_rows_kernel(Attentio
     constexpr int STEP = kWaves * kTile;
     const int64_t first = from + wave * kTile;
     Pages pages;
-    pages.fetch(a, table, h, first, to, STEP);
+    pages.fetch(a, table, h, first, to, STEP, late_lane());
     int at = 0;  // the tile's lane of `pages`
     int32_t page = __builtin_amdgcn_readlane(pages.page, 0);
     float ks = Pages::lane_of(pages.ks, 0), vs = Pages::lane_of(pages.vs, 0);
@@ -306,7 +340,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_rows_kernel(Attentio
         }
         asm volatile("" ::: "memory");  // (and the next tile's writes behind them)
         if (++at == 64) {
-            pages.fetch(a, table, h, base + STEP, to, STEP);
+            pages.fetch(a, table, h, base + STEP, to, STEP, late_lane());
             at = 0;
         }
         page = __builtin_amdgcn_readlane(pages.page, at);
@@ -395,25 +429,30 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_rows_kernel(Attentio
     // Join the waves: a thread takes DV / 16 channels of one row.
     constexpr int C = DV / 16;
     const int jr = threadIdx.x >> 4, c0 = (threadIdx.x & 15) * C;
-    if (row0 + jr < job.rows) {
-        float m = s_m[0][jr];
+    const int32_t ji = (row0 + jr) / a.G;
+    float m = s_m[0][jr], l = 0.f, f[kWaves];
 #pragma unroll
-        for (int w = 1; w < kWaves; ++w) m = fmaxf(m, s_m[w][jr]);
-        const float ref = m == -kInf ? 0.f : m;
-        float l = 0.f, out[C];
+    for (int w = 1; w < kWaves; ++w) m = fmaxf(m, s_m[w][jr]);
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+        f[w] = __builtin_amdgcn_exp2f(s_m[w][jr] - (m == -kInf ? 0.f : m));
+        l += f[w] * s_l[w][jr];
+    }
+    if (__ballot(row0 + jr < job.rows && m == -kInf)) {
+        const bool some = sees_some(a, table, from, to, kTile, job.kv - job.len + ji);
+        if (m == -kInf && some) l += 1.f;
+    }
+    if (row0 + jr < job.rows) {
+        float out[C];
 #pragma unroll
         for (int k = 0; k < C; ++k) out[k] = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) {
-            const float f = __builtin_amdgcn_exp2f(s_m[w][jr] - ref);
-            l += f * s_l[w][jr];
+        for (int w = 0; w < kWaves; ++w)
 #pragma unroll
-            for (int k = 0; k < C; ++k) out[k] += f * reinterpret_cast<const float(*)[DV + 4]>(s_wave[w])[jr][c0 + k];
-        }
-        const int32_t ji = (row0 + jr) / a.G;
+            for (int k = 0; k < C; ++k) out[k] += f[w] * reinterpret_cast<const float(*)[DV + 4]>(s_wave[w])[jr][c0 + k];
         const int64_t orow = (job.t0 + ji) * a.H + h * a.G + (row0 + jr - ji * a.G);
         if (job.alone()) {
-            const float inv = l == 0.f && m == -kInf ? 0.f : 1.f / l;
+            const float inv = reciprocal_sum(l, m);
 #pragma unroll
             for (int k = 0; k < C; k += 4)
                 store4(static_cast<TI*>(a.o) + orow * DV + c0 + k,
@@ -583,7 +622,7 @@ __global__ __launch_bounds__(64 * kWaves, sizeof(TI) == 4 ? 1 : 2) void attentio
     };
 
     if (count > 0) {
-        pages.fetch(a, table, h, from, to, kTile);
+        pages.fetch(a, table, h, from, to, kTile, lane);
         load_keys(0);
         load_values(0);
     }
@@ -713,7 +752,7 @@ __global__ __launch_bounds__(64 * kWaves, sizeof(TI) == 4 ? 1 : 2) void attentio
     };
     auto fetch_pages = [&](int32_t tile) {
         window = tile;
-        pages.fetch(a, table, h, from + (int64_t)window * kTile, to, kTile);
+        pages.fetch(a, table, h, from + (int64_t)window * kTile, to, kTile, lane);
     };
     // One tile that every row sees whole, as it sees the one after it: `now` holds
     // its scores, in the maximum already; `next` receives those of the tile after
@@ -819,9 +858,13 @@ __global__ __launch_bounds__(64 * kWaves, sizeof(TI) == 4 ? 1 : 2) void attentio
     }
     for (; tile < count; ++tile) last_step(tile, tile & 1);
     sum = across<Sum, 32>(sum);
+    if (__ballot(live && mx == -kInf)) {
+        const bool some = sees_some(a, table, from, to, kTile, from + sees);
+        if (mx == -kInf && some) sum += 1.f;
+    }
     if (!live) return;
     const bool alone = job.alone();
-    const float inv = !alone ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
+    const float inv = alone ? reciprocal_sum(sum, mx) : 1.f;
     if (!alone && orow >= a.part_rows[1]) return;  // (with offsets that are no offsets)
     const int64_t prow = part * a.part_rows[1] + orow;
 #pragma unroll
@@ -834,7 +877,7 @@ __global__ __launch_bounds__(64 * kWaves, sizeof(TI) == 4 ? 1 : 2) void attentio
             else *reinterpret_cast<floatx4*>(a.ws_o[1] + prow * DV + ch) = z;
         }
     if (!alone && hf == 0) {
-        a.ws_ml[1][2 * prow] = sum == 0.f ? -kInf : ref;
+        a.ws_ml[1][2 * prow] = mx == -kInf ? mx : ref;
         a.ws_ml[1][2 * prow + 1] = sum;
     }
 }
@@ -886,14 +929,13 @@ __device__ void join_rows(const Attention& a, int32_t block) {
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) m = fmaxf(m, s_m[w]);
     }
-    const float ref = m == -kInf ? 0.f : m;
     const int c = thread % L, s0 = thread / L, at0 = wave / W * STEP;
     float l = 0.f;
     floatx4 out = zero4();
 #pragma unroll 4
     for (int s = s0; s < parts; s += STEP) {
         const int64_t at = s * step + r;
-        const float f = __builtin_amdgcn_exp2f(ml[2 * at] - ref);
+        const float f = joined(ml[2 * at], m);
         l += f * ml[2 * at + 1];
         out += f * *reinterpret_cast<const floatx4*>(wo + at * DV + 4 * c);
     }
@@ -906,7 +948,7 @@ __device__ void join_rows(const Attention& a, int32_t block) {
         out += s_o[at0 + s][c];
         l += s_l[at0 + s];
     }
-    const float inv = l == 0.f && m == -kInf ? 0.f : 1.f / l;
+    const float inv = reciprocal_sum(l, m);
     store4(static_cast<TI*>(a.o) + orow * DV + 4 * c, out * inv);
 }
 // The requests of few rows, W waves to a row, and then the others: one launch,

@@ -144,7 +144,8 @@ int32_t gdn_cache_write(const void* k, const void* v, const int32_t* slots, int6
  * token's own position.  Tokens whose block table entry is outside
  * [0, num_pages) or whose row is outside [0, num_rows) are left out; a row that
  * sees no token (kv_lens 0, or more new tokens than kv_lens) is 0.  A NaN in a
- * key or value reaches only the rows that see its token.  Scales that are not
+ * key or value reaches only the rows that see its token; Inf in a query makes
+ * its row NaN, also where it makes all its scores -Inf.  Scales that are not
  * powers of two are not supported (they are exact factors of bf16 operands).
  * Two calls in flight at once need two workspaces.
  * GDN_VALIDATE=1 returns GDN_ERR_DOMAIN for offsets that decrease or end behind

@@ -402,6 +402,38 @@ def test_attention_far_apart_scores(dtype, dk, dv, kv, rise):
     _attention_check(s, [60], 4, dtype, scale=1.0)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("lens,kv,hints", [([1, 1, 1, 1], [3000, 70, 0, 64], {}), ([3, 1, 2, 1], [130, 70, 1, 64], {}),
+                                           ([70, 90, 1, 33], [3000, 90, 0, 1000], {}),
+                                           ([200, 40], [3000, 9000], dict(max_new=200, max_kv=9000))])
+def test_attention_infinite_queries(dtype, lens, kv, hints):
+    # Inf in a query: its scores are Inf, -Inf or both, and the row NaN, unless it sees no token; other rows are as ever
+    log(f"attention: Inf in queries new={lens} kv={kv} {dtype}")
+    s = ref.Server(kv, 64, 2, 64, 64, seed=sum(kv))
+    k = s.k.float()
+    k[..., 0] = k[..., 0].abs().clamp(min=1.0)  # of one sign
+    s.k = k.to(ref.E4M3)
+    s.table[0, 0] = -1
+    gen = torch.Generator().manual_seed(sum(lens))
+    T, H = sum(lens), 8
+    q = torch.randn((T, H, 64), generator=gen)
+    odd = torch.rand((T, H), generator=gen) < 0.5
+    ends = torch.tensor(np.cumsum(lens)) - 1
+    odd[ends, 0], odd[ends, 1], odd[ends, 2] = True, True, False
+    q[..., 0] = torch.where(odd, torch.where(torch.rand((T, H), generator=gen) < 0.7, -math.inf, math.inf), q[..., 0])
+    q[ends, 0, 0] = -math.inf
+    q = q.to(dtype).cuda()
+    want, mag, _ = s.reference(q.double(), lens, 0.125, "cuda")
+    kc, vc, ks, vs, tab, kv_lens, _ = s.to("cuda")
+    o = gdn.gdn_cache_attention(q, kc, vc, ks, vs, tab, kv_lens, i32([0] + list(np.cumsum(lens))), scale=0.125, **hints)
+    assert torch.equal(torch.isnan(o), torch.isnan(want))
+    assert torch.isnan(want).any() and not torch.isnan(want).all()
+    # the other rows: p and o rounded to bf16 (or 2^-24, with the sums' roundings), scores below 2^5 off by their sums
+    eps = EPS16 if dtype == torch.bfloat16 else EPS32 * (max(kv) + 64)
+    calm = ~odd.cuda()
+    assert ((o.double() - want).abs()[calm] <= (3 * eps + 2 * 200 * EPS32 * 2 ** 6) * (mag + want.abs())[calm] + 1e-30).all()
+
+
 @pytest.mark.parametrize("scale", [0.0, -0.3, 4.0])
 def test_attention_scale(scale):
     _attention_check(ref.Server([150, 20], 64, 2, 64, 64, seed=1), [1, 20], 4, torch.float32, scale=scale)
