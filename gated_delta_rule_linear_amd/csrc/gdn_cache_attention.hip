@@ -1008,15 +1008,25 @@ Plan plan(const CacheAttentionLaunch& p) {
         // With fewer tiles than the device holds, all are cut (128 tokens over 32000,
         // 64 units: 83 us, with 256 at once 121 and with 1024 94.6).  Else the last
         // that start, where they would leave the device more than half empty and
-        // each has a long cache before it.  2,100 tokens, 536 units, over 1024: 89.2 us
+        // each has a long cache before it.  2,100 tokens, 528 units, over 1024: 89.2 us
         // uncut, 92.6 cut; over 2048 134.8 and 125.1; over 8192, 176 units past 512
-        // 442 and 432, 240 past it 458 and 471.
+        // 442 and 432, 240 past it 458 and 471.  What is past a multiple of 512 goes by
+        // the tiles that have rows: of one request they are known; of more they are
+        // guessed, with the last tile of three requests out of four more than the full
+        // ones, since too few cost more than too many (4 requests of 900 to 1,200
+        // tokens over 8192, 24 units past 1024: 576 us with 24 or more cut, 653 with
+        // 16).  The grid's other tiles end at once.  (The cut
+        // tiles are the batch's first: behind requests of few rows, which have none,
+        // the tiles that end last stay whole.)  Parts of the cut tiles come nearest to 512 (96 units: 373 us in 5 parts, 381 in 6; 48: 337 in 10, 335 in
+        // 11).
         constexpr int32_t BR = 32 * kWaves;
         r.tiles = (int32_t)(all / BR + p.num_seqs);
-        const int64_t units = std::max<int64_t>(up(all, BR), p.num_seqs) * p.H_kv, rest = r.tiles * (int64_t)p.H_kv % kAtOnce;
+        const int64_t full = up(all, BR), units = std::max<int64_t>(full, p.num_seqs) * p.H_kv;
+        const int64_t rest = std::min<int64_t>(full + (int64_t)p.num_seqs * 3 / 4, r.tiles) * p.H_kv % kAtOnce;
         if (units < kAtOnce) r.tail = r.tiles;
         else if (rest <= kAtOnce * 3 / 8 && kv - most / G >= kTailCache) r.tail = (int32_t)up(rest, p.H_kv);
-        const int64_t cut = std::min(up(kAtOnce, units < kAtOnce ? units : std::max<int64_t>(rest, 1)), up(kv, kMinPart));
+        const int64_t share = std::max<int64_t>((int64_t)r.tail * p.H_kv, 1);
+        const int64_t cut = std::min(units < kAtOnce ? up(kAtOnce, units) : (kAtOnce + share / 2) / share, up(kv, kMinPart));
         if (r.tail > 0) r.splits[1] = (int32_t)std::max<int64_t>(cut, 1);
         if (r.splits[1] == 1) r.tail = 0;
         // Rows of the first `tail` tiles are among the first (tail + 1) * BR: see first_tile.

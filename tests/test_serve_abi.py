@@ -113,6 +113,33 @@ def test_workspace_sizes():
     assert size(1, 1, 0, 0, 64, 1024, 32, 8, 128, 128) == size(1, 1, 0, 65536, 64, 1024, 32, 8, 128, 128)
 
 
+def test_attention_workspace_of_last_tiles():
+    # Tiles past a multiple of 512 workgroups are cut into parts.  One request that is such a multiple has none.
+    size = gdn.gdn_cache_attention_workspace_bytes
+    for T in (2048, 4096, 8192):
+        for hint in (0, T):
+            assert size(1, T, hint, 32768, 64, 512, 32, 8, 128, 128) == 0
+            assert size(1, T + 1, hint, 32768, 64, 512, 32, 8, 128, 128) > 0
+    # heads that do not divide 512: 312 tiles of 36 heads are 21 x 512 + 480, 313 are 22 x 512 + 4
+    assert size(1, 4992, 0, 131072, 64, 2048, 288, 36, 128, 128) == 0
+    # one tile's 36 workgroups cut into 14 parts, of at most two tiles' 32 tokens
+    assert 0 < size(1, 5008, 0, 131072, 64, 2048, 288, 36, 128, 128) <= 14 * 32 * 288 * (128 + 2) * 4 + 512
+
+
+def test_attention_workspace_is_bounded():
+    # of few rows at most 16384 workgroups of 16 rows, of many at most 1024 of 128 and as many that they share a tile with
+    rng = np.random.RandomState(7)
+    most = (16384 * 16 + 2 * 1024 * 128) * (128 + 2) * 4 + 2048
+    for _ in range(20000):
+        hkv, G = int(rng.choice([1, 2, 3, 5, 8, 12, 16, 36, 40, 100, 300])), int(rng.choice([1, 2, 4, 7, 8, 16]))
+        n = int(2 ** rng.uniform(0, 9))
+        T = max(n, int(2 ** rng.uniform(0, 14)))
+        blocks = int(2 ** rng.uniform(0, 12))
+        hint = int(rng.choice([0, 1, 5, T // n, T]))
+        assert gdn.gdn_cache_attention_workspace_bytes(n, T, hint, 0, 64, blocks, hkv * G, hkv, 128, 128) <= most, \
+            (n, T, hint, blocks, hkv, G)
+
+
 def test_binding_refuses_host_tensors_and_wrong_shapes():
     k = torch.zeros(3, 2, 64)
     with pytest.raises(ValueError):
