@@ -1015,10 +1015,10 @@ Plan plan(const CacheAttentionLaunch& p) {
         // guessed, with the last tile of three requests out of four more than the full
         // ones, since too few cost more than too many (4 requests of 900 to 1,200
         // tokens over 8192, 24 units past 1024: 576 us with 24 or more cut, 653 with
-        // 16).  The grid's other tiles end at once.  (The cut
-        // tiles are the batch's first: behind requests of few rows, which have none,
-        // the tiles that end last stay whole.)  Parts of the cut tiles come nearest to 512 (96 units: 373 us in 5 parts, 381 in 6; 48: 337 in 10, 335 in
-        // 11).
+        // 16).  The grid's other tiles end at once.  (The cut tiles are the batch's
+        // first: behind requests of few rows, which have none, the tiles that end last
+        // stay whole.)  Parts of the cut tiles come nearest to 512 (96 units: 373 us in
+        // 5 parts, 381 in 6; 48: 337 in 10, 335 in 11).
         constexpr int32_t BR = 32 * kWaves;
         r.tiles = (int32_t)(all / BR + p.num_seqs);
         const int64_t full = up(all, BR), units = std::max<int64_t>(full, p.num_seqs) * p.H_kv;
