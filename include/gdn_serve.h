@@ -82,7 +82,9 @@ extern "C" {
  * rows[n] is outside [0, num_rows).  A refused request keeps its pages and its
  * kv_lens entry is context_lens[n]; its tokens stay in cu_seqlens.  Pages given
  * back in a call are free for the next call.  Calling again with the same
- * lengths changes nothing.  A call reads and updates the tables and the ring:
+ * lengths changes nothing, unless a request was refused (free_state[2]): the call
+ * after it may find pages for it, those that the first one got back among them.
+ * A call reads and updates the tables and the ring:
  * calls on the same ones are ordered by the caller, as on one stream.
  * GDN_VALIDATE=1 copies the lengths, the rows, the counts and the ring to the
  * host and returns GDN_ERR_DOMAIN for negative context_lens, rows that repeat

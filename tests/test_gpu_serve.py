@@ -92,6 +92,24 @@ def n_seed(case):
     return case["n"] * 31 + case["page"] + case["hi"]
 
 
+def test_tables_called_again():
+    # one page, held by a request that ends: the other is refused, and finds it free in the next call with the same
+    # lengths; from then on, as always where none is refused, a repeat changes nothing
+    for extra in (0, 3000):  # in one launch and in two
+        ctx, new, T = [64, 0], [-1, 5], 5 + extra
+        table, counts, free, state = [[0], [-1]], [1, 0], [-9], [0, 0, 0]
+        d = [i32(table), i32(counts), i32(free), i32(state)]
+        seen = []
+        for _ in range(3):
+            got = gdn.gdn_batch_tables(i32(ctx), i32(new), T, 64, *d)
+            want = ref.tables(ctx, new, None, T, 64, table, counts, free, state)
+            assert [x.tolist() for x in got] == list(want) and [x.tolist() for x in d] == [table, counts, free, state]
+            seen.append([x.tolist() for x in list(got) + d])
+        assert seen[0][2][:5] == [-1] * 5 and seen[0][7] == [0, 1, 1] and seen[0][1] == [0, 0]
+        assert seen[1][2][:5] == [0, 1, 2, 3, 4] and seen[1][7] == [0, 0, 0] and seen[1][4] == [[-1], [0]]
+        assert seen[2] == seen[1]
+
+
 def test_tables_long_request():
     # one request of 2^20 tokens: positions and slots far from zero
     T, page = 1 << 20, 64
