@@ -104,7 +104,9 @@ def gdn_batch_tables(context_lens, new_lens, T_total: int, page_size: int, block
     page_counts [num_rows], free_pages [num_pages] and free_state [3] (ring head, free pages, refused requests).
 
     context_lens and new_lens are int32 [num_seqs] on the device (new_lens < 0: the request has ended); rows int32
-    [num_seqs] names each request's row (None: row n)."""
+    [num_seqs] names each request's row (None: row n).  kv_lens - context_lens is the tokens that were taken: 0 for a
+    request that found no pages, whose tokens stay in cu_seqlens; as `commit` of gdn_decode_pool it keeps their states
+    as they are."""
     lib, dev, i32 = _gdn._load(), _device_of(context_lens, "context_lens"), torch.int32
     if _elsewhere(dev, stream):
         with _On(dev, stream):

@@ -80,7 +80,12 @@ extern "C" {
  * requests before it do not fit in the free pages, when its row has no room
  * (max_blocks), when it owns fewer pages than context_lens needs, or when
  * rows[n] is outside [0, num_rows).  A refused request keeps its pages and its
- * kv_lens entry is context_lens[n]; its tokens stay in cu_seqlens.  Pages given
+ * kv_lens entry is context_lens[n]; its tokens stay in cu_seqlens, without slots.
+ * What the step's layers then compute for them is not the request's: its outputs
+ * are to be dropped and its state kept.  kv_lens[n] - context_lens[n], the tokens
+ * that were taken, is 0 for it: as `commit` of gdn_decode_pool that difference
+ * leaves the states of refused requests (and of ended ones) as they are, and
+ * behind gdn_prefill it says which final states to store.  Pages given
  * back in a call are free for the next call.  Calling again with the same
  * lengths changes nothing, unless a request was refused (free_state[2]): the call
  * after it may find pages for it, those that the first one got back among them.
@@ -191,7 +196,9 @@ size_t gdn_cache_attention_workspace_bytes(int32_t num_seqs, int64_t T_total, in
  *   commit  device int32 [num_seqs], or NULL for all: the state that is stored
  *           is the one after the first commit[n] tokens (cut to the request's
  *           tokens; 0 or less: the state stays).  o is written for every token,
- *           so drafted tokens can be tried without being kept.
+ *           so drafted tokens can be tried without being kept.  Behind
+ *           gdn_batch_tables it is kv_lens - context_lens, so that a refused
+ *           request's state stays.
  *   q_scale factor of q
  *   l2_eps  > 0: q and k are first divided by sqrt(sum of squares + l2_eps)
  *           over d_k, per token and head; 0: they are taken as they are

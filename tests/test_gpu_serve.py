@@ -673,6 +673,51 @@ def test_a_server_runs():
     log("  a server's steps agree with whole-sequence forms")
 
 
+def test_a_server_runs_out_of_pages():
+    # A request is refused: its state and its cache stay as they were, the other's go on, and when pages have come back
+    # it takes the same tokens and has the state of a request that was never refused.
+    e = _Engine(2, pages=3, max_blocks=4)
+    rows = i32([0, 1])
+    x0 = e.tokens(160, 0)
+    e.step(i32([0, 0]), i32([100, 60]), rows, x0, 160, prompt=True)
+    assert e.state.tolist()[1:] == [0, 0]
+
+    def decode(ctx, new, x, T):
+        cu, kv, slots, _ = gdn.gdn_batch_tables(i32(ctx), i32(new), T, e.page, e.table, e.counts, e.ring, e.state, rows=rows)
+        took = kv - i32(ctx)
+        before = e.states.clone()
+        gdn.gdn_decode_pool(x["q"], x["k"], x["v"], x["g"], x["beta"], e.states, rows, cu_seqlens=cu, commit=took)
+        if T:  # the same by the prompts' way
+            _, last = gdn.gdn_prefill(x["q"], x["k"], x["v"], x["g"], x["beta"], cu, initial_state=before)
+            last = torch.where((took > 0)[:, None, None, None], last, before)
+            assert (last - e.states).abs().max() <= 2e-2 * last.abs().max()
+        gdn.gdn_cache_write(x["ak"], x["av"], slots, e.kc, e.vc, e.ks, e.vs)
+        o = gdn.gdn_cache_attention(x["aq"], e.kc, e.vc, e.ks, e.vs, e.table, kv, cu, rows=rows)
+        return took.tolist(), o
+
+    x1, kept, page = e.tokens(6, 1), e.states.clone(), int(e.table[1, 0])
+    held = [t[page].clone() for t in (e.kc, e.vc, e.ks, e.vs)]
+    assert decode([100, 60], [1, 5], x1, 6)[0] == [1, 0] and e.state.tolist()[2] == 1
+    assert torch.equal(e.states[1], kept[1]) and not torch.equal(e.states[0], kept[0])
+    assert all(torch.equal(a.view(torch.uint8), b[page].view(torch.uint8)) for a, b in zip(held, (e.kc, e.vc, e.ks, e.vs)))
+    none = {k: v[:0] for k, v in x1.items()}
+    kept = e.states.clone()
+    assert decode([101, 60], [-1, 0], none, 0)[0] == [-101, 0] and torch.equal(e.states, kept)
+    later = {k: v[1:].contiguous() for k, v in x1.items()}
+    took, o = decode([0, 60], [0, 5], later, 5)
+    assert took == [0, 5] and e.state.tolist()[2] == 0 and torch.equal(e.states[0], kept[0])
+    whole = {k: torch.cat([x0[k][100:], later[k]]).contiguous() for k in later}
+    S = gdn.gdn_prefill(whole["q"], whole["k"], whole["v"], whole["g"], whole["beta"], i32([0, 65]))[1]
+    assert (S[0] - e.states[1]).abs().max() <= 2e-2 * S.abs().max()
+    k, v = whole["ak"].double(), whole["av"].double()
+    for h in range(e.H):
+        j = h // (e.H // e.hkv)
+        want, _, _ = ref.attention(later["aq"][:, h:h + 1].double(), k[:, j], v[:, j], e.d ** -0.5, 60,
+                                   torch.ones(65, dtype=torch.bool, device="cuda"))
+        # keys and values are off by half a step of 3 mantissa bits of the page's largest
+        assert (o[:, h].double() - want[:, 0]).abs().max() <= 2.0 ** -4 * 2 * v[:, j].abs().max()
+
+
 def _calls():
     """Every serving call on inputs of its own: (name, function, tensors it updates)."""
     gen = torch.Generator().manual_seed(5)
