@@ -46,10 +46,13 @@ bool repeats(const std::vector<int32_t>& v, int64_t below, bool negative_is_fine
 }
 
 int32_t validate_tables(const gdn::TablesLaunch& p, hipStream_t s) {
-    std::vector<int32_t> ctx, rows, counts, state;
-    if (!to_host(ctx, p.context_lens, p.num_seqs, s) || !to_host(state, p.free_state, 3, s) ||
-        !to_host(counts, p.page_counts, p.num_rows, s))
+    std::vector<int32_t> ctx, added, rows, counts, state;
+    if (!to_host(ctx, p.context_lens, p.num_seqs, s) || !to_host(added, p.new_lens, p.num_seqs, s) ||
+        !to_host(state, p.free_state, 3, s) || !to_host(counts, p.page_counts, p.num_rows, s))
         return GDN_ERR_HIP;
+    int64_t tokens = 0;
+    for (const int32_t x : added) tokens += x > 0 ? x : 0;
+    if (tokens > p.T_total) return GDN_ERR_DOMAIN;
     if (p.rows) {
         if (!to_host(rows, p.rows, p.num_seqs, s)) return GDN_ERR_HIP;
         if (repeats(rows, p.num_rows, false)) return GDN_ERR_DOMAIN;

@@ -92,8 +92,9 @@ extern "C" {
  * A call reads and updates the tables and the ring:
  * calls on the same ones are ordered by the caller, as on one stream.
  * GDN_VALIDATE=1 copies the lengths, the rows, the counts and the ring to the
- * host and returns GDN_ERR_DOMAIN for negative context_lens, rows that repeat
- * or lie outside, and a ring that does not fit its array. */
+ * host and returns GDN_ERR_DOMAIN for negative context_lens, new lengths whose sum
+ * passes T_total, rows that repeat or lie outside, and a ring that does not fit its
+ * array. */
 int32_t gdn_batch_tables(const int32_t* context_lens, const int32_t* new_lens, const int32_t* rows, int32_t num_seqs,
                          int64_t T_total, int32_t page_size, int32_t* block_table, int32_t num_rows,
                          int32_t max_blocks, int32_t* page_counts, int32_t* free_pages, int32_t num_pages,

@@ -864,3 +864,17 @@ def test_validation_mode(monkeypatch):
         t[3] = i32(state)
         with pytest.raises(gdn.GdnError):
             gdn.gdn_batch_tables(i32(ctx), i32([1, 1]), 2, 64, *t, rows=i32(rows))
+
+
+def test_validation_of_new_lengths(monkeypatch):
+    # more new tokens than T_total: the call would cut them; those of ended requests are none
+    monkeypatch.setenv("GDN_VALIDATE", "1")
+    for new, T, fine in (([1, 2], 3, True), ([1, 2], 2, False), ([-5, 3], 3, True), ([2 ** 31 - 1, 2 ** 31 - 1], 9, False)):
+        t = [i32([[-1] * 4] * 2), i32([0, 0]), i32([0, 1, 2]), i32([0, 3, 0])]
+        call = lambda: gdn.gdn_batch_tables(i32([0, 0]), i32(new), T, 64, *t)
+        if fine:
+            assert call()[0].tolist()[-1] == T
+            continue
+        with pytest.raises(gdn.GdnError) as e:
+            call()
+        assert e.value.status == gdn.GDN_ERR_DOMAIN and t[1].tolist() == [0, 0]
