@@ -71,6 +71,8 @@ class _On:
     """The device and the stream of a call, while it allocates and enqueues."""
 
     def __init__(self, device, stream):
+        if stream is not None and stream.device_index != device:
+            raise ValueError("stream must be of the device of the call's first tensor")
         self.entered = [torch.cuda.device(device)] + ([] if stream is None else [torch.cuda.stream(stream)])
 
     def __enter__(self):

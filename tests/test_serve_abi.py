@@ -155,6 +155,22 @@ def test_binding_refuses_host_tensors_and_wrong_shapes():
         gdn.gdn_batch_tables(i, i, 0, 64, torch.zeros(3, 4, dtype=torch.int32), i, i, i)
 
 
+def test_binding_refuses_a_stream_of_another_device():
+    # else the call would run on its own device's current stream, not ordered behind the stream it was given
+    class Stream:
+        device_index = 1
+
+    with pytest.raises(ValueError):
+        gdn.serve._On(0, Stream())
+    Stream.device_index = 0
+    try:
+        gdn.serve._On(0, Stream())
+    except ValueError:
+        pytest.fail("a stream of the same device is refused")
+    except (AssertionError, RuntimeError):
+        pass  # without a device
+
+
 # ---------------------------------------------------------------- the plain forms themselves
 
 
