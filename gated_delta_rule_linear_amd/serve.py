@@ -172,7 +172,8 @@ def gdn_cache_attention(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_l
     """Causal attention of the step's queries q [T, H, dk] (bf16 or fp32) over the paged cache (see gdn_cache_write);
     returns o [T, H, dv].  Request n's queries are rows cu_seqlens[n] .. cu_seqlens[n + 1] - 1 and the last of the
     kv_lens[n] tokens that row rows[n] (None: row n) of block_table holds.  scale: 1 / sqrt(dk) by default.  max_new
-    and max_kv, host-side bounds on a request's new tokens and on kv_lens, help to plan (0: unknown)."""
+    and max_kv, host-side bounds on a request's new tokens and on kv_lens, help to plan (0: unknown).  Rows behind
+    cu_seqlens[-1] are not written: they keep what a given o holds, and of an o made here they are uninitialised."""
     lib, dt, dev, i32 = _gdn._load(), _gdn._dtype_code(q), _device_of(q, "q"), torch.int32
     if _elsewhere(dev, stream):
         with _On(dev, stream):
@@ -210,7 +211,8 @@ def gdn_decode_pool(q, k, v, g, beta, states, slots, cu_seqlens=None, commit=Non
     request; returns o [T, H, dv].  q, k [T, H_k, dk] and v [T, H, dv] in bf16 or fp32 (head h reads key head
     h // (H // H_k)); g [T, H, dk] or [T, H] and beta [T, H] in fp32; slots int32 [num_seqs]; cu_seqlens int32
     [num_seqs + 1] (None: one token each); commit int32 [num_seqs]: the tokens whose update is kept (None: all);
-    l2_eps > 0: q and k are L2-normalised in the kernel."""
+    l2_eps > 0: q and k are L2-normalised in the kernel.  Rows behind cu_seqlens[-1] and those of requests whose slot is
+    outside the pool are not written: they keep what a given o holds, and of an o made here they are uninitialised."""
     lib, dt, dev, i32, f32 = _gdn._load(), _gdn._dtype_code(q), _device_of(q, "q"), torch.int32, torch.float32
     if _elsewhere(dev, stream):
         with _On(dev, stream):

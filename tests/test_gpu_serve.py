@@ -549,6 +549,17 @@ def test_pool_one_token_each(N, H):
     _pool_check(args, slots, list(range(N + 1)), None, 0.0, null_cu=True)
 
 
+def test_pool_leaves_rows_behind_the_last_offset():
+    # a batch padded to a fixed number of tokens: rows behind the offsets, and those of a skipped slot, keep what o held
+    args = _pool_inputs([2, 1, 1, 3], 4, 2, 64, 64, torch.bfloat16, False, [1, 0, 2, 3], 0, 5, True)
+    d = [t.cuda() for t in args]
+    o = torch.full((7, 4, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    before = d[5].clone()
+    assert gdn.gdn_decode_pool(*d, i32([1, 9, 0]), cu_seqlens=i32([0, 2, 3, 4]), q_scale=0.7, o=o) is o
+    assert torch.all(o[2:3] == 7.0) and torch.all(o[4:] == 7.0) and not torch.any(o[[0, 1, 3]] == 7.0)
+    assert torch.equal(d[5][2:], before[2:])
+
+
 def test_pool_many_tokens():
     # longer than a server's steps: the same recurrence
     args = _pool_inputs([200, 33], 2, 1, 64, 64, torch.float32, True, [1, 0], 0, 7, False)
