@@ -452,6 +452,44 @@ def test_attention_infinite_queries(dtype, lens, kv, hints):
     assert ((o.double() - want).abs()[calm] <= (3 * eps + 2 * 200 * EPS32 * 2 ** 6) * (mag + want.abs())[calm] + 1e-30).all()
 
 
+def _gaps(s, gaps):
+    """Without the pages of these blocks of the first request."""
+    row = 0 if s.rows is None else int(s.rows[0])
+    s.table[row, gaps] = -1
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("dk,dv", [(64, 64), (128, 128)])
+@pytest.mark.parametrize("gaps", [[7], [8], [0], [60], [61], [62], [63], [64], [65], [3, 4, 59, 66, 67, 100, 129],
+                                  list(range(20, 90))])
+def test_attention_prompt_with_gaps(dtype, dk, dv, gaps):
+    # pages left out of the tiles that every row sees whole, at even and odd tiles and around every 64th
+    log(f"attention: a chunk with gaps {gaps} {dtype} dk={dk} dv={dv}")
+    for kv, lens, hints in (([9000], [150], {}), ([9000, 300], [150, 40], dict(max_new=150, max_kv=9000))):
+        s = ref.Server(kv, 64, 1, dk, dv, seed=gaps[0])
+        _gaps(s, gaps)
+        _attention_check(s, lens, 4, dtype, **hints)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("page,gaps", [(64, []), (128, [1, 5]), (256, [0])])
+def test_attention_prompt_nan_early(dtype, page, gaps):
+    # NaN codes in tiles that every row sees whole: a value's channel, and a key (every channel of its head)
+    log(f"attention: NaN early {dtype} page={page} gaps={gaps}")
+    for where in ("value", "key"):
+        s = ref.Server([5000, 700], page, 2, 128, 128, seed=page)
+        codes = (s.v if where == "value" else s.k).view(torch.uint8)
+        codes[s.table[0, gaps].long(), 0, 5, 3] = 0xff  # in a page that is left out it reaches none
+        _gaps(s, gaps)
+        codes[int(s.table[0, 3]), 1, 9, 77] = 0x7f
+        lens = [150, 60]
+        want = torch.isnan(s.reference(torch.ones((210, 8, 128), dtype=torch.float64), lens, 0.1)[0])
+        kc, vc, ks, vs, tab, kv_lens, _ = s.to("cuda")
+        q = torch.randn((210, 8, 128), generator=torch.Generator().manual_seed(1)).to(dtype).cuda()
+        o = gdn.gdn_cache_attention(q, kc, vc, ks, vs, tab, kv_lens, i32([0, 150, 210]))
+        assert want.any() and not want.all() and torch.equal(torch.isnan(o).cpu(), want)
+
+
 @pytest.mark.parametrize("scale", [0.0, -0.3, 4.0])
 def test_attention_scale(scale):
     _attention_check(ref.Server([150, 20], 64, 2, 64, 64, seed=1), [1, 20], 4, torch.float32, scale=scale)
