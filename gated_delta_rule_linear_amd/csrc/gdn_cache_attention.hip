@@ -36,7 +36,7 @@ typedef float floatx16 __attribute__((ext_vector_type(16)));
 
 constexpr int kTile = 64;      // tokens of a tile
 constexpr int kFewRows = 32;   // a request with up to so many rows is one of few rows
-constexpr int kMinPart = 512;  // tokens of a part of a request's cache, at least
+constexpr int kMinPart = 512;  // tokens of a part of a request's cache, at least (measured for few rows)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kInf = __builtin_inff();
 
@@ -228,12 +228,12 @@ constexpr int kWaves = 4;
 //
 // Bound by reading the cache: 5.6 TB/s over 64 requests of 512 to 16384 tokens
 // (8 heads of 128 channels, 8 KB of a page at a time in random order), which the
-// same kernel with the loads alone does not exceed by more than 3%; 4.8 over one
-// request of 65536.  Keys' loads that take half a line of each row instead ran
-// at 4.4, temporal loads at 4.7.  Requests of up to 32 rows take two workgroups
-// side by side rather than a tile of the other kernel: 5 new tokens of 16
-// requests over 4000 take 49 us here and 48 there, but 52 and 98 in fp32, and 6
-// tokens over 300 7 and 14.
+// same kernel with the loads alone does not exceed by more than 3%; 5.9 over one
+// request of 65536 (22.6 us; with the join the call takes 28, 4.8 TB/s).  Keys'
+// loads that take half a line of each row instead ran at 4.4, temporal loads at
+// 4.7.  Requests of up to 32 rows take two workgroups side by side rather than a
+// tile of the other kernel: 5 new tokens of 16 requests over 4000 take 43 us here
+// and 47 there, in fp32 45 and 96, and 6 tokens over 300 7 and 14.
 template <typename TI, int DK, int DV>
 __global__ __launch_bounds__(64 * kWaves, 2) void attention_rows_kernel(Attention a) {
     constexpr int NS = sizeof(TI) == 4 ? 3 : 1;
@@ -496,13 +496,14 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_rows_kernel(Attentio
 // maximum has grown by at most 2^8 (p stays below 2^8, and all of it is kept).
 // With p rounded to bf16 the largest p is kept at 1, which is exact: put off
 // too, the rescaling would save 2%, but the largest terms would be rounded like
-// the others and the output's error grow from 1.1 to 1.3 times that of its own
-// rounding.
+// the others and the output's error grow from 1.1 times that of its own rounding
+// (1.15 over 16384 tokens) to 1.3.
 //
-// Bound by the matrix cores and the power they draw: 1.05 PFLOP/s over two
-// prompts of 8192 tokens (32 heads, 8 for keys, 128 channels), 1.07 over chunks
-// of 1021 to 2048 tokens behind 16384, where a plain
-// product of 8192 x 8192 matrices reaches 1.24; with 64 channels, where a tile's
+// Bound by the matrix cores and the power they draw: 1.03 to 1.05 PFLOP/s over two
+// prompts of 8192 tokens (32 heads, 8 for keys, 128 channels), 1.04 to 1.07 over
+// chunks of 1021 to 2048 tokens behind 16384, on several devices of one model
+// (0.91 and 0.92 on the slowest), where a plain product of 8192 x 8192 matrices
+// reaches 1.18 to 1.24; with 64 channels, where a tile's
 // products are half and its exponentials the same, 0.85.  In full precision
 // (three products for one) 0.36.
 template <typename TI, int DK, int DV>
@@ -997,9 +998,10 @@ Plan plan(const CacheAttentionLaunch& p) {
         // enough parts to fill the device, since the lengths may differ much (23
         // over 1 to 4097, 92 units: 15.0 us with 512 at once, 18.2 with 256), none
         // below 512 tokens (with 256, 4 over 100 to 500 take 9.2 us instead of 7.0,
-        // 1 over 1000 takes 9.0 instead of 9.8).  A long request beside many short
-        // ones should not be waited for: at most 16384 tokens to a part (which is no
-        // cut for 64 over 512 to 16384: 206 us; with 8192, 212).  For the
+        // 1 over 1000 takes 9.0 instead of 9.8).  A very long request beside many
+        // short ones is not waited for: at most 16384 tokens to a part (which is no cut
+        // for 64 over 512 to 16384: 206 us; with 8192, 212; and one of 16384 beside 31
+        // of 500 is waited for, 75 us).  For the
         // workspace's sake, not more parts than 16384 in all.
         const int64_t units = (int64_t)p.num_seqs * p.H_kv * up(r.few_rows, 16);
         int64_t splits = std::max(units >= kAtOnce / 2 ? 1 : up(kAtOnce, units), up(kv, 16384));

@@ -28,7 +28,9 @@ namespace {
 // Waves of a workgroup for each 64 places of a page, so that a thread's part of a
 // whole page is 16 words at every page size and four waves fit a SIMD.  (Four
 // waves for pages of 256 need 64 words, one wave fits: 32,768 tokens with the
-// grid below took 115 us and take 64.)
+// grid below took 115 us and take 64 to 66, where a copy of as many bytes takes 41:
+// a compute unit holds one such workgroup, whose loads, barrier and stores nothing
+// overlaps.)
 constexpr int kWaves = 4;
 // Tiles grow, from a token for each wave up to a page, while the grid has more
 // workgroups than this (of 4 waves): twice what the card holds at once

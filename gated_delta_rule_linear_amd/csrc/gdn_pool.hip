@@ -14,9 +14,10 @@
 // Tokens therefore need no barrier and no LDS.  The state is touched once: it
 // is read and written with non-temporal hints.
 //
-// Measured: 512 requests of 32 heads of 128 x 128, one token, 2.17 GB, 380 to 394
-// us, 5.5 to 5.7 TB/s (a large in-place multiplication: 5.9); with 16 columns to a
-// wave, half a line of each row, 628.  One request, 4.2 MB, 4.4 us, of which a
+// Measured: 512 requests of 32 heads of 128 x 128, one token, 2.17 GB, 380 to 396
+// us, 5.5 to 5.7 TB/s (gdn_decode's kernel, which reads whole rows and takes no
+// slots, 361 us for the same states, 6.0; a large in-place multiplication: 5.9);
+// with 16 columns to a wave, half a line of each row, 628.  One request, 4.2 MB, 4.4 us, of which a
 // launch is 3.5.  45 requests of 1 to 7 tokens, 12 heads of 64 x 128, fp32, 37.5
 // MB, 13 us: two workgroups for each compute unit, and each token's sums wait for
 // the token before.  A request of one token needs 128 registers, of more, with the
