@@ -7,7 +7,10 @@ libgdn.so.  There is no CPU fallback: the first call raises ImportError when
 libgdn.so has not been built (python -m gated_delta_rule_linear_amd.build).
 The calls a server makes beside the layer (include/gdn_serve.h: batch tables,
 a paged 8-bit cache and its attention, a pool of states) are in the submodule
-`serve` and have the same form; all are reached from here.
+`serve` and have the same form, and so have those around the layer in training
+and serving (include/gdn_stack.h: queries and keys normalised and rotated, the
+gated linear recurrence, attention behind a common prefix) in `stack`; all are
+reached from here.
 The submodule `inputs` (seeded synthetic inputs) does not need the library.
 """
 
@@ -29,6 +32,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libgdn_hostsan.so" if os.environ.get("GDN_HOST_SANITIZE") == "1" else "libgdn.so")
 HEADER = os.path.join(os.path.dirname(_HERE), "include", "gdn.h")
 SERVE_HEADER = os.path.join(os.path.dirname(_HERE), "include", "gdn_serve.h")
+STACK_HEADER = os.path.join(os.path.dirname(_HERE), "include", "gdn_stack.h")
 
 GDN_OK, GDN_ERR_INVALID_ARG, GDN_ERR_UNSUPPORTED, GDN_ERR_DOMAIN, GDN_ERR_OOM, GDN_ERR_HIP, GDN_ERR_SCRATCH_LIMIT = range(7)
 GDN_NOALLOC_SCRATCH_BYTES = 64 << 20
@@ -91,6 +95,7 @@ def _load():
     lib.gdn_prefill_tiles.argtypes = [P, P, P, P, P, P, i32, i64, P, P, P, i32, i32, i32, i32, i32, P]
     lib.gdn_prefill_tiles.restype = i32
     serve.bind(lib)
+    stack.bind(lib)
     _LIB = lib
     return lib
 
@@ -516,3 +521,8 @@ from . import serve  # noqa: E402  (it uses the helpers above)
 from .serve import *  # noqa: E402,F401,F403
 
 __all__ += serve.__all__
+
+from . import stack  # noqa: E402
+from .stack import *  # noqa: E402,F401,F403
+
+__all__ += stack.__all__

@@ -1,0 +1,40 @@
+// What the recurrence's kernels share: the decay of a log-decay, and four
+// neighbouring channels.
+#pragma once
+
+#include "gdn_device.h"
+
+namespace gdn {
+
+__device__ __forceinline__ float decay(float g) { return __builtin_amdgcn_exp2f(1.4426950408889634f * g); }
+// 1 - e^g without the difference's loss near g = 0: there by the exponential's
+// series, whose next term is below 2^-25 of the sum.
+__device__ __forceinline__ float one_minus_decay(float g, float a) {
+    float p = 1.f + g * (1.f / 7.f);
+    p = 1.f + g * (1.f / 6.f) * p;
+    p = 1.f + g * (1.f / 5.f) * p;
+    p = 1.f + g * (1.f / 4.f) * p;
+    p = 1.f + g * (1.f / 3.f) * p;
+    p = 1.f + g * (1.f / 2.f) * p;
+    return g > -0.35f ? -g * p : 1.f - a;
+}
+
+// Four neighbouring values as they are in memory.
+template <typename T>
+struct Four;
+template <>
+struct Four<float> {
+    typedef floatx4 raw;
+    floatx4 v;
+    __device__ __forceinline__ floatx4 f() const { return v; }
+    __device__ __forceinline__ static floatx4 of(floatx4 x) { return x; }
+};
+template <>
+struct Four<bf16> {
+    typedef bf16x4 raw;
+    bf16x4 v;
+    __device__ __forceinline__ floatx4 f() const { return {(float)v[0], (float)v[1], (float)v[2], (float)v[3]}; }
+    __device__ __forceinline__ static bf16x4 of(floatx4 x) { return {(bf16)x[0], (bf16)x[1], (bf16)x[2], (bf16)x[3]}; }
+};
+
+}  // namespace gdn

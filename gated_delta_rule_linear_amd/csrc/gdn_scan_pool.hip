@@ -1,0 +1,74 @@
+// The gated linear recurrence on a pool of states, one or a few tokens for each
+// request (gdn_scan_pool): h = e^g h + b per channel, b = x or (1 - e^g) x.
+//
+// A state is read and written once per call, 8 bytes for three operations a token:
+// bound by HBM, and by a launch where requests are few.  A lane has 4 neighbouring
+// channels of one request; the next token's inputs are on their way while one is
+// worked on.
+#include "gdn_device.h"
+#include "gdn_scan.h"
+#include "gdn_stack_kernels.h"
+
+namespace gdn {
+namespace {
+
+struct Pool {
+    const void* x;
+    const float* g;
+    float* states;
+    const int32_t *slots, *cu, *commit;
+    int64_t T;
+    int32_t num_slots, C, blocks;
+    bool mix;
+    void* h;
+};
+
+template <typename TI>
+__global__ __launch_bounds__(64) void scan_pool_kernel(Pool a) {
+    const int64_t n = blockIdx.x / a.blocks;
+    const int32_t c = (int32_t)(blockIdx.x - n * a.blocks) * 256 + 4 * threadIdx.x;
+    const int32_t slot = a.slots[n];
+    if (slot < 0 || slot >= a.num_slots || c >= a.C) return;
+    int64_t t0 = n, t1 = n + 1;
+    if (a.cu) {
+        t0 = a.cu[n] < 0 ? 0 : a.cu[n];
+        t1 = a.cu[n + 1] < a.T ? a.cu[n + 1] : a.T;
+    }
+    if (t1 <= t0) return;
+    int64_t keep = t1 - t0;
+    if (a.commit && a.commit[n] < keep) keep = a.commit[n];
+    float* const state = a.states + (int64_t)slot * a.C + c;
+    auto gate = [&](int64_t t) { return *reinterpret_cast<const floatx4*>(a.g + t * a.C + c); };
+    auto input = [&](int64_t t) { return *reinterpret_cast<const typename Four<TI>::raw*>(static_cast<const TI*>(a.x) + t * a.C + c); };
+    floatx4 g = gate(t0);
+    Four<TI> x{input(t0)};
+    floatx4 s = *reinterpret_cast<const floatx4*>(state);
+    for (int64_t t = t0; t < t1; ++t) {
+        const floatx4 now = g, in = x.f();
+        if (t + 1 < t1) {
+            g = gate(t + 1);
+            x.v = input(t + 1);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float al = decay(now[k]);
+            s[k] = __builtin_fmaf(al, s[k], a.mix ? one_minus_decay(now[k], al) * in[k] : in[k]);
+        }
+        *reinterpret_cast<typename Four<TI>::raw*>(static_cast<TI*>(a.h) + t * a.C + c) = Four<TI>::of(s);
+        if (t - t0 + 1 == keep) *reinterpret_cast<floatx4*>(state) = s;
+    }
+}
+
+}  // namespace
+
+hipError_t launch_scan_pool(const ScanPoolLaunch& p, hipStream_t s) {
+    if (p.num_seqs == 0 || p.T == 0) return hipSuccess;
+    const int32_t blocks = (p.C + 255) / 256;
+    const Pool a = {p.x, p.g, p.states, p.slots, p.cu_seqlens, p.commit, p.T, p.num_slots, p.C, blocks, p.mix, p.h};
+    const dim3 grid((unsigned)((int64_t)p.num_seqs * blocks));
+    if (p.bf16) hipLaunchKernelGGL(scan_pool_kernel<bf16>, grid, dim3(64), 0, s, a);
+    else hipLaunchKernelGGL(scan_pool_kernel<float>, grid, dim3(64), 0, s, a);
+    return hipGetLastError();
+}
+
+}  // namespace gdn

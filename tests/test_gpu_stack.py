@@ -1,0 +1,522 @@
+"""GPU parity of the calls of include/gdn_stack.h with plain 64-bit forms (tests/stack_reference.py): queries and keys
+normalised and rotated, the gated linear recurrence, and their gradients; the calls together with the layer's."""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import gated_delta_rule_linear_amd as gdn
+import stack_reference as ref
+from helpers import log
+
+pytestmark = pytest.mark.gpu
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    gdn.load_library()
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def f64(t):
+    return None if t is None else t.detach().cpu().double()
+
+
+def close(name, got, want, bound, dtype):
+    """Within the bound of the arithmetic and half a step of the output's type of everything (of what is below the type's
+    normal numbers, of the smallest of them)."""
+    got, want, bound = f64(got), f64(want), bound.double()
+    tiny = torch.finfo(dtype).tiny
+    assert torch.equal(torch.isfinite(got), torch.isfinite(want)), f"{name}: not finite elsewhere"
+    limit = bound + ref.half_step(dtype) * (want.abs() + bound) + ref.half_step(dtype) * tiny
+    fine = torch.isfinite(want)
+    over = ((got - want).abs() / limit)[fine]
+    worst = float(over.max()) if over.numel() else 0.0
+    log(f"  {name}: {worst:.3f} of the bound")
+    assert worst <= 1.0, f"{name}: {worst:.3f} times the bound"
+
+
+# ---------------------------------------------------------------- norm and rotation
+
+
+def norm_case(T, H, hk, d, norm, weights, rotary, interleaved, dtype, strided, seed, far=100000):
+    gen = torch.Generator().manual_seed(seed)
+    r = lambda *s: torch.randn(s, generator=gen)
+    wide = (r(T, H + 2 * hk, d) * torch.exp(r(H + 2 * hk, 1))).to(dtype).cuda()
+    q, k = wide[:, :H], wide[:, H:H + hk]
+    if not strided:
+        q, k = q.contiguous(), k.contiguous()
+    pos = torch.randint(-far, far, (T,), generator=gen).to(torch.int32)
+    freq = (10000.0 ** (-torch.arange(0, rotary, 2).double() / max(rotary, 1))).float()
+    return dict(q=q, k=k if hk else None, norm=norm, eps=1e-5, q_weight=(1 + 0.3 * r(d)).cuda() if weights else None,
+                k_weight=(1 + 0.3 * r(d)).cuda() if weights else None, positions=pos.cuda() if rotary else None,
+                inv_freq=freq.cuda() if rotary else None, interleaved=interleaved, q_scale=0.37)
+
+
+def norm_reference(a, kind):
+    return (f64(a[kind]), a["norm"], a["eps"], f64(a[kind + "_weight"]),
+            None if a["positions"] is None else a["positions"].cpu(), f64(a["inv_freq"]), a["interleaved"],
+            a["q_scale"] if kind == "q" else 1.0)
+
+
+NORMS = [(1, 1, 1, 64, 2, True, 64, False, True), (1, 32, 8, 128, 2, True, 128, False, True),
+         (3, 4, 2, 128, 1, False, 0, False, False), (7, 5, 3, 64, 0, True, 32, True, True),
+         (129, 12, 4, 64, 2, True, 32, True, False), (65, 3, 1, 128, 2, False, 64, False, True),
+         (500, 9, 9, 128, 1, False, 128, True, True), (33, 40, 0, 64, 2, True, 8, False, False),
+         (33, 17, 2, 128, 0, False, 16, False, True), (2, 70, 33, 128, 2, True, 120, False, True),
+         (9001, 2, 1, 64, 2, True, 64, False, True), (12, 6, 6, 64, 2, True, 56, True, False)]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("case", NORMS)
+def test_norm(case, dtype):
+    log(f"norm {case} {dtype}")
+    a = norm_case(*case[:-1], dtype, case[-1], seed=sum(map(int, case)))
+    q, k = gdn.gdn_qk_norm(**a)
+    for kind, got in (("q", q), ("k", k)):
+        if a[kind] is None:
+            assert got is None
+            continue
+        want, bound = ref.qk_norm(*norm_reference(a, kind)[:1], *norm_reference(a, kind)[1:])
+        close(kind, got, want, bound, dtype)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("case", NORMS)
+def test_norm_backward(case, dtype):
+    log(f"norm backward {case} {dtype}")
+    a = norm_case(*case[:-1], dtype, case[-1], seed=sum(map(int, case)))
+    gen = torch.Generator().manual_seed(99)
+    g = {s: None if a[s] is None else torch.randn(a[s].shape, generator=gen).to(dtype).cuda() for s in "qk"}
+    need = gdn.gdn_qk_norm_backward_workspace_bytes(case[0], case[1], case[2], case[3])
+    space = torch.full((need // 4,), float("nan"), device="cuda")  # what a workspace held before does not matter
+    rest = {s: v for s, v in a.items() if s not in "qk"}
+    dq, dk, dwq, dwk = gdn.gdn_qk_norm_backward(a["q"], a["k"], g["q"], g["k"], workspace=space, **rest)
+    for kind, got, dw in (("q", dq, dwq), ("k", dk, dwk)):
+        if a[kind] is None:
+            continue
+        x, *more = norm_reference(a, kind)
+        want, bound, weight, weight_bound = ref.qk_norm_backward(x, f64(g[kind]), *more)
+        close("d" + kind, got, want, bound, dtype)
+        if a[kind + "_weight"] is None:
+            assert dw is None
+        else:
+            close("dw" + kind, dw, weight, weight_bound, F32)
+
+
+def test_norm_backward_into_slices():
+    a = norm_case(77, 6, 2, 64, 2, True, 64, False, BF16, True, seed=5)
+    g = [torch.randn(s, device="cuda").to(BF16) for s in ((77, 6, 64), (77, 2, 64))]
+    rest = {s: v for s, v in a.items() if s not in "qk"}
+    plain = gdn.gdn_qk_norm_backward(a["q"], a["k"], *g, **rest)
+    whole = torch.full((77, 10, 64), 3.0, dtype=BF16, device="cuda")
+    got = gdn.gdn_qk_norm_backward(a["q"], a["k"], *g, dq=whole[:, :6], dk=whole[:, 6:8], **rest)
+    assert torch.equal(whole[:, :6], plain[0]) and torch.equal(whole[:, 6:8], plain[1])
+    assert bool((whole[:, 8:] == 3.0).all())
+    assert torch.equal(got[2], plain[2]) and torch.equal(got[3], plain[3])
+    # in the place of the outputs' gradients, and without the weights'
+    over = gdn.gdn_qk_norm_backward(a["q"], a["k"], *g, dq=g[0], dk=g[1], want_d_weights=False, **rest)
+    assert torch.equal(g[0], plain[0]) and torch.equal(g[1], plain[1]) and over[2] is None and over[3] is None
+
+
+def test_norm_in_place():
+    a = norm_case(300, 8, 4, 128, 2, True, 128, False, BF16, False, seed=6)
+    want = gdn.gdn_qk_norm(**a)
+    got = gdn.gdn_qk_norm(**a, q_out=a["q"], k_out=a["k"])
+    assert got[0] is a["q"] and torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("position", [0, 1, (1 << 20) + 1, (1 << 31) - 1, -(1 << 31)])
+def test_norm_far_positions(position):
+    a = norm_case(4, 2, 1, 128, 0, False, 128, False, F32, True, seed=7)
+    a["positions"] = i32([position] * 4)
+    q, _ = gdn.gdn_qk_norm(**a)
+    close("q", q, *ref.qk_norm(*norm_reference(a, "q")), F32)
+
+
+def test_norm_of_nothing_and_of_zeros():
+    a = norm_case(0, 4, 2, 64, 2, True, 64, False, BF16, False, seed=8)
+    q, k = gdn.gdn_qk_norm(**a)
+    assert q.shape == (0, 4, 64) and k.shape == (0, 2, 64)
+    rest = {s: v for s, v in a.items() if s not in "qk"}
+    out = gdn.gdn_qk_norm_backward(a["q"], a["k"], q, k, **rest)
+    assert bool((out[2] == 0).all()) and bool((out[3] == 0).all())
+    z = torch.zeros((5, 3, 64), device="cuda")
+    for norm in (0, 1, 2):
+        assert bool((gdn.gdn_qk_norm(z, norm=norm)[0] == 0).all())
+        dq, _, _, _ = gdn.gdn_qk_norm_backward(z, None, z + 1, None, norm=norm, eps=1e-6)
+        # r = 1 / sqrt(eps), a thousand, where there is a norm
+        close("dq", dq, torch.full((5, 3, 64), 1e3 if norm else 1.0, dtype=torch.float64), torch.full((5, 3, 64), 32e3 * ref.E32), F32)
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_norm_nan_stays_where_it_is(interleaved):
+    a = norm_case(6, 4, 2, 64, 2, True, 32, interleaved, F32, False, seed=9)
+    want, _ = gdn.gdn_qk_norm(**a)
+    a["q"][2, 1, 5] = math.nan
+    a["q"][3, 0, 40] = math.inf
+    got, _ = gdn.gdn_qk_norm(**a)
+    touched = torch.zeros((6, 4), dtype=torch.bool)
+    touched[2, 1] = touched[3, 0] = True
+    assert torch.equal(got[~touched.cuda()], want[~touched.cuda()]) and bool(torch.isnan(got[2, 1]).all())
+    # without a norm a channel that is not rotated keeps to itself, one that is reaches its partner
+    a["norm"] = gdn.GDN_NORM_NONE
+    got, _ = gdn.gdn_qk_norm(**a)
+    assert int(torch.isinf(got[3, 0]).sum()) == 1 and int(torch.isnan(got[3, 0]).sum()) == 0
+    assert int(torch.isnan(got[2, 1]).sum()) == 2
+
+
+# ---------------------------------------------------------------- the recurrence
+
+
+def scan_case(lens, C, mix, init, dtype, seed, extra=0, slow=True):
+    gen = torch.Generator().manual_seed(seed)
+    r = lambda *s: torch.randn(s, generator=gen)
+    T, n = sum(lens) + extra, len(lens)
+    g = torch.log(0.7 + 0.3 * torch.sigmoid(r(T, C) + 2 * r(C))) if slow else -5 * torch.rand((T, C), generator=gen)
+    return dict(x=r(T, C).to(dtype).cuda(), g=g.cuda(), cu_seqlens=i32([0] + list(np.cumsum(lens))), mix=mix,
+                initial_state=r(n, C).cuda() if init else None), (r(T, C).to(dtype).cuda(), r(n, C).cuda() if init else None)
+
+
+def scan_reference(a):
+    return f64(a["x"]), f64(a["g"]), a["cu_seqlens"].tolist(), a["mix"], f64(a["initial_state"])
+
+
+LENS = [[1], [0], [2, 0, 0, 7], [63, 64, 65], [1] * 150, [0] * 130 + [5] + [0] * 90 + [3, 0], [700], [513, 2, 0, 129, 1],
+        [8] * 40, [3000], [1, 1023, 64, 0, 0, 960], [16, 112, 128, 256, 1]]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("mix", [False, True])
+@pytest.mark.parametrize("lens,C", [(l, c) for l, c in zip(LENS, [4, 8, 252, 256, 260, 516, 64, 1028, 12, 20, 300, 1024])])
+def test_scan(lens, C, mix, dtype):
+    init = len(lens) % 2 == 0 or C > 500
+    log(f"scan {lens[:6]} x{len(lens)} C={C} mix={mix} init={init} {dtype}")
+    a, _ = scan_case(lens, C, mix, init, dtype, seed=len(lens) + C, extra=3 * (C % 8 == 4))
+    h = torch.full_like(a["x"], 7.0)
+    out, final = gdn.gdn_scan(**a, h=h)
+    assert out is h
+    want = ref.scan(*scan_reference(a))
+    end = sum(lens)
+    close("h", h[:end], want["h"][:end], want["bound"][:end], dtype)
+    assert bool((h[end:] == 7.0).all())
+    close("final", final, want["final"], want["final_bound"], F32)
+    for m, length in enumerate(lens):
+        if length == 0:
+            assert torch.equal(f64(final[m]), want["final"][m])
+    again, none = gdn.gdn_scan(**a, output_final_state=False)
+    assert none is None and torch.equal(again[:end], h[:end])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("mix", [False, True])
+@pytest.mark.parametrize("lens,C", [(l, c) for l, c in zip(LENS, [4, 8, 252, 256, 260, 516, 64, 1028, 12, 20, 300, 1024])])
+def test_scan_backward(lens, C, mix, dtype):
+    init = len(lens) % 2 == 0 or C > 500
+    log(f"scan backward {lens[:6]} x{len(lens)} C={C} mix={mix} init={init} {dtype}")
+    a, (dh, df) = scan_case(lens, C, mix, init, dtype, seed=len(lens) + C, extra=3 * (C % 8 == 4))
+    kept = gdn.gdn_scan_checkpoints(a["x"])
+    gdn.gdn_scan(**a, checkpoints=kept)
+    space = torch.full((gdn.gdn_scan_backward_workspace_bytes(*a["x"].shape) // 4,), float("nan"), device="cuda")
+    outs = [gdn.gdn_scan_backward(**a, d_h=dh, d_final_state=df, checkpoints=c, workspace=space) for c in (None, kept)]
+    end = sum(lens)
+    assert all(torch.equal(x[:end] if i < 2 else x, y[:end] if i < 2 else y) for i, (x, y) in enumerate(zip(*outs)))
+    want = ref.scan_backward(*scan_reference(a), f64(dh), f64(df))
+    dx, dg, d_init = outs[0]
+    close("dx", dx[:end], want["dx"][:end], want["dx_bound"][:end], dtype)
+    close("dg", dg[:end], want["dg"][:end], want["dg_bound"][:end], F32)
+    close("d_init", d_init, want["d_init"], want["d_init_bound"], F32)
+    assert gdn.gdn_scan_backward(**a, d_h=dh, d_final_state=df, want_d_initial_state=False)[2] is None
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_scan_fast_decays_and_long(dtype):
+    # products of decays far below fp32's smallest number
+    for lens, C in (([5000, 37], 8), ([300], 260)):
+        a, (dh, df) = scan_case(lens, C, True, True, dtype, seed=3, slow=False)
+        h, final = gdn.gdn_scan(**a)
+        want = ref.scan(*scan_reference(a))
+        close("h", h, want["h"], want["bound"], dtype)
+        close("final", final, want["final"], want["final_bound"], F32)
+        back = ref.scan_backward(*scan_reference(a), f64(dh), f64(df))
+        dx, dg, d_init = gdn.gdn_scan_backward(**a, d_h=dh, d_final_state=df)
+        close("dx", dx, back["dx"], back["dx_bound"], dtype)
+        close("dg", dg, back["dg"], back["dg_bound"], F32)
+        close("d_init", d_init, back["d_init"], back["d_init_bound"], F32)
+
+
+def test_scan_borders_of_the_gate():
+    # no decay at all (sums), and decays of 0 (each token by itself)
+    T, C = 400, 8
+    x = torch.randn((T, C), device="cuda")
+    cu = i32([0, T])
+    h, _ = gdn.gdn_scan(x, torch.zeros_like(x), cu)
+    mags = f64(x).abs().cumsum(0)
+    steps = torch.arange(1, T + 1).double()[:, None]
+    close("sums", h, f64(x).cumsum(0), steps * 8 * ref.E32 * mags, F32)
+    assert bool((gdn.gdn_scan(x, torch.zeros_like(x), cu, mix=True, initial_state=torch.full((1, C), 2.0, device="cuda"))[0] == 2).all())
+    g = torch.full_like(x, -math.inf)
+    for mix in (False, True):
+        h, final = gdn.gdn_scan(x, g, cu, mix=mix)
+        assert torch.equal(h, x) and torch.equal(final[0], x[-1])
+        dx, dg, d0 = gdn.gdn_scan_backward(x, g, cu, x, mix=mix)
+        assert torch.equal(dx, x) and bool((dg == 0).all()) and bool((d0 == 0).all())
+
+
+def test_scan_nan_and_inf_stay_in_their_sequence():
+    lens, C = [100, 70, 0, 300, 9], 12
+    for bad in (math.nan, math.inf):
+        a, (dh, df) = scan_case(lens, C, False, True, F32, seed=12)
+        want, final = gdn.gdn_scan(**a)
+        back = gdn.gdn_scan_backward(**a, d_h=dh, d_final_state=df)
+        a["x"][130, 3] = bad  # sequence 1
+        a["initial_state"][3, 5] = bad
+        dh[140, 2] = bad
+        got, got_final = gdn.gdn_scan(**a)
+        off = torch.zeros_like(want, dtype=torch.bool)
+        off[130:170, 3] = True
+        off[170:470, 5] = True
+        assert torch.equal(got[~off], want[~off]) and bool((~torch.isfinite(got[off])).all())
+        assert torch.equal(torch.isinf(got[off]), torch.full_like(got[off], bad == math.inf, dtype=torch.bool))
+        assert int((~torch.isfinite(got_final)).sum()) == 2 and not math.isfinite(float(got_final[1, 3]))
+        dx, dg, d0 = gdn.gdn_scan_backward(**a, d_h=dh, d_final_state=df)
+        off[:] = False
+        off[100:141, 2] = True
+        assert torch.equal(dx[~off], back[0][~off]) and bool((~torch.isfinite(dx[off])).all())
+        off[131:170, 3] = off[170:470, 5] = True
+        assert torch.equal(dg[~off], back[1][~off])
+        assert not math.isfinite(float(d0[1, 2])) and int((~torch.isfinite(d0)).sum()) == 1
+
+
+def test_scan_offsets_that_are_none():
+    # outputs are then no one's, but nothing outside the arrays is touched and the call ends
+    a, (dh, df) = scan_case([300, 300], 64, False, True, F32, seed=13)
+    for cu in ([0, 700, 600], [500, 20, 600], [-5, 9, 1 << 30], [0, 0, -7], [9, 9, 9]):
+        a["cu_seqlens"] = i32(cu)
+        gdn.gdn_scan(**a)
+        gdn.gdn_scan_backward(**a, d_h=dh, d_final_state=df)
+        torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("n,C,lens,commit,mix", [
+    (1, 4, None, False, False), (3, 260, None, False, True), (65, 1024, None, True, False),
+    (5, 256, [1, 0, 7, 3, 2], True, True), (4, 1300, [2, 9, 1, 1], False, False)])
+def test_scan_pool(dtype, n, C, lens, commit, mix):
+    gen = torch.Generator().manual_seed(n + C)
+    r = lambda *s: torch.randn(s, generator=gen)
+    cu = list(range(n + 1)) if lens is None else [0] + [int(v) for v in np.cumsum(lens)]
+    T = cu[-1]
+    x, g, states = r(T, C).to(dtype).cuda(), -torch.rand((T, C), generator=gen).cuda(), r(n + 3, C).cuda()
+    slots = torch.randperm(n + 3, generator=gen)[:n].tolist()
+    if n > 2:
+        slots[1] = -4 if n % 2 else n + 9
+    keep = [int(v) for v in torch.randint(-1, 5, (n,), generator=gen)] if commit else None
+    want, bound, after, after_bound = ref.scan_pool(f64(x), f64(g), f64(states), slots, cu, keep, mix)
+    was, h = states.clone(), torch.full_like(x, 7.0)
+    gdn.gdn_scan_pool(x, g, states, i32(slots), cu_seqlens=None if lens is None else i32(cu),
+                      commit=None if keep is None else i32(keep), mix=mix, h=h)
+    skipped = torch.isnan(want)
+    assert bool((h.cpu()[skipped] == 7.0).all())
+    close("h", torch.where(skipped, 0.0, f64(h)), torch.where(skipped, 0.0, want), bound, dtype)
+    close("states", states, after, after_bound, F32)
+    for s in range(n + 3):
+        if s not in slots or (keep is not None and keep[slots.index(s)] <= 0):
+            assert torch.equal(states[s], was[s])
+
+
+def test_scan_pool_goes_on_from_scan():
+    # a prompt with gdn_scan, then tokens one by one on a pool: as the whole sequence at once
+    a, _ = scan_case([137], 512, True, False, F32, seed=14)
+    x, g = a["x"], a["g"]
+    whole, final = gdn.gdn_scan(**a)
+    h, state = gdn.gdn_scan(x[:100], g[:100], i32([0, 100]), mix=True)
+    pool = torch.zeros((3, 512), device="cuda")
+    pool[1] = state[0]
+    rows = [gdn.gdn_scan_pool(x[t:t + 1], g[t:t + 1], pool, i32([1]), mix=True) for t in range(100, 137)]
+    want = ref.scan(*scan_reference(a))
+    close("h", torch.cat([h] + rows), want["h"], want["bound"], F32)
+    close("state", pool[1:2], want["final"], want["final_bound"], F32)
+    assert bool((pool[0] == 0).all()) and bool((pool[2] == 0).all())
+
+
+# ---------------------------------------------------------------- the calls together
+
+
+def _calls():
+    """Every call on fixed inputs; returns their outputs."""
+    n = norm_case(200, 8, 2, 128, 2, True, 128, False, BF16, True, seed=21)
+    rest = {s: v for s, v in n.items() if s not in "qk"}
+    gq, gk = torch.randn((200, 8, 128), device="cuda").to(BF16), torch.randn((200, 2, 128), device="cuda").to(BF16)
+    a, (dh, df) = scan_case([400, 0, 3, 250], 516, True, True, BF16, seed=22)
+    pool, was = torch.empty((9, 516), device="cuda"), torch.randn((9, 516), device="cuda")
+    slots = i32([3, 8, 0])
+
+    def calls():
+        out = list(gdn.gdn_qk_norm(**n))
+        out += gdn.gdn_qk_norm_backward(n["q"], n["k"], gq, gk, **rest)
+        kept = gdn.gdn_scan_checkpoints(a["x"])
+        out += gdn.gdn_scan(**a, checkpoints=kept)
+        out += gdn.gdn_scan_backward(**a, d_h=dh, d_final_state=df, checkpoints=kept)
+        out += gdn.gdn_scan_backward(**a, d_h=dh, d_final_state=df)
+        pool.copy_(was)
+        out += [gdn.gdn_scan_pool(a["x"][:3], a["g"][:3], pool, slots, mix=True), pool]
+        return out
+
+    return calls
+
+
+def test_graphs_replay_every_call():
+    calls = _calls()
+    eager = [t.clone() for t in calls()]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        calls()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    outs = []
+    for g in graphs:
+        with torch.cuda.graph(g):
+            outs.append(calls())
+    for rep in range(4):
+        junk = torch.randn(1 << 20, device="cuda")
+        assert torch.isfinite((junk * 2).sum()).item()
+        for g, got in zip(graphs, outs):
+            for t in got:
+                t.fill_(3.0)
+            g.replay()
+            torch.cuda.synchronize()
+            for i, (x, y) in enumerate(zip(got, eager)):
+                assert torch.equal(x, y), f"replay {rep}: output {i} differs from the eager call"
+
+
+def test_other_streams_and_repeats_give_the_same_bits():
+    calls = _calls()
+    want = [t.clone() for t in calls()]
+    for rep in range(3):
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            got = calls()
+        side.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
+def test_scans_on_two_streams_at_once():
+    a, (dh, df) = scan_case([9000], 1024, False, True, BF16, seed=23)
+    want = [t.clone() for t in gdn.gdn_scan(**a)] + [t.clone() for t in gdn.gdn_scan_backward(**a, d_h=dh, d_final_state=df)]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in range(3)], []
+    for s in streams:  # of each call its own workspace
+        got.append(gdn.gdn_scan(**a, stream=s) + gdn.gdn_scan_backward(**a, d_h=dh, d_final_state=df, stream=s))
+    torch.cuda.synchronize()
+    for out in got:
+        assert all(torch.equal(x, y) for x, y in zip(out, want))
+
+
+def test_a_training_step():
+    """Unit queries and keys into the layer, the recurrence behind it, and the gradients back through all three: against
+    differences of the same forward calls in full precision."""
+    torch.manual_seed(30)
+    T, H, d = 150, 2, 64
+    lens = [80, 0, 70]
+    cu = i32([0, 80, 80, 150])
+    r = lambda *s: torch.randn(s, device="cuda")
+    p = dict(q=r(T, H, d), k=r(T, H, d), v=r(T, H, d), g=-torch.rand((T, H, d), device="cuda"), beta=torch.sigmoid(r(T, H)),
+             gate=-torch.rand((T, H * d), device="cuda"))
+    dy = r(T, H * d)
+    norm = dict(norm=gdn.GDN_NORM_L2, eps=1e-6, q_scale=d ** -0.5)
+
+    def forward(p):
+        q, k = gdn.gdn_qk_norm(p["q"], p["k"], **norm)
+        o, _ = gdn.gdn_prefill(q, k, p["v"], p["g"], p["beta"], cu)
+        y, _ = gdn.gdn_scan(o.view(T, H * d), p["gate"], cu, mix=True)
+        return q, k, o, y
+
+    q, k, o, y = forward(p)
+    dx, dgate, _ = gdn.gdn_scan_backward(o.view(T, H * d), p["gate"], cu, dy, mix=True)
+    dqn, dkn, dv, dg, dbeta, _ = gdn.gdn_prefill_backward(q, k, p["v"], p["g"], p["beta"], cu, dx.view(T, H, d))
+    dq, dk, _, _ = gdn.gdn_qk_norm_backward(p["q"], p["k"], dqn, dkn, **norm)
+    got = dict(q=dq, k=dk, v=dv, g=dg, beta=dbeta, gate=dgate)
+    for name in got:
+        # along the gradient itself, so that the difference is large against fp32's noise: the two halves of a central
+        # difference of step e carry E32-sized noise of |y||dy|, over 2 e |gradient|
+        direction = got[name] / got[name].norm()
+        e = 2e-3 * float(p[name].norm()) / 10
+        ends = [float((forward({**p, name: p[name] + s * e * direction})[3].double() * dy.double()).sum()) for s in (1, -1)]
+        slope, want = (ends[0] - ends[1]) / (2 * e), float(got[name].double().norm())
+        log(f"  {name}: gradient {want:.6f}, difference {slope:.6f}")
+        assert abs(slope - want) <= 2e-2 * want, name
+
+
+def test_binding_refusals():
+    x = torch.zeros((4, 2, 64), device="cuda")
+    w = torch.ones(64, device="cuda")
+    for kw in (dict(q=x[:, :, :32]), dict(q=x.transpose(0, 1)), dict(q=x[..., ::2]), dict(k=x[:3]), dict(positions=i32([0] * 4)),
+               dict(inv_freq=w[:32]), dict(q_weight=w[:32]), dict(q_out=x[:3]), dict(k_out=x), dict(q_weight=w.cpu()),
+               dict(k=x, k_out=x[:, :1])):
+        with pytest.raises((ValueError, gdn.GdnError)):
+            gdn.gdn_qk_norm(**{**dict(q=x), **kw})
+    for kw in (dict(q=x.to(BF16), k=x), dict(q_weight=w.double()), dict(q=x.half())):
+        with pytest.raises(TypeError):
+            gdn.gdn_qk_norm(**{**dict(q=x), **kw})
+    with pytest.raises(gdn.GdnError):
+        gdn.gdn_qk_norm(x, positions=i32([0] * 4), inv_freq=torch.ones(6, device="cuda"))  # 12 channels
+    with pytest.raises(gdn.GdnError):
+        gdn.gdn_qk_norm(x, eps=0.0)
+    with pytest.raises(gdn.GdnError):
+        gdn.gdn_qk_norm_backward(x, None, x, None, q_weight=w, workspace=torch.empty(4, device="cuda"))
+    with pytest.raises(ValueError):
+        gdn.gdn_qk_norm_backward(x, x, x, x, dq=torch.empty((4, 3, 64), device="cuda"))
+    y, cu = torch.zeros((9, 8), device="cuda"), i32([0, 9])
+    s = torch.zeros((1, 8), device="cuda")
+    for kw in (dict(g=y[:8]), dict(x=y[:, :6], g=y[:, :6]), dict(initial_state=s[:, :4]), dict(final_state=s[:0]),
+               dict(h=y.t()), dict(checkpoints=y[0, :1]), dict(workspace=torch.empty(1 << 16))):
+        with pytest.raises((ValueError, gdn.GdnError)):
+            gdn.gdn_scan(**{**dict(x=y, g=y, cu_seqlens=cu), **kw})
+    for kw in (dict(g=y.to(BF16)), dict(cu_seqlens=cu.long()), dict(initial_state=s.to(BF16)), dict(x=y.half())):
+        with pytest.raises(TypeError):
+            gdn.gdn_scan(**{**dict(x=y, g=y, cu_seqlens=cu), **kw})
+    with pytest.raises(gdn.GdnError):
+        gdn.gdn_scan(y[:, :6].contiguous(), y[:, :6].contiguous(), cu)  # channels in fours
+    with pytest.raises(gdn.GdnError):
+        gdn.gdn_scan(y, y, cu, initial_state=s, final_state=s)
+    with pytest.raises(gdn.GdnError):
+        gdn.gdn_scan(y, y, cu, workspace=torch.empty(1, device="cuda"))
+    with pytest.raises((ValueError, TypeError)):
+        gdn.gdn_scan_backward(y, y, cu, y.to(BF16))
+    with pytest.raises((ValueError, gdn.GdnError)):
+        gdn.gdn_scan_pool(y, y, s, cu)
+
+
+def test_validation_mode(monkeypatch):
+    monkeypatch.setenv("GDN_VALIDATE", "1")
+    y = torch.zeros((9, 8), device="cuda")
+    s, good = torch.zeros((4, 8), device="cuda"), i32([0, 4, 9])
+    gdn.gdn_scan(y, y, good)
+    gdn.gdn_scan(y, y, i32([0, 4, 8]))
+    gdn.gdn_scan_pool(y, y, s, i32([3, 1]), cu_seqlens=good)
+    bad = y.clone()
+    bad[3, 2] = 1e-3
+    nan = y.clone()
+    nan[8, 7] = math.nan
+    for kw in (dict(cu_seqlens=i32([0, 5, 4])), dict(cu_seqlens=i32([1, 4, 9])), dict(cu_seqlens=i32([0, 4, 10])), dict(g=bad),
+               dict(g=nan)):
+        for call in (gdn.gdn_scan, lambda **k: gdn.gdn_scan_backward(**k, d_h=y)):
+            with pytest.raises(gdn.GdnError) as e:
+                call(**{**dict(x=y, g=y, cu_seqlens=good), **kw})
+            assert e.value.status == gdn.GDN_ERR_DOMAIN
+    for kw in (dict(slots=i32([1, 1])), dict(cu_seqlens=i32([0, 4, 8])), dict(g=nan)):
+        with pytest.raises(gdn.GdnError) as e:
+            gdn.gdn_scan_pool(**{**dict(x=y, g=y, states=s, slots=i32([3, 1]), cu_seqlens=good), **kw})
+        assert e.value.status == gdn.GDN_ERR_DOMAIN
