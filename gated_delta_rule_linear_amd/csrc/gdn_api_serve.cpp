@@ -1,9 +1,12 @@
 // libgdn C-ABI, serving side: argument validation, status codes and dispatch.
-// Declarations and the contract of every entry point are in include/gdn_serve.h.
+// Declarations and the contract of every entry point are in include/gdn_serve.h, and
+// of the attention behind a common beginning in include/gdn_stack.h.
 #include "gdn_serve.h"
+#include "gdn_stack.h"
 
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdlib>
 #include <new>
@@ -153,6 +156,50 @@ int32_t attention_sizes(const gdn::CacheAttentionLaunch& p) {
     return GDN_OK;
 }
 
+// Arguments of an attention call besides its workspace; GDN_OK and T_total 0: nothing to do.
+int32_t attention_arguments(const gdn::CacheAttentionLaunch& p, int32_t dtype) {
+    const int32_t st = attention_sizes(p);
+    if (st != GDN_OK) return st;
+    if (!supported_dtype(dtype)) return GDN_ERR_UNSUPPORTED;
+    if (p.num_rows < 0 || p.num_pages < 0 || p.num_pages > INT32_MAX || !std::isfinite(p.scale)) return GDN_ERR_INVALID_ARG;
+    if (p.T_total == 0) return GDN_OK;
+    if (!aligned(p.q, 16) || !aligned(p.o, 16)) return GDN_ERR_INVALID_ARG;
+    if (!aligned(p.kv_lens, 4) || !aligned(p.cu_seqlens, 4) || !aligned_or_null(p.rows, 4)) return GDN_ERR_INVALID_ARG;
+    if (p.num_rows > 0 && p.max_blocks > 0 && !aligned(p.block_table, 4)) return GDN_ERR_INVALID_ARG;
+    if (p.num_pages > 0 &&
+        (!aligned(p.k_cache, 16) || !aligned(p.v_cache, 16) || !aligned(p.k_scale, 4) || !aligned(p.v_scale, 4)))
+        return GDN_ERR_INVALID_ARG;
+    return GDN_OK;
+}
+int32_t prefix_sizes(const gdn::CachePrefixLaunch& p) {
+    const int32_t st = attention_sizes(p.all);
+    return st != GDN_OK ? st : p.num_groups < 0 || p.max_prefix < 0 ? GDN_ERR_INVALID_ARG : GDN_OK;
+}
+int32_t validate_prefix(const gdn::CachePrefixLaunch& p, hipStream_t s) {
+    const int32_t st = validate_attention(p.all, s);
+    if (st != GDN_OK) return st;
+    std::vector<int32_t> offsets, shared, rows, kv, cu, table;
+    if (!to_host(offsets, p.group_offsets, (int64_t)p.num_groups + 1, s) || !to_host(shared, p.prefix_lens, p.num_groups, s) ||
+        !to_host(kv, p.all.kv_lens, p.all.num_seqs, s) || !to_host(cu, p.all.cu_seqlens, (int64_t)p.all.num_seqs + 1, s) ||
+        !to_host(table, p.all.block_table, (int64_t)p.all.num_rows * p.all.max_blocks, s) ||
+        (p.all.rows && !to_host(rows, p.all.rows, p.all.num_seqs, s)))
+        return GDN_ERR_HIP;
+    if (offsets.front() != 0 || offsets.back() > p.all.num_seqs) return GDN_ERR_DOMAIN;
+    for (int32_t g = 0; g < p.num_groups; ++g) {
+        if (offsets[(size_t)g + 1] < offsets[(size_t)g] || shared[(size_t)g] < 0) return GDN_ERR_DOMAIN;
+        const int64_t blocks = std::min<int64_t>(shared[(size_t)g] / p.all.page_size, p.all.max_blocks);
+        const int32_t* first = nullptr;
+        for (int32_t n = offsets[(size_t)g]; n < offsets[(size_t)g + 1]; ++n) {
+            const int64_t row = p.all.rows ? rows[(size_t)n] : n, len = cu[(size_t)n + 1] - cu[(size_t)n];
+            if (row < 0 || row >= p.all.num_rows || len == 0 || kv[(size_t)n] - len < blocks * p.all.page_size) continue;
+            const int32_t* const at = table.data() + row * p.all.max_blocks;
+            if (first && !std::equal(first, first + blocks, at)) return GDN_ERR_DOMAIN;
+            if (!first) first = at;
+        }
+    }
+    return GDN_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -235,16 +282,8 @@ int32_t gdn_cache_attention(const void* q, const void* k_cache, const void* v_ca
                                          k_scale, v_scale, block_table, rows, kv_lens, cu_seqlens, num_seqs, T_total,
                                          max_new, max_kv, num_pages, page_size, num_rows, max_blocks, scale, o, H,
                                          H_kv, d_k, d_v, dtype == GDN_BF16, workspace};
-    const int32_t st = attention_sizes(p);
-    if (st != GDN_OK) return st;
-    if (!supported_dtype(dtype)) return GDN_ERR_UNSUPPORTED;
-    if (num_rows < 0 || num_pages < 0 || num_pages > INT32_MAX || !std::isfinite(scale)) return GDN_ERR_INVALID_ARG;
-    if (T_total == 0) return GDN_OK;
-    if (!aligned(q, 16) || !aligned(o, 16)) return GDN_ERR_INVALID_ARG;
-    if (!aligned(kv_lens, 4) || !aligned(cu_seqlens, 4) || !aligned_or_null(rows, 4)) return GDN_ERR_INVALID_ARG;
-    if (num_rows > 0 && max_blocks > 0 && !aligned(block_table, 4)) return GDN_ERR_INVALID_ARG;
-    if (num_pages > 0 && (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(k_scale, 4) || !aligned(v_scale, 4)))
-        return GDN_ERR_INVALID_ARG;
+    const int32_t st = attention_arguments(p, dtype);
+    if (st != GDN_OK || T_total == 0) return st;
     const size_t need = gdn::cache_attention_workspace_bytes(p);
     if (need > 0 && (!aligned(workspace, 16) || workspace_bytes < need)) return GDN_ERR_INVALID_ARG;
     hipStream_t s = static_cast<hipStream_t>(stream);
@@ -253,6 +292,45 @@ int32_t gdn_cache_attention(const void* q, const void* k_cache, const void* v_ca
         if (v != GDN_OK) return v;
     }
     return status_of(gdn::launch_cache_attention(p, s));
+}
+
+size_t gdn_cache_attention_prefix_workspace_bytes(int32_t num_seqs, int32_t num_groups, int64_t T_total,
+                                                  int64_t max_new, int64_t max_kv, int64_t max_prefix,
+                                                  int32_t page_size, int32_t max_blocks, int32_t H, int32_t H_kv,
+                                                  int32_t d_k, int32_t d_v) {
+    gdn::CachePrefixLaunch p = {};
+    p.all.num_seqs = num_seqs; p.all.T_total = T_total; p.all.max_new = max_new; p.all.max_kv = max_kv;
+    p.all.page_size = page_size; p.all.max_blocks = max_blocks; p.all.H = H; p.all.H_kv = H_kv; p.all.dk = d_k; p.all.dv = d_v;
+    p.num_groups = num_groups; p.max_prefix = max_prefix;
+    if (prefix_sizes(p) != GDN_OK || T_total == 0) return 0;
+    return gdn::cache_prefix_workspace_bytes(p);
+}
+
+int32_t gdn_cache_attention_prefix(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
+                                   const float* v_scale, const int32_t* block_table, const int32_t* rows,
+                                   const int32_t* kv_lens, const int32_t* cu_seqlens, const int32_t* group_offsets,
+                                   const int32_t* prefix_lens, int32_t num_seqs, int32_t num_groups, int64_t T_total,
+                                   int64_t max_new, int64_t max_kv, int64_t max_prefix, int64_t num_pages,
+                                   int32_t page_size, int32_t num_rows, int32_t max_blocks, float scale, void* o,
+                                   int32_t H, int32_t H_kv, int32_t d_k, int32_t d_v, int32_t dtype, void* workspace,
+                                   size_t workspace_bytes, void* stream) {
+    const gdn::CachePrefixLaunch p = {{q, static_cast<const uint8_t*>(k_cache), static_cast<const uint8_t*>(v_cache),
+                                       k_scale, v_scale, block_table, rows, kv_lens, cu_seqlens, num_seqs, T_total,
+                                       max_new, max_kv, num_pages, page_size, num_rows, max_blocks, scale, o, H, H_kv,
+                                       d_k, d_v, dtype == GDN_BF16, workspace},
+                                      group_offsets, prefix_lens, num_groups, max_prefix};
+    int32_t st = prefix_sizes(p);
+    if (st == GDN_OK) st = attention_arguments(p.all, dtype);
+    if (st != GDN_OK || T_total == 0) return st;
+    if (num_groups > 0 && (!aligned(group_offsets, 4) || !aligned(prefix_lens, 4))) return GDN_ERR_INVALID_ARG;
+    const size_t need = gdn::cache_prefix_workspace_bytes(p);
+    if (need > 0 && (!aligned(workspace, 16) || workspace_bytes < need)) return GDN_ERR_INVALID_ARG;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (validate_mode()) {
+        const int32_t v = num_groups > 0 ? validated(validate_prefix, p, s) : validated(validate_attention, p.all, s);
+        if (v != GDN_OK) return v;
+    }
+    return status_of(gdn::launch_cache_prefix(p, s));
 }
 
 int32_t gdn_decode_pool(const void* q, const void* k, const void* v, const float* g, int32_t head_gate,

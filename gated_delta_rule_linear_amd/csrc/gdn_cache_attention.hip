@@ -40,6 +40,12 @@ constexpr int kMinPart = 512;  // tokens of a part of a request's cache, at leas
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kInf = __builtin_inff();
 
+// What of a request's tokens a kernel reads: all, or, where requests share the
+// pages of a beginning (gdn_cache_attention_prefix), the beginning, once for all
+// rows of a group of requests, or the tokens behind it.  Of these two every part
+// goes to the workspace, at its row of o.
+enum Reach { kAll, kPrefix, kOwn };
+
 struct Attention {
     const void* q;
     const uint8_t *kc, *vc;
@@ -64,6 +70,7 @@ struct Attention {
     // and sum).  Rows: for few, (n * Hkv + h) * few_rows + row; else the first of q.
     int64_t part_rows[2];
     float *ws_o[2], *ws_ml[2];
+    const int32_t* skip;  // kOwn: tokens of each request's beginning, whole pages
 };
 
 // Tiles of BR rows that the requests before n take at most: the tiles of
@@ -82,7 +89,14 @@ __device__ __forceinline__ int32_t request_of(const Attention& a, int64_t b, int
     return below - 1;
 }
 
-// A request, as every kernel sees it.
+// Tokens of a request that its group has read, whatever the offsets of the groups were.
+__device__ __forceinline__ int64_t beginning(const Attention& a, int32_t n) {
+    const int64_t skip = a.skip[n] >> a.page_log2 << a.page_log2;
+    return skip < 0 || skip > a.kv_lens[n] || skip >> a.page_log2 > a.max_blocks ? 0 : skip;
+}
+
+// A request, as every kernel sees it (kPrefix: a group of them).
+template <int REACH = kAll>
 struct Request {
     int64_t t0;       // first new token
     int32_t len;      // new tokens
@@ -93,7 +107,8 @@ struct Request {
     __device__ __forceinline__ Request(const Attention& a, int32_t n) {
         int64_t t1 = a.cu[n + 1];
         t0 = a.cu[n];
-        const int64_t most = (int64_t)a.max_blocks << a.page_log2, held = a.kv_lens[n];
+        const int64_t begin = REACH == kOwn ? beginning(a, n) : 0;
+        const int64_t most = ((int64_t)a.max_blocks << a.page_log2) - begin, held = a.kv_lens[n] - begin;
         t0 = t0 < 0 ? 0 : t0;
         t1 = t1 < a.T ? t1 : a.T;
         len = t1 > t0 ? (int32_t)(t1 - t0) : 0;
@@ -105,12 +120,17 @@ struct Request {
         if (chunk < kMinPart) chunk = kMinPart;
         if (!few && !a.tiled && chunk < kv) chunk = (kv + kTile - 1) / kTile * kTile;  // there is no room for its parts
     }
-    __device__ __forceinline__ bool alone() const { return kv <= chunk; }
+    __device__ __forceinline__ bool alone() const { return REACH == kAll && kv <= chunk; }
+    // The last token that new token i sees.
+    __device__ __forceinline__ int64_t sees(int32_t i) const { return REACH == kPrefix ? kv - 1 : kv - len + i; }
+    __device__ __forceinline__ int64_t parts() const { return (kv + chunk - 1) / chunk; }
 };
 
+template <int REACH = kAll>
 __device__ __forceinline__ const int32_t* table_of(const Attention& a, int32_t n) {
     const int32_t row = a.rows ? a.rows[n] : n;
-    return row >= 0 && row < a.num_rows && a.num_pages > 0 ? a.table + (int64_t)row * a.max_blocks : nullptr;
+    const int64_t begin = REACH == kOwn ? beginning(a, n) >> a.page_log2 : 0;
+    return row >= 0 && row < a.num_rows && a.num_pages > 0 ? a.table + (int64_t)row * a.max_blocks + begin : nullptr;
 }
 
 // The lane's number where it is needed: what is made of threadIdx.x is kept in
@@ -234,7 +254,7 @@ constexpr int kWaves = 4;
 // 4.7.  Requests of up to 32 rows take two workgroups side by side rather than a
 // tile of the other kernel: 5 new tokens of 16 requests over 4000 take 43 us here
 // and 47 there, in fp32 45 and 96, and 6 tokens over 300 7 and 14.
-template <typename TI, int DK, int DV>
+template <typename TI, int DK, int DV, int REACH>
 __global__ __launch_bounds__(64 * kWaves, 2) void attention_rows_kernel(Attention a) {
     constexpr int NS = sizeof(TI) == 4 ? 3 : 1;
     constexpr int BR = 16, KS = DK / 32, VT = DV / 16;
@@ -245,24 +265,24 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_rows_kernel(Attentio
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
     const int h = blockIdx.y, per = (a.few_rows + BR - 1) / BR;  // workgroups side by side along a request's rows
     const int32_t n = blockIdx.x / per;
-    const Request job(a, n);
+    const Request<REACH> job(a, n);
     if (a.tiled && !job.few) return;
     const int64_t from = blockIdx.z * job.chunk;
     if (blockIdx.z > 0 && from >= job.kv) return;
-    const int32_t* const table = table_of(a, n);
+    const int32_t* const table = table_of<REACH>(a, n);
     const int page_mask = (1 << a.page_log2) - 1;
     // (With a request of more rows than it was planned for, more than one turn.)
     for (int32_t row0 = (blockIdx.x - n * per) * BR; row0 < job.rows; row0 += per * BR) {
     const int32_t last_row = (row0 + BR < job.rows ? row0 + BR : job.rows) - 1;
-    int64_t to = job.kv - job.len + last_row / a.G + 1;  // no row of the tile sees more
+    int64_t to = job.sees(last_row / a.G) + 1;  // no row of the tile sees more
     to = !table ? from : to < from + job.chunk ? to : from + job.chunk;
-    const int64_t all_see = job.kv - job.len + row0 / a.G;  // every row of the tile sees up to here
+    const int64_t all_see = job.sees(row0 / a.G);  // every row of the tile sees up to here
 
     // this lane's row; lanes behind the last one work on the first, unseen
     const int32_t row = row0 + r;
     const bool live = row < job.rows;
     const int32_t i = live ? row / a.G : 0, head = h * a.G + (live ? row - i * a.G : 0);
-    const int64_t sees = live ? job.kv - job.len + i : -1;  // the last token that the row sees
+    const int64_t sees = live ? job.sees(i) : -1;  // the last token that the row sees
     Eight<TI> q8[KS];
 #pragma unroll
     for (int m = 0; m < KS; ++m)
@@ -439,7 +459,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_rows_kernel(Attentio
         l += f[w] * s_l[w][jr];
     }
     if (__ballot(row0 + jr < job.rows && m == -kInf)) {
-        const bool some = sees_some(a, table, from, to, kTile, job.kv - job.len + ji);
+        const bool some = sees_some(a, table, from, to, kTile, job.sees(ji));
         if (m == -kInf && some) l += 1.f;
     }
     if (row0 + jr < job.rows) {
@@ -458,7 +478,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_rows_kernel(Attentio
                 store4(static_cast<TI*>(a.o) + orow * DV + c0 + k,
                        floatx4{out[k] * inv, out[k + 1] * inv, out[k + 2] * inv, out[k + 3] * inv});
         } else {
-            const int64_t prow = blockIdx.z * a.part_rows[0] + ((int64_t)n * a.Hkv + h) * a.few_rows + row0 + jr;
+            const int64_t prow = blockIdx.z * a.part_rows[0] + (REACH == kAll ? ((int64_t)n * a.Hkv + h) * a.few_rows + row0 + jr : orow);
 #pragma unroll
             for (int k = 0; k < C; k += 4)
                 *reinterpret_cast<floatx4*>(a.ws_o[0] + prow * DV + c0 + k) = floatx4{out[k], out[k + 1], out[k + 2], out[k + 3]};
@@ -506,7 +526,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_rows_kernel(Attentio
 // reaches 1.18 to 1.24; with 64 channels, where a tile's
 // products are half and its exponentials the same, 0.85.  In full precision
 // (three products for one) 0.36.
-template <typename TI, int DK, int DV>
+template <typename TI, int DK, int DV, int REACH>
 __global__ __launch_bounds__(64 * kWaves, sizeof(TI) == 4 ? 1 : 2) void attention_tile_kernel(Attention a) {
     constexpr int NS = sizeof(TI) == 4 ? 3 : 1;
     constexpr int BR = 32 * kWaves, KS = DK / 16, DT = DV / 32;
@@ -525,17 +545,17 @@ __global__ __launch_bounds__(64 * kWaves, sizeof(TI) == 4 ? 1 : 2) void attentio
     const int32_t rtile = over < 0 ? a.tiles - 1 - id : a.tail - 1 - over % a.tail;
     const int32_t n = request_of(a, rtile, BR);
     if (n < 0) return;
-    Request job(a, n);
+    Request<REACH> job(a, n);
     if (rtile >= a.tail) job.chunk = job.kv;
     const int64_t row0_ = (rtile - first_tile(a, n, BR)) * BR;
     if (job.few || row0_ < 0 || row0_ >= job.rows) return;
     const int32_t row0 = (int32_t)row0_, last_row = (row0 + BR < job.rows ? row0 + BR : job.rows) - 1;
     const int64_t from = part * job.chunk;
     if (part > 0 && from >= job.kv) return;
-    const int32_t* const table = table_of(a, n);
-    int64_t to = job.kv - job.len + last_row / a.G + 1;  // no row of the tile sees more
+    const int32_t* const table = table_of<REACH>(a, n);
+    int64_t to = job.sees(last_row / a.G) + 1;  // no row of the tile sees more
     to = !table ? from : to < from + job.chunk ? to : from + job.chunk;
-    const int64_t all_see = job.kv - job.len + row0 / a.G;  // every row of the workgroup sees up to here
+    const int64_t all_see = job.sees(row0 / a.G);  // every row of the workgroup sees up to here
     const int32_t count = to > from ? (int32_t)((to - from + kTile - 1) / kTile) : 0;  // tiles
     const int page_mask = (1 << a.page_log2) - 1;
 
@@ -544,15 +564,15 @@ __global__ __launch_bounds__(64 * kWaves, sizeof(TI) == 4 ? 1 : 2) void attentio
     const bool live = row < job.rows;
     const int32_t i = live ? row / a.G : 0, head = h * a.G + (live ? row - i * a.G : 0);
     const int64_t orow = (job.t0 + i) * a.H + head;
-    const int64_t sees = live ? job.kv - job.len + i - from : -1;  // the last token of the part that the row sees
+    const int64_t sees = live ? job.sees(i) - from : -1;  // the last token of the part that the row sees
     // Of this wave: no row sees tiles from wave_tiles on, every row sees the first wave_all.
     const int32_t wrow = row0 + 32 * wave, wlast = wrow + 31 < job.rows ? wrow + 31 : job.rows - 1;
     auto tiles_below = [&](int64_t tokens, int64_t up) {  // whole tiles, or tiles begun, of the part's first tokens
         const int64_t t = tokens <= 0 ? 0 : (tokens + up) / kTile;
         return (int32_t)(t < count ? t : count);
     };
-    const int32_t wave_tiles = wrow < job.rows ? tiles_below(job.kv - job.len + wlast / a.G + 1 - from, kTile - 1) : 0;
-    const int32_t wave_all = wrow < job.rows ? tiles_below(job.kv - job.len + wrow / a.G + 1 - from, 0) : 0;
+    const int32_t wave_tiles = wrow < job.rows ? tiles_below(job.sees(wlast / a.G) + 1 - from, kTile - 1) : 0;
+    const int32_t wave_all = wrow < job.rows ? tiles_below(job.sees(wrow / a.G) + 1 - from, 0) : 0;
     const int32_t group_all = tiles_below(all_see + 1 - from, 0);  // every row of the workgroup sees these tiles whole
     Eight<TI> q8[KS];
 #pragma unroll
@@ -911,8 +931,8 @@ __device__ void join_rows(const Attention& a, int32_t block) {
     }
     int parts = 0;
     if (mine && n >= 0) {
-        const Request q(a, n);
-        parts = q.few == FEW && !q.alone() ? (int)((q.kv + q.chunk - 1) / q.chunk) : 0;
+        const Request<> q(a, n);
+        parts = q.few == FEW && !q.alone() ? (int)q.parts() : 0;
         if (FEW) {
             const int32_t row = (int32_t)(r % a.few_rows), h = (int32_t)(r / a.few_rows % a.Hkv), i = row / a.G;
             if (row >= q.rows) parts = 0;
@@ -961,6 +981,116 @@ template <typename TI, int DV, int W>
 __global__ __launch_bounds__(256) void attention_join_kernel(Attention a, int32_t few_blocks) {
     if ((int32_t)blockIdx.x < few_blocks) join_rows<TI, DV, true, W>(a, blockIdx.x);
     else join_rows<TI, DV, false, 1>(a, blockIdx.x - few_blocks);
+}
+
+// ---------------------------------------------------------------- a common beginning
+//
+// Requests of a group hold the same pages at their beginning.  Every row of the
+// group sees all of it, so the beginning is one request of many rows without a
+// mask, which the kernels above take as such (kPrefix); what is behind it is a
+// request each (kOwn).  All parts go to the workspace at their row of o and are
+// joined in one launch.
+struct Groups {
+    const int32_t *offsets, *shared;
+    int32_t count;
+    int32_t *cu, *kv, *row;  // of each group, as a request: tokens, length of the beginning, row of the table
+    int32_t *skip, *of;      // of each request: tokens of the beginning and its group, or 0 and -1
+};
+// A wave to a group.  A request that does not hold the whole beginning before its
+// new tokens (a refused one, say) takes no part: all its tokens are its own.
+__global__ __launch_bounds__(64) void groups_kernel(Attention a, Groups g) {
+    const int lane = threadIdx.x, b = blockIdx.x;
+    auto offset = [&](int32_t i) {
+        const int32_t x = g.offsets[i];
+        return x < 0 ? 0 : x < a.num_seqs ? x : a.num_seqs;
+    };
+    const int32_t n0 = offset(b), n1 = offset(b + 1);
+    const int64_t room = (int64_t)a.max_blocks << a.page_log2, most = g.shared[b] < room ? g.shared[b] : room;
+    const int32_t shared = most < 0 ? 0 : (int32_t)(most >> a.page_log2 << a.page_log2);
+    int32_t first = INT32_MAX;
+    for (int32_t n = n0 + lane; n < n1; n += 64) {
+        const int64_t len = (int64_t)a.cu[n + 1] - a.cu[n];
+        const bool takes = shared > 0 && len > 0 && a.kv_lens[n] - len >= shared;
+        g.skip[n] = takes ? shared : 0;
+        g.of[n] = takes ? b : -1;
+        if (takes && n < first) first = n;
+    }
+    for (int d = 32; d > 0; d /= 2) first = min(first, __shfl_xor(first, d));
+    if (b == 0)
+        for (int32_t n = lane; n < n0; n += 64) {
+            g.skip[n] = 0;
+            g.of[n] = -1;
+        }
+    if (b == g.count - 1)
+        for (int32_t n = n1 + lane; n < a.num_seqs; n += 64) {
+            g.skip[n] = 0;
+            g.of[n] = -1;
+        }
+    if (lane > 0) return;
+    g.cu[b] = a.cu[n0];
+    if (b == g.count - 1) g.cu[g.count] = a.cu[n1];
+    g.kv[b] = first < INT32_MAX ? shared : 0;
+    g.row[b] = first == INT32_MAX ? -1 : a.rows ? a.rows[first] : first;
+}
+
+// Parts of a row of request n at token t, as the kernels wrote them.
+template <int REACH>
+__device__ __forceinline__ int32_t parts_of(const Attention& a, int32_t n, int64_t t, int32_t in_group) {
+    const Request<REACH> q(a, n);
+    if (q.kv == 0) return 0;
+    if (!q.few && first_tile(a, n, 32 * kWaves) + ((t - q.t0) * a.G + in_group) / (32 * kWaves) >= a.tail) return 1;
+    return (int32_t)q.parts();
+}
+// W waves to a row, as in join_rows: `p` of the groups, `o` of the requests, whose
+// parts lie behind those of `p`.
+template <typename TI, int DV, int W>
+__global__ __launch_bounds__(256) void prefix_join_kernel(Attention p, Attention o, Groups g, int32_t first_own) {
+    constexpr int L = DV / 4, STEP = 64 * W / L, ROWS = kWaves / W;
+    __shared__ floatx4 s_o[STEP * ROWS][L];
+    __shared__ float s_l[STEP * ROWS], s_m[kWaves];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, thread = threadIdx.x % (64 * W);
+    const int64_t step = o.T * o.H, r = (int64_t)blockIdx.x * ROWS + wave / W, t = r / o.H;
+    int32_t below = 0;
+    for (int32_t n0 = 0; n0 <= o.num_seqs; n0 += 64) below += __popcll(__ballot(n0 + lane <= o.num_seqs && o.cu[n0 + lane] <= t));
+    const int32_t n = below - 1;
+    const bool mine = r < step && n >= 0 && n < o.num_seqs;  // (not behind the last request)
+    int32_t shared = 0, parts = 0;
+    if (mine) {
+        const int32_t in_group = (int32_t)(r - t * o.H) % o.G, of = g.of[n];
+        if (of >= 0 && of < g.count) shared = parts_of<kPrefix>(p, of, t, in_group);
+        parts = shared + parts_of<kOwn>(o, n, t, in_group);
+    }
+    auto at = [&](int32_t s) { return (s < shared ? s : first_own + s - shared) * step + r; };
+    const float *ml = p.ws_ml[0], *wo = p.ws_o[0];
+    float m = -kInf;
+    for (int s = thread; s < parts; s += 64 * W) m = fmaxf(m, ml[2 * at(s)]);
+    m = across<Max>(m);
+    if (W > 1) {
+        if (lane == 0) s_m[wave] = m;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) m = fmaxf(m, s_m[w]);
+    }
+    const int c = thread % L, s0 = thread / L, at0 = wave / W * STEP;
+    float l = 0.f;
+    floatx4 out = zero4();
+#pragma unroll 4
+    for (int s = s0; s < parts; s += STEP) {
+        const int64_t i = at(s);
+        const float f = joined(ml[2 * i], m);
+        l += f * ml[2 * i + 1];
+        out += f * *reinterpret_cast<const floatx4*>(wo + i * DV + 4 * c);
+    }
+    s_o[at0 + s0][c] = out;
+    if (c == 0) s_l[at0 + s0] = l;
+    __syncthreads();
+    if (s0 > 0 || !mine) return;
+#pragma unroll
+    for (int s = 1; s < STEP; ++s) {
+        out += s_o[at0 + s][c];
+        l += s_l[at0 + s];
+    }
+    store4(static_cast<TI*>(o.o) + r * DV + 4 * c, out * reciprocal_sum(l, m));
 }
 
 // ---------------------------------------------------------------- planning
@@ -1051,19 +1181,26 @@ Plan plan(const CacheAttentionLaunch& p) {
     return r;
 }
 
-template <typename TI, int DK, int DV>
-hipError_t run(const Attention& a, const Plan& pl, hipStream_t s) {
+// The kernels that form the parts.
+template <typename TI, int DK, int DV, int REACH>
+hipError_t run_parts(const Attention& a, const Plan& pl, hipStream_t s) {
     hipError_t e = hipSuccess;
     if (pl.many) {
         const int64_t tiles = a.tiles + (int64_t)a.tail * (a.splits[1] - 1);
-        hipLaunchKernelGGL((attention_tile_kernel<TI, DK, DV>), dim3((unsigned)(tiles * a.Hkv)), dim3(64 * kWaves), 0, s, a);
+        hipLaunchKernelGGL((attention_tile_kernel<TI, DK, DV, REACH>), dim3((unsigned)(tiles * a.Hkv)), dim3(64 * kWaves), 0, s, a);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     if (pl.few) {
         const dim3 grid((unsigned)(a.num_seqs * ((a.few_rows + 15) / 16)), (unsigned)a.Hkv, (unsigned)a.splits[0]);
-        hipLaunchKernelGGL((attention_rows_kernel<TI, DK, DV>), grid, dim3(64 * kWaves), 0, s, a);
-        if ((e = hipGetLastError()) != hipSuccess) return e;
+        hipLaunchKernelGGL((attention_rows_kernel<TI, DK, DV, REACH>), grid, dim3(64 * kWaves), 0, s, a);
+        e = hipGetLastError();
     }
+    return e;
+}
+template <typename TI, int DK, int DV>
+hipError_t run(const Attention& a, const Plan& pl, hipStream_t s) {
+    hipError_t e = run_parts<TI, DK, DV, kAll>(a, pl, s);
+    if (e != hipSuccess) return e;
     const bool wide = a.splits[0] > 16;
     auto blocks = [&](int c, int at_once) { return a.splits[c] > 1 ? (a.part_rows[c] + at_once - 1) / at_once : 0; };
     const int64_t few = blocks(0, wide ? 1 : kWaves), all = few + blocks(1, kWaves);
@@ -1082,13 +1219,51 @@ hipError_t run_t(const Attention& a, const CacheAttentionLaunch& p, const Plan& 
     return run<TI, 64, 64>(a, pl, s);
 }
 
+// A call with a common beginning: the beginnings' plan, the requests' own, and
+// the workspace.
+struct PrefixPlan {
+    Plan p, o;
+    int32_t parts[2];  // of a row at most: of the beginning, of its own
+    size_t ml, groups, bytes;
+};
+CacheAttentionLaunch beginnings(const CachePrefixLaunch& p) {
+    CacheAttentionLaunch a = p.all;
+    a.num_seqs = p.num_groups;
+    a.max_new = 0;
+    a.max_kv = p.max_prefix;
+    return a;
+}
+CacheAttentionLaunch own_tokens(const CachePrefixLaunch& p) {
+    CacheAttentionLaunch a = p.all;
+    if (a.max_kv > 0 && p.max_prefix > 0) a.max_kv = std::max<int64_t>(a.max_kv - p.max_prefix / a.page_size * a.page_size, 1);
+    return a;
+}
+PrefixPlan plan(const CachePrefixLaunch& c) {
+    PrefixPlan r = {};
+    r.p = plan(beginnings(c));
+    r.o = plan(own_tokens(c));
+    r.parts[0] = std::max(r.p.splits[0], r.p.splits[1]);
+    r.parts[1] = std::max(r.o.splits[0], r.o.splits[1]);
+    auto take = [&](size_t bytes) {
+        const size_t at = r.bytes;
+        r.bytes += (bytes + 255) & ~(size_t)255;
+        return at;
+    };
+    const size_t rows = (size_t)(r.parts[0] + r.parts[1]) * (size_t)(c.all.T_total * c.all.H);
+    take(rows * c.all.dv * sizeof(float));
+    r.ml = take(rows * 2 * sizeof(float));
+    r.groups = take(((size_t)c.num_groups * 3 + 1 + (size_t)c.all.num_seqs * 2) * sizeof(int32_t));
+    return r;
+}
+// Requests that share nothing with others are gdn_cache_attention's.
+bool shares(const CachePrefixLaunch& p) { return p.num_groups < p.all.num_seqs && p.num_groups > 0; }
+
 }  // namespace
 
 size_t cache_attention_workspace_bytes(const CacheAttentionLaunch& p) { return plan(p).bytes; }
 
-hipError_t launch_cache_attention(const CacheAttentionLaunch& p, hipStream_t s) {
-    if (p.T_total == 0 || p.num_seqs == 0) return hipSuccess;
-    const Plan pl = plan(p);
+namespace {
+Attention arguments(const CacheAttentionLaunch& p, const Plan& pl) {
     Attention a = {};
     a.q = p.q; a.kc = p.k_cache; a.vc = p.v_cache; a.ks = p.k_scale; a.vs = p.v_scale;
     a.table = p.block_table; a.rows = p.rows; a.kv_lens = p.kv_lens; a.cu = p.cu_seqlens;
@@ -1099,7 +1274,7 @@ hipError_t launch_cache_attention(const CacheAttentionLaunch& p, hipStream_t s) 
     a.scale2 = std::max(std::fabs(p.scale) * kLog2e, std::numeric_limits<float>::min());
     a.negative = p.scale < 0.f;
     a.o = p.o; a.H = p.H; a.Hkv = p.H_kv; a.G = p.H / p.H_kv;
-    a.few_rows = pl.few_rows;
+    a.few_rows = pl.few ? pl.few_rows : 0;  // else every request goes to the tile kernel
     a.tiled = pl.many;
     a.tiles = pl.tiles;
     a.tail = pl.tail;
@@ -1109,8 +1284,61 @@ hipError_t launch_cache_attention(const CacheAttentionLaunch& p, hipStream_t s) 
         a.ws_o[c] = reinterpret_cast<float*>(static_cast<char*>(p.workspace) + pl.off[2 * c]);
         a.ws_ml[c] = reinterpret_cast<float*>(static_cast<char*>(p.workspace) + pl.off[2 * c + 1]);
     }
-    if (!pl.few) a.few_rows = 0;  // every request goes to the tile kernel
+    return a;
+}
+template <typename TI, int DK, int DV>
+hipError_t run_prefix(const Attention& p, const Attention& o, const PrefixPlan& pl, const Groups& g, hipStream_t s) {
+    hipLaunchKernelGGL(groups_kernel, dim3((unsigned)g.count), dim3(64), 0, s, o, g);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || (e = run_parts<TI, DK, DV, kPrefix>(p, pl.p, s)) != hipSuccess ||
+        (e = run_parts<TI, DK, DV, kOwn>(o, pl.o, s)) != hipSuccess)
+        return e;
+    const int64_t rows = o.T * o.H;
+    if (pl.parts[0] + pl.parts[1] > 16)
+        hipLaunchKernelGGL((prefix_join_kernel<TI, DV, kWaves>), dim3((unsigned)rows), dim3(256), 0, s, p, o, g, pl.parts[0]);
+    else
+        hipLaunchKernelGGL((prefix_join_kernel<TI, DV, 1>), dim3((unsigned)((rows + kWaves - 1) / kWaves)), dim3(256), 0, s, p, o, g, pl.parts[0]);
+    return hipGetLastError();
+}
+template <typename TI>
+hipError_t run_prefix_t(const Attention& p, const Attention& o, int32_t dk, int32_t dv, const PrefixPlan& pl, const Groups& g, hipStream_t s) {
+    if (dk == 128 && dv == 128) return run_prefix<TI, 128, 128>(p, o, pl, g, s);
+    if (dk == 128) return run_prefix<TI, 128, 64>(p, o, pl, g, s);
+    if (dv == 128) return run_prefix<TI, 64, 128>(p, o, pl, g, s);
+    return run_prefix<TI, 64, 64>(p, o, pl, g, s);
+}
+}  // namespace
+
+hipError_t launch_cache_attention(const CacheAttentionLaunch& p, hipStream_t s) {
+    if (p.T_total == 0 || p.num_seqs == 0) return hipSuccess;
+    const Plan pl = plan(p);
+    const Attention a = arguments(p, pl);
     return p.bf16 ? run_t<bf16>(a, p, pl, s) : run_t<float>(a, p, pl, s);
+}
+
+size_t cache_prefix_workspace_bytes(const CachePrefixLaunch& p) { return shares(p) ? plan(p).bytes : plan(p.all).bytes; }
+
+hipError_t launch_cache_prefix(const CachePrefixLaunch& c, hipStream_t s) {
+    if (!shares(c)) return launch_cache_attention(c.all, s);
+    if (c.all.T_total == 0) return hipSuccess;
+    const PrefixPlan pl = plan(c);
+    Attention p = arguments(beginnings(c), pl.p), o = arguments(own_tokens(c), pl.o);
+    char* const at = static_cast<char*>(c.all.workspace);
+    float *const ws_o = reinterpret_cast<float*>(at), *const ws_ml = reinterpret_cast<float*>(at + pl.ml);
+    const int64_t rows = o.T * o.H;
+    for (int k = 0; k < 2; ++k) {
+        p.part_rows[k] = o.part_rows[k] = rows;
+        p.ws_o[k] = ws_o;
+        p.ws_ml[k] = ws_ml;
+        o.ws_o[k] = ws_o + pl.parts[0] * rows * c.all.dv;
+        o.ws_ml[k] = ws_ml + pl.parts[0] * rows * 2;
+    }
+    int32_t* const ints = reinterpret_cast<int32_t*>(at + pl.groups);
+    Groups g = {c.group_offsets, c.prefix_lens, c.num_groups, ints, ints + c.num_groups + 1, ints + 2 * c.num_groups + 1,
+                ints + 3 * c.num_groups + 1, ints + 3 * c.num_groups + 1 + c.all.num_seqs};
+    o.skip = g.skip;
+    p.cu = g.cu; p.kv_lens = g.kv; p.rows = g.row;
+    return c.all.bf16 ? run_prefix_t<bf16>(p, o, c.all.dk, c.all.dv, pl, g, s) : run_prefix_t<float>(p, o, c.all.dk, c.all.dv, pl, g, s);
 }
 
 }  // namespace gdn

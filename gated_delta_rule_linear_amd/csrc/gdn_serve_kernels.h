@@ -59,6 +59,16 @@ struct CacheAttentionLaunch {
 size_t cache_attention_workspace_bytes(const CacheAttentionLaunch& p);
 hipError_t launch_cache_attention(const CacheAttentionLaunch& p, hipStream_t stream);
 
+// The same with groups of requests that share a beginning.
+struct CachePrefixLaunch {
+    CacheAttentionLaunch all;
+    const int32_t *group_offsets, *prefix_lens;
+    int32_t num_groups;
+    int64_t max_prefix;
+};
+size_t cache_prefix_workspace_bytes(const CachePrefixLaunch& p);
+hipError_t launch_cache_prefix(const CachePrefixLaunch& p, hipStream_t stream);
+
 struct DecodePoolLaunch {
     const void *q, *k, *v;
     const float* g;

@@ -38,6 +38,11 @@ def bind(lib):
     lib.gdn_scan_backward.restype = i32
     lib.gdn_scan_pool.argtypes = [P, P, P, P, P, P, i32, i64, i32, i32, i32, P, i32, P]
     lib.gdn_scan_pool.restype = i32
+    lib.gdn_cache_attention_prefix.argtypes = [P, P, P, P, P, P, P, P, P, P, P, i32, i32, i64, i64, i64, i64, i64, i32, i32,
+                                               i32, f32, P, i32, i32, i32, i32, i32, P, sz, P]
+    lib.gdn_cache_attention_prefix.restype = i32
+    lib.gdn_cache_attention_prefix_workspace_bytes.argtypes = [i32, i32, i64, i64, i64, i64, i32, i32, i32, i32, i32, i32]
+    lib.gdn_cache_attention_prefix_workspace_bytes.restype = sz
 
 
 # ---------------------------------------------------------------- norm and rotation
@@ -281,6 +286,61 @@ def gdn_scan_pool(x, g, states, slots, cu_seqlens=None, commit=None, mix: bool =
     return h
 
 
+# ---------------------------------------------------------------- attention behind a common beginning
+
+
+def gdn_cache_attention_prefix_workspace_bytes(num_seqs: int, num_groups: int, T_total: int, max_new: int, max_kv: int,
+                                               max_prefix: int, page_size: int, max_blocks: int, H: int, H_kv: int, dk: int,
+                                               dv: int) -> int:
+    return int(_gdn._load().gdn_cache_attention_prefix_workspace_bytes(num_seqs, num_groups, T_total, int(max_new),
+                                                                       int(max_kv), int(max_prefix), page_size, max_blocks, H,
+                                                                       H_kv, dk, dv))
+
+
+def gdn_cache_attention_prefix(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, cu_seqlens, group_offsets,
+                               prefix_lens, rows=None, scale=None, max_new: int = 0, max_kv: int = 0, max_prefix: int = 0,
+                               o=None, workspace=None, stream=None):
+    """gdn_cache_attention for requests of which groups share the pages of a long beginning, which their queries then read
+    once; returns o [T, H, dv].  Group i is requests group_offsets[i] .. group_offsets[i + 1] - 1 (int32 [num_groups + 1]);
+    its first prefix_lens[i] tokens (int32 [num_groups]) lie in the same pages, that is, the rows of block_table of its
+    requests agree in those blocks.  The other arguments are gdn_cache_attention's; max_prefix, a host-side bound on
+    prefix_lens, helps to plan as max_new and max_kv do (0: unknown)."""
+    lib, dt, dev, i32 = _gdn._load(), _gdn._dtype_code(q), _device_of(q, "q"), torch.int32
+    if _elsewhere(dev, stream):
+        with _On(dev, stream):
+            return gdn_cache_attention_prefix(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, cu_seqlens,
+                                              group_offsets, prefix_lens, rows, scale, max_new, max_kv, max_prefix, o,
+                                              workspace)
+    pages, page, hkv, dk, dv, kc, vc, ks, vs = _cache(k_cache, v_cache, k_scale, v_scale, dev)
+    (T, H, _), (n,), (num_rows, max_blocks), (groups,) = q.shape, kv_lens.shape, block_table.shape, prefix_lens.shape
+    qp = _take(q, "q", q.dtype, (T, H, dk), dev)
+    table = _take(block_table, "block_table", i32, (num_rows, max_blocks), dev)
+    rp = None if rows is None else _take(rows, "rows", i32, (n,), dev)
+    kv, cu = _take(kv_lens, "kv_lens", i32, (n,), dev), _take(cu_seqlens, "cu_seqlens", i32, (n + 1,), dev)
+    go = _take(group_offsets, "group_offsets", i32, (groups + 1,), dev)
+    pl = _take(prefix_lens, "prefix_lens", i32, (groups,), dev)
+    if o is None:
+        o = torch.empty_like(q) if dv == dk else q.new_empty((T, H, dv))
+        op = o.data_ptr()
+    else:
+        op = _take(o, "o", q.dtype, (T, H, dv), dev)
+    if workspace is None:
+        wp, wb = None, lib.gdn_cache_attention_prefix_workspace_bytes(n, groups, T, max_new, max_kv, max_prefix, page,
+                                                                      max_blocks, H, hkv, dk, dv)
+        if wb:
+            workspace = k_scale.new_empty((wb + 3) // 4)  # fp32
+            wp = workspace.data_ptr()
+    else:
+        wp, wb = _space(workspace, dev)
+    st = lib.gdn_cache_attention_prefix(qp, kc, vc, ks, vs, table, rp, kv, cu, go, pl, n, groups, T, max_new, max_kv,
+                                        max_prefix, pages, page, num_rows, max_blocks, dk ** -0.5 if scale is None else scale,
+                                        op, H, hkv, dk, dv, dt, wp, wb, _stream(dev))
+    if st:
+        _gdn._check(st, "gdn_cache_attention_prefix")
+    return o
+
+
 __all__ = ["GDN_NORM_NONE", "GDN_NORM_L2", "GDN_NORM_RMS", "gdn_qk_norm", "gdn_qk_norm_backward",
            "gdn_qk_norm_backward_workspace_bytes", "gdn_scan", "gdn_scan_backward", "gdn_scan_pool", "gdn_scan_checkpoints",
-           "gdn_scan_checkpoint_bytes", "gdn_scan_workspace_bytes", "gdn_scan_backward_workspace_bytes"]
+           "gdn_scan_checkpoint_bytes", "gdn_scan_workspace_bytes", "gdn_scan_backward_workspace_bytes",
+           "gdn_cache_attention_prefix", "gdn_cache_attention_prefix_workspace_bytes"]

@@ -174,6 +174,45 @@ int32_t gdn_scan_pool(const void* x, const float* g, float* states, const int32_
                       const int32_t* commit, int32_t num_seqs, int64_t T_total, int32_t num_slots, int32_t C,
                       int32_t mix, void* h, int32_t dtype, void* stream);
 
+/* gdn_cache_attention (gdn_serve.h) for requests of which groups share the pages
+ * of a long beginning (a common prompt): a group's queries read it once.
+ *
+ *   group_offsets  device int32 [num_groups + 1]: group i is requests
+ *                  group_offsets[i] .. group_offsets[i+1]-1, which are neighbours;
+ *                  a request that shares with no other is a group of its own, or
+ *                  in none
+ *   prefix_lens    device int32 [num_groups]: tokens at the beginning of each
+ *                  request of the group that lie in the same pages; what is
+ *                  behind the last whole page of them is read by each request
+ *   max_prefix     bound on prefix_lens, for planning only (0: unknown)
+ *   workspace      gdn_cache_attention_prefix_workspace_bytes(...) bytes, 16-byte
+ *                  aligned
+ *
+ * The other arguments and the result are gdn_cache_attention's: the rows of the
+ * block table that a group's requests have agree in the blocks of the beginning,
+ * and these are read through one of them.  A request that holds fewer than
+ * prefix_lens tokens before its new ones (a refused one, say) takes no part and
+ * reads all of its own.  Sums of parts are joined in an order that sizes, lengths
+ * and groups decide; outputs differ from gdn_cache_attention's by rounding.
+ * GDN_VALIDATE=1 returns GDN_ERR_DOMAIN for what gdn_cache_attention does, for
+ * group offsets that decrease, do not begin at 0 or end behind num_seqs, negative
+ * prefix_lens, and requests of a group whose blocks of the beginning differ. */
+int32_t gdn_cache_attention_prefix(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
+                                   const float* v_scale, const int32_t* block_table, const int32_t* rows,
+                                   const int32_t* kv_lens, const int32_t* cu_seqlens, const int32_t* group_offsets,
+                                   const int32_t* prefix_lens, int32_t num_seqs, int32_t num_groups, int64_t T_total,
+                                   int64_t max_new, int64_t max_kv, int64_t max_prefix, int64_t num_pages,
+                                   int32_t page_size, int32_t num_rows, int32_t max_blocks, float scale, void* o,
+                                   int32_t H, int32_t H_kv, int32_t d_k, int32_t d_v, int32_t dtype, void* workspace,
+                                   size_t workspace_bytes, void* stream);
+
+/* Device scratch bytes of gdn_cache_attention_prefix; a function of the arguments
+ * only (0 for invalid ones). */
+size_t gdn_cache_attention_prefix_workspace_bytes(int32_t num_seqs, int32_t num_groups, int64_t T_total,
+                                                  int64_t max_new, int64_t max_kv, int64_t max_prefix,
+                                                  int32_t page_size, int32_t max_blocks, int32_t H, int32_t H_kv,
+                                                  int32_t d_k, int32_t d_v);
+
 #ifdef __cplusplus
 }
 #endif

@@ -8,6 +8,7 @@ import pytest
 import torch
 
 import gated_delta_rule_linear_amd as gdn
+import serve_reference as serve
 import stack_reference as ref
 from helpers import log
 
@@ -348,6 +349,244 @@ def test_scan_pool_goes_on_from_scan():
     assert bool((pool[0] == 0).all()) and bool((pool[2] == 0).all())
 
 
+# ---------------------------------------------------------------- attention behind a common beginning
+
+
+def shared_server(groups, page, hkv, dk, dv, seed, rows=True):
+    """groups: [(tokens of the beginning, [(own tokens before the step, new tokens), ...])]; a paged cache in which the
+    whole pages of a group's beginning are the same.  Returns (server, new tokens, group offsets, beginnings)."""
+    kv = [p + own + new for p, reqs in groups for own, new in reqs]
+    server = serve.Server(kv, page, hkv, dk, dv, seed=seed, rows=rows)
+    n = 0
+    for p, reqs in groups:
+        at = [n + i if server.rows is None else int(server.rows[n + i]) for i in range(len(reqs))]
+        for row in at[1:]:
+            server.table[row, :p // page] = server.table[at[0], :p // page]
+        n += len(reqs)
+    sizes = [len(reqs) for _, reqs in groups]
+    return server, [new for _, reqs in groups for _, new in reqs], [0] + [int(x) for x in np.cumsum(sizes)], [p for p, _ in groups]
+
+
+def prefix_check(server, lens, offsets, shared, H, dtype, seed=0, extra=2, **kw):
+    gen = torch.Generator().manual_seed(seed + 100)
+    dk, dv, T = server.k.shape[3], server.v.shape[3], sum(lens)
+    q = torch.randn((T + extra, H, dk), generator=gen).to(dtype).cuda()
+    kc, vc, ks, vs, table, kv_lens, rows = server.to("cuda")
+    cu = i32([0] + [int(x) for x in np.cumsum(lens)])
+    o = torch.full((T + extra, H, dv), 7.0, dtype=dtype, device="cuda")
+    need = gdn.gdn_cache_attention_prefix_workspace_bytes(
+        len(lens), len(shared), T + extra, kw.get("max_new", 0), kw.get("max_kv", 0), kw.get("max_prefix", 0), server.page,
+        server.table.shape[1], H, server.k.shape[1], dk, dv)
+    space = torch.full((need // 4 + 4,), float("nan"), device="cuda")
+    got = gdn.gdn_cache_attention_prefix(q, kc, vc, ks, vs, table, kv_lens, cu, i32(offsets), i32(shared), rows=rows, o=o,
+                                         workspace=space, **kw)
+    assert got is o and bool((o[T:] == 7.0).all())
+    scale = kw.get("scale", dk ** -0.5)
+    want, mag, big = server.reference(q[:T].double(), lens, scale, "cuda")
+    got = o[:T].double()
+    assert torch.equal(torch.isnan(got), torch.isnan(want))
+    # Scores: dk + 4 fp32 roundings of sum |q||k| (three of them for each of the split parts of fp32 q), and the
+    # exponential and its argument in base 2.  p is off by twice that (numerator and denominator), the sums over S tokens
+    # by at most S roundings each of sum p|v|; p itself is rounded once to the type's bf16 parts (three: 2^-24), o once to
+    # its type.  A part's factor in the join is an exponential more: 8 roundings of p are added for it.
+    S = max([1] + [int(x) for x in server.kv_lens])
+    parts, half = (3, ref.E32) if dtype == F32 else (1, ref.E16)
+    score = (parts * (dk + 4) + 16) * ref.E32 * big
+    tol = (2 * score + 2 * (S + 64) * ref.E32 + half + 16 * ref.E32) * mag + half * want.abs() + 1e-30
+    err = torch.nan_to_num((got - want).abs() / tol, nan=0.0).max().item() if T else 0.0
+    log(f"  behind a common beginning: largest error / tolerance {err:.3f}")
+    assert err <= 1.0, err
+    return q, o
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("dk,dv", [(64, 64), (128, 128), (64, 128), (128, 64)])
+@pytest.mark.parametrize("page,hkv,G", [(64, 2, 1), (128, 1, 7), (256, 2, 4), (64, 1, 20)])
+def test_prefix(dtype, dk, dv, page, hkv, G):
+    groups = [(1300, [(5, 1), (64, 1), (0, 1), (300, 2)]), (0, [(10, 1), (700, 1)]), (257, [(1, 3)]),
+              (64, [(63, 1), (1, 0), (128, 40)]), (page - 1, [(3, 1), (9, 1)])]
+    log(f"prefix page={page} H_kv={hkv} G={G} dk={dk} dv={dv} {dtype}")
+    prefix_check(*shared_server(groups, page, hkv, dk, dv, seed=dk + page), hkv * G, dtype)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("hints", [{}, dict(max_new=1, max_kv=10240, max_prefix=9000), dict(max_new=1, max_kv=64, max_prefix=64),
+                                   dict(max_new=4000, max_prefix=100000)])
+def test_prefix_long(dtype, hints):
+    groups = [(9000, [(i * 37 % 700, 1) for i in range(40)])]
+    prefix_check(*shared_server(groups, 64, 2, 128, 128, seed=3), 8, dtype, **hints)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("groups", [
+    [(4096, [(0, 300), (17, 1), (0, 129)])], [(1000, [(0, 1)] * 3), (2000, [(5, 2)] * 2), (3000, [(9, 200), (0, 7)])],
+    [(640, [(0, 1)] * 33), (64, [(0, 33), (0, 1)])], [(300, [(0, 0), (0, 0)]), (300, [(1, 1), (2, 0), (3, 5)])],
+    [(70, [(0, 1), (0, 1)])] * 70, [(6000, [(3000, 1), (1, 1), (9000, 1)])]])
+def test_prefix_of_many_and_few_rows(dtype, groups):
+    prefix_check(*shared_server(groups, 64, 1, 64, 64, seed=4), 4, dtype)
+
+
+def test_prefix_requests_that_take_no_part():
+    # of the second group one request holds less than the beginning and one has been refused (it holds fewer tokens than it
+    # adds); requests behind the last group are in none
+    server, lens, offsets, shared = shared_server([(640, [(0, 1), (70, 2)]), (700, [(5, 1), (5, 1), (40, 3), (0, 1)]),
+                                                   (500, [(0, 1), (1, 1)])], 64, 2, 64, 64, seed=5)
+    server.kv_lens[3], server.kv_lens[4] = 333, 2
+    prefix_check(server, lens, offsets[:3], shared[:2], 6, BF16)
+    # a length of the beginning that no request holds, or below zero
+    prefix_check(server, lens, offsets, [10 ** 9, -5, 500], 6, BF16)
+    # no group, and groups of one: gdn_cache_attention itself
+    for offs, lengths in ([[0], []], [list(range(9)), [64] * 8]):
+        q, o = prefix_check(server, lens, offs, lengths, 6, BF16, extra=0)
+        kc, vc, ks, vs, table, kv_lens, rows = server.to("cuda")
+        cu = i32([0] + [int(x) for x in np.cumsum(lens)])
+        assert torch.equal(gdn.gdn_cache_attention(q, kc, vc, ks, vs, table, kv_lens, cu, rows=rows), o)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_prefix_bad_pages_and_nan(dtype):
+    groups = [(1024, [(100, 1), (0, 1), (30, 70)]), (128, [(0, 1), (64, 2)])]
+    for what in ("gone", "all gone", "nan value", "nan key", "past"):
+        server, lens, offsets, shared = shared_server(groups, 64, 2, 64, 64, seed=6, rows=False)
+        if what == "gone":
+            server.table[:3, 4] = -1
+            server.table[1, 16] = 10 ** 6
+        elif what == "all gone":
+            server.table[:3, :16] = -3
+            server.table[1, 16:] = -1
+            server.table[3:, :2] = 10 ** 6
+        elif what == "nan value":
+            page = int(server.table[0, 7])
+            server.v[page, 1, 13, 5] = math.nan
+            server.v[int(server.table[4, 2]), 0, 63, 9] = math.nan
+        elif what == "nan key":
+            server.k[int(server.table[0, 2]), 0, 3, 1] = math.nan
+        else:
+            server.table = server.table[:, :9].contiguous()  # of the beginning too there is no more than the table has
+            server.kv_lens = [min(x, 9 * 64) for x in server.kv_lens]
+            shared = [512, 128]
+        prefix_check(server, lens, offsets, shared, 6, dtype)
+
+
+def test_prefix_rows_that_see_nothing():
+    server, lens, offsets, shared = shared_server([(128, [(3, 1), (0, 1)])], 64, 1, 64, 64, seed=7, rows=False)
+    server.rows = torch.tensor([5, -1], dtype=torch.int32)
+    _, o = prefix_check(server, lens, offsets, shared, 2, BF16)
+    assert bool((o[:2] == 0).all())
+
+
+def test_prefix_infinite_queries():
+    # a row whose scores are all -Inf is NaN, as without a common beginning
+    server, lens, offsets, shared = shared_server([(320, [(10, 1), (99, 1), (5, 1)])], 64, 1, 64, 64, seed=8, rows=False)
+    server.k[..., 0] = 8.0
+    kc, vc, ks, vs, table, kv_lens, _ = server.to("cuda")
+    q = torch.randn((3, 40, 64), device="cuda")
+    q[1, 7, 0], q[2, 39, 0] = -math.inf, math.inf
+    o = gdn.gdn_cache_attention_prefix(q, kc, vc, ks, vs, table, kv_lens, i32([0, 1, 2, 3]), i32(offsets), i32(shared))
+    bad = torch.zeros((3, 40), dtype=torch.bool, device="cuda")
+    bad[1, 7] = bad[2, 39] = True
+    assert bool(torch.isnan(o[bad]).all()) and bool(torch.isfinite(o[~bad]).all())
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.3, 4.0])
+def test_prefix_scale(scale):
+    prefix_check(*shared_server([(700, [(100, 1), (0, 3), (64, 1)])], 64, 2, 64, 64, seed=9), 6, BF16, scale=scale)
+
+
+def test_prefix_offsets_that_are_none():
+    # outputs are then no one's, but nothing outside the arrays is touched and the call ends
+    server, lens, offsets, shared = shared_server([(640, [(9, 1)] * 4), (128, [(9, 2)] * 3)], 64, 2, 64, 64, seed=10)
+    kc, vc, ks, vs, table, kv_lens, rows = server.to("cuda")
+    q = torch.randn((sum(lens), 4, 64), device="cuda").to(BF16)
+    good = [0] + [int(x) for x in np.cumsum(lens)]
+    for offs, cu in (([5, 2, 7], good), ([-9, 3, 1 << 30], good), ([0, 9, -1], good), ([3, 3, 3], good), ([0, 4, 7], [9, 3, 3, 1, 50, 2, 0, -4]),
+                     ([7, 4, 0], [0, 900, 3, 5, 5, 5, 7, 1 << 30])):
+        gdn.gdn_cache_attention_prefix(q, kc, vc, ks, vs, table, kv_lens, i32(cu), i32(offs), i32(shared), rows=rows)
+        torch.cuda.synchronize()
+    gdn.gdn_cache_attention_prefix(q, kc, vc, ks, vs, table, i32([-5, 1 << 30, 0, 7, -(1 << 31), 700, 3]), i32(good), i32(offsets),
+                                   i32(shared), rows=rows)
+    torch.cuda.synchronize()
+
+
+def test_prefix_two_graphs_and_other_streams():
+    server, lens, offsets, shared = shared_server([(3000, [(i, 1) for i in range(20)]), (640, [(0, 70), (9, 1)])], 64, 2, 128, 128,
+                                                  seed=11)
+    kc, vc, ks, vs, table, kv_lens, rows = server.to("cuda")
+    cu, go, pl = i32([0] + [int(x) for x in np.cumsum(lens)]), i32(offsets), i32(shared)
+    q = torch.randn((sum(lens), 8, 128), device="cuda").to(BF16)
+
+    def call(stream=None):
+        return gdn.gdn_cache_attention_prefix(q, kc, vc, ks, vs, table, kv_lens, cu, go, pl, rows=rows, stream=stream)
+
+    want = call().clone()
+    side = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    outs = [call(s) for s in side]
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in outs)
+    graphs, outs = [torch.cuda.CUDAGraph() for _ in range(2)], []
+    for g in graphs:
+        with torch.cuda.graph(g):
+            outs.append(call())
+    for rep in range(4):
+        junk = torch.randn(1 << 20, device="cuda")
+        assert torch.isfinite((junk * 2).sum()).item()
+        for g, o in zip(graphs, outs):
+            o.fill_(3.0)
+            g.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(o, want), rep
+
+
+def test_a_server_behind_one_prompt():
+    """Steps of a server: a prompt written once, its pages put into the rows of twelve requests, then tokens of each: tables,
+    norm and rotation, cache write, attention behind the prompt, recurrence on a pool."""
+    torch.manual_seed(31)
+    page, hkv, H, d, n, P, C = 64, 2, 8, 64, 12, 1000, 256
+    pages, blocks = 64, 24
+    kc = torch.zeros((pages, hkv, page, d), dtype=torch.float8_e4m3fn, device="cuda")
+    vc = torch.zeros((pages, hkv, page // 16, d, 16), dtype=torch.float8_e4m3fn, device="cuda")
+    ks, vs = (torch.ones((pages, hkv), device="cuda") for _ in range(2))
+    table, counts = i32([[-1] * blocks] * (n + 1)), i32([0] * (n + 1))
+    free, state = i32(list(range(pages))), i32([0, pages, 0])
+    freq = (10000.0 ** (-torch.arange(0, d, 2).double() / d)).float().cuda()
+    norm = dict(norm=gdn.GDN_NORM_RMS, q_weight=torch.ones(d, device="cuda"), k_weight=torch.ones(d, device="cuda"),
+                inv_freq=freq)
+    wide = lambda T: torch.randn((T, H + 2 * hkv, d), device="cuda").to(BF16)
+
+    def step(ctx, new, T, rows):
+        cu, kv, slots, pos = gdn.gdn_batch_tables(i32(ctx), i32(new), T, page, table, counts, free, state, rows=i32(rows))
+        x = wide(T)
+        q, k = gdn.gdn_qk_norm(x[:, :H], x[:, H:H + hkv], positions=pos, **norm)
+        gdn.gdn_cache_write(k, x[:, H + hkv:].contiguous(), slots, kc, vc, ks, vs)
+        return q, cu, kv
+
+    step([0], [P], P, [n])  # the prompt, in the last row
+    whole = P // page
+    table[:n, :whole] = table[n, :whole]
+    counts[:n] = whole
+    pool = torch.randn((n + 2, C), device="cuda")
+    groups, shared = i32([0, n]), i32([whole * page])
+    for turn in range(3):
+        held = [whole * page + turn * 2] * n
+        q, cu, kv = step(held, [2] * n, 2 * n, list(range(n)))
+        kw = dict(rows=i32(list(range(n))), max_new=2, max_kv=1024)
+        o = gdn.gdn_cache_attention_prefix(q, kc, vc, ks, vs, table, kv, cu, groups, shared, max_prefix=P, **kw)
+        plain = gdn.gdn_cache_attention(q, kc, vc, ks, vs, table, kv, cu, **kw)
+        # two roundings of bf16 apart: each rounds p and o of its own sums
+        assert float((o.double() - plain.double()).norm() / plain.double().norm()) <= 2 * ref.E16
+        y = o.reshape(2 * n, -1)[:, :C].contiguous()
+        before = pool.clone()
+        commit = kv - i32(held)
+        g = -torch.rand((2 * n, C), device="cuda")
+        h = gdn.gdn_scan_pool(y, g, pool, i32(list(range(n))), cu_seqlens=cu, commit=commit)
+        want, bound, after, after_bound = ref.scan_pool(f64(y), f64(g), f64(before), list(range(n)), list(range(0, 2 * n + 1, 2)),
+                                                        [2] * n, False)
+        close("h", h, want, bound, BF16)
+        close("pool", pool, after, after_bound, F32)
+    assert int(state[2]) == 0
+
+
 # ---------------------------------------------------------------- the calls together
 
 
@@ -497,6 +736,17 @@ def test_binding_refusals():
         gdn.gdn_scan_backward(y, y, cu, y.to(BF16))
     with pytest.raises((ValueError, gdn.GdnError)):
         gdn.gdn_scan_pool(y, y, s, cu)
+    server, lens, offsets, shared = shared_server([(128, [(3, 1), (0, 1)])], 64, 1, 64, 64, seed=7, rows=False)
+    kc, vc, ks, vs, table, kv_lens, _ = server.to("cuda")
+    q = torch.randn((2, 2, 64), device="cuda")
+    fine = dict(block_table=table, kv_lens=kv_lens, cu_seqlens=i32([0, 1, 2]), group_offsets=i32(offsets),
+                prefix_lens=i32(shared))
+    for kw in (dict(group_offsets=i32([0])), dict(cu_seqlens=i32([0, 1])), dict(prefix_lens=i32([1, 2])), dict(o=q[:1]),
+               dict(workspace=torch.empty(4, device="cuda")), dict(max_prefix=-1), dict(group_offsets=i32([0, 2]).cpu())):
+        with pytest.raises((ValueError, gdn.GdnError)):
+            gdn.gdn_cache_attention_prefix(q, kc, vc, ks, vs, **{**fine, **kw})
+    with pytest.raises(TypeError):
+        gdn.gdn_cache_attention_prefix(q, kc, vc, ks, vs, **{**fine, "prefix_lens": i32([1]).long()})
 
 
 def test_validation_mode(monkeypatch):
@@ -516,6 +766,20 @@ def test_validation_mode(monkeypatch):
             with pytest.raises(gdn.GdnError) as e:
                 call(**{**dict(x=y, g=y, cu_seqlens=good), **kw})
             assert e.value.status == gdn.GDN_ERR_DOMAIN
+    server, lens, offsets, shared = shared_server([(128, [(3, 1), (0, 1)]), (0, [(0, 1)])], 64, 1, 64, 64, seed=7, rows=False)
+    kc, vc, ks, vs, table, kv_lens, _ = server.to("cuda")
+    q = torch.randn((3, 2, 64), device="cuda")
+    other = table.clone()
+    other[1, 1] = table[2, 0]
+    fine = dict(block_table=table, kv_lens=kv_lens, cu_seqlens=i32([0, 1, 2, 3]), group_offsets=i32(offsets),
+                prefix_lens=i32(shared))
+    gdn.gdn_cache_attention_prefix(q, kc, vc, ks, vs, **fine)
+    gdn.gdn_cache_attention_prefix(q, kc, vc, ks, vs, **{**fine, "block_table": other, "prefix_lens": i32([64, 0])})
+    for kw in (dict(group_offsets=i32([0, 2, 4])), dict(group_offsets=i32([1, 2, 3])), dict(group_offsets=i32([0, 2, 1])),
+               dict(prefix_lens=i32([-1, 0])), dict(block_table=other), dict(cu_seqlens=i32([0, 2, 1, 3]))):
+        with pytest.raises(gdn.GdnError) as e:
+            gdn.gdn_cache_attention_prefix(q, kc, vc, ks, vs, **{**fine, **kw})
+        assert e.value.status == gdn.GDN_ERR_DOMAIN
     for kw in (dict(slots=i32([1, 1])), dict(cu_seqlens=i32([0, 4, 8])), dict(g=nan)):
         with pytest.raises(gdn.GdnError) as e:
             gdn.gdn_scan_pool(**{**dict(x=y, g=y, states=s, slots=i32([3, 1]), cu_seqlens=good), **kw})

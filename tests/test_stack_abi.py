@@ -27,7 +27,8 @@ def test_exports(lib):
     names = gdn.exported_symbols_in_header(gdn.STACK_HEADER)
     assert {"gdn_qk_norm", "gdn_qk_norm_backward", "gdn_qk_norm_backward_workspace_bytes", "gdn_scan", "gdn_scan_backward",
             "gdn_scan_pool", "gdn_scan_checkpoint_bytes", "gdn_scan_workspace_bytes",
-            "gdn_scan_backward_workspace_bytes"} <= set(names)
+            "gdn_scan_backward_workspace_bytes", "gdn_cache_attention_prefix",
+            "gdn_cache_attention_prefix_workspace_bytes"} == set(names)
     for n in names:
         assert hasattr(lib, n) and n in gdn.__all__ and hasattr(gdn, n), n
 
@@ -112,6 +113,36 @@ def _pool(lib, x=FAKE, g=FAKE, states=FAKE, slots=FAKE, cu=NUL, commit=NUL, n=3,
     (dict(commit=BAD), INVALID), (dict(n=0, T=0, x=NUL), OK), (dict(ns=0, states=NUL), OK)])
 def test_scan_pool_refusals(lib, kw, want):
     assert _pool(lib, **kw) == want
+
+
+def _prefix(lib, q=FAKE, kc=FAKE, vc=FAKE, ks=FAKE, vs=FAKE, table=FAKE, rows=NUL, kv=FAKE, cu=FAKE, go=FAKE, pl=FAKE, n=4,
+            groups=2, T=4, max_new=0, max_kv=0, max_prefix=0, pages=5, page=64, nr=4, mb=4, scale=0.1, o=FAKE, H=4, hkv=2, dk=64,
+            dv=64, dt=1, ws=FAKE, wb=MANY):
+    return lib.gdn_cache_attention_prefix(q, kc, vc, ks, vs, table, rows, kv, cu, go, pl, n, groups, T, max_new, max_kv,
+                                          max_prefix, pages, page, nr, mb, scale, o, H, hkv, dk, dv, dt, ws, wb, None)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(n=-1), INVALID), (dict(groups=-1), INVALID), (dict(T=-1), INVALID), (dict(T=1 << 31), INVALID),
+    (dict(max_new=-1), INVALID), (dict(max_kv=-1), INVALID), (dict(max_prefix=-1), INVALID), (dict(mb=-1), INVALID),
+    (dict(H=5), INVALID), (dict(hkv=0), INVALID), (dict(dk=96), UNSUPPORTED), (dict(dv=256), UNSUPPORTED),
+    (dict(page=48), UNSUPPORTED), (dict(dt=5), UNSUPPORTED), (dict(n=0), INVALID), (dict(T=1 << 30, H=64), UNSUPPORTED),
+    (dict(nr=-1), INVALID), (dict(pages=-1), INVALID), (dict(scale=math.inf), INVALID), (dict(q=BAD), INVALID),
+    (dict(o=NUL), INVALID), (dict(kv=NUL), INVALID), (dict(cu=BAD), INVALID), (dict(rows=BAD), INVALID),
+    (dict(table=NUL), INVALID), (dict(kc=BAD), INVALID), (dict(vs=NUL), INVALID), (dict(go=NUL), INVALID),
+    (dict(go=BAD), INVALID), (dict(pl=NUL), INVALID), (dict(ws=NUL), INVALID), (dict(wb=16), INVALID),
+    (dict(T=0, n=0, q=NUL, go=NUL), OK)])
+def test_prefix_refusals(lib, kw, want):
+    assert _prefix(lib, **kw) == want
+
+
+def test_prefix_workspace_sizes():
+    size = gdn.gdn_cache_attention_prefix_workspace_bytes
+    sizes = (64, 1024, 32, 8, 128, 128)
+    plain = gdn.gdn_cache_attention_workspace_bytes(8, 8, 1, 9000, *sizes)
+    assert size(8, 8, 8, 1, 9000, 4096, *sizes) == plain and size(8, 0, 8, 1, 9000, 4096, *sizes) == plain
+    assert size(8, 1, 8, 1, 9000, 4096, *sizes) > 0
+    assert size(8, 1, 0, 1, 9000, 4096, *sizes) == 0 and size(8, -1, 8, 1, 9000, 4096, *sizes) == 0
 
 
 def test_workspace_sizes():
