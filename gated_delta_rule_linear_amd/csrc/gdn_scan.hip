@@ -38,11 +38,15 @@ struct Scan {
     const float* d_final;
     void* dx;
     float *dg, *d_init;
+    float* states;      // [T / kCheck][C] state before every kCheck tokens, or NULL
+    uint64_t* maps;     // [tiles][C] maps of the tiles, and [groups][C] what comes into a group of them (NULL: one tile)
+    uint32_t* tickets;  // workgroups that have begun
     int64_t tiles;
-    float* states;  // [tiles][C] state before each tile, or NULL
-    floatx2* maps;  // [tiles][C] maps of the tiles
-    float* carry;   // [tiles][C] c of the token after each tile (backward)
 };
+
+constexpr int kCheck = 64;
+constexpr uint64_t kNotReady = ~0ull;       // of a tile's map
+constexpr int32_t kMostPolls = 1 << 22;     // seconds: no wait is without end, whatever happened
 
 // A run's map per channel.  A constant map has A < 0: e alone counts, whatever
 // the state before (Inf and NaN among it).
@@ -124,30 +128,68 @@ struct Tokens {
     }
 };
 
-enum What { kSums, kBackSums, kForward, kBackward };
+// The map of a tile, as other workgroups read it: A and e in one word, so that it is
+// there as a whole or not at all.
+__device__ __forceinline__ void publish(uint64_t* at, const Map& m) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        // (No NaN of a caller's looks like a map that is not there yet.)
+        const uint32_t A = m.A[k] != m.A[k] ? 0x7fc00000u : __float_as_uint(m.A[k]);
+        __hip_atomic_store(at + k, (uint64_t)__float_as_uint(m.e[k]) << 32 | A, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+}
+__device__ __forceinline__ Map await(const uint64_t* at, bool live) {
+    uint64_t w[4];
+    for (int32_t n = 0;; ++n) {
+        bool there = true;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            w[k] = __hip_atomic_load(at + k, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            there &= (uint32_t)w[k] != (uint32_t)kNotReady;
+        }
+        if (__ballot(live && !there) == 0 || n == kMostPolls) break;
+        __builtin_amdgcn_s_sleep(1);
+    }
+    Map m;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        m.A[k] = __uint_as_float((uint32_t)w[k]);
+        m.e[k] = __uint_as_float((uint32_t)(w[k] >> 32));  // (NaN where nothing came, as A)
+    }
+    return m;
+}
 
-template <typename TI, int L, int NW, int WHAT>
-__global__ __launch_bounds__(64 * NW) void scan_kernel(Scan a) {
-    constexpr bool BACK = WHAT == kBackward, REVERSE = BACK || WHAT == kBackSums;
+template <typename TI, int L, int NW, bool BACK>
+__global__ __launch_bounds__(64 * NW, 4) void scan_kernel(Scan a) {
+    constexpr int TILE = L * NW;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int32_t blocks = (a.C + kChannels - 1) / kChannels;
-    const int64_t tile = blockIdx.x / blocks;
-    const int32_t c = (int32_t)(blockIdx.x - tile * blocks) * kChannels + 4 * lane, ch = c < a.C ? c : 0;
+    __shared__ uint32_t s_ticket;
+    // A workgroup waits for tiles before its own only (behind it, in the backward
+    // pass): their workgroups have begun, since tiles are dealt out in that order.
+    uint32_t ticket = blockIdx.x;
+    if (a.maps) {
+        if (threadIdx.x == 0) s_ticket = atomicAdd(a.tickets, 1u);
+        __syncthreads();
+        ticket = __builtin_amdgcn_readfirstlane(s_ticket);
+    }
+    const int64_t place = ticket / (uint32_t)blocks, tile = BACK ? a.tiles - 1 - place : place;
+    const int32_t c = (int32_t)(ticket - (uint32_t)place * (uint32_t)blocks) * kChannels + 4 * lane, ch = c < a.C ? c : 0;
     const bool live = c < a.C;
     int64_t end = a.cu[a.num_seqs];
     end = end < a.T ? end : a.T;
-    const int64_t first = tile * (L * NW) + wave * L;
+    const int64_t first = tile * TILE + wave * L;
     const floatx4 zero = {0.f, 0.f, 0.f, 0.f};
 
-    if (tile * (L * NW) < end) {  // of the whole workgroup
-        Four<TI> x[L], dh[REVERSE ? L : 1];
+    if (tile * TILE < end) {  // of the whole workgroup
+        Four<TI> x[L], dh[BACK ? L : 1];
         floatx4 g[L];
 #pragma unroll
         for (int i = 0; i < L; ++i) {
             const int64_t at = (first + i < end ? first + i : end - 1) * a.C + ch;
             g[i] = *reinterpret_cast<const floatx4*>(a.g + at);
-            if (WHAT != kBackSums) x[i].v = *reinterpret_cast<const typename Four<TI>::raw*>(static_cast<const TI*>(a.x) + at);
-            if (REVERSE) dh[i].v = *reinterpret_cast<const typename Four<TI>::raw*>(static_cast<const TI*>(a.dh) + at);
+            x[i].v = *reinterpret_cast<const typename Four<TI>::raw*>(static_cast<const TI*>(a.x) + at);
+            if (BACK) dh[i].v = *reinterpret_cast<const typename Four<TI>::raw*>(static_cast<const TI*>(a.dh) + at);
         }
         const Tokens<L> tokens(a, first, end);
         auto vector = [&](const float* v, int i) {  // of token i's sequence
@@ -174,12 +216,10 @@ __global__ __launch_bounds__(64 * NW) void scan_kernel(Scan a) {
             return s;
         };
         auto before = [&](floatx4 s, int i, floatx4& l) {  // c of token i from the next token's
-            floatx4 al, om;
-            gate(i, al, om);
             if (tokens.ends >> i & 1) s = vector(a.d_final, i);
             l = dh[i].f() + s;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) s[k] = al[k] * l[k];
+            for (int k = 0; k < 4; ++k) s[k] = decay(g[i][k]) * l[k];
             return s;
         };
         // What the wave's tokens do to a state, or to the gradient that comes from behind.
@@ -201,22 +241,45 @@ __global__ __launch_bounds__(64 * NW) void scan_kernel(Scan a) {
             for (int k = 0; k < 4; ++k) m.A[k] = constant ? -1.f : m.A[k] < 0x1p-149f ? 0x1p-149f : m.A[k];
             return m;
         };
-        __shared__ Map maps[2][NW][64];
-        if (WHAT != kBackSums) maps[0][wave][lane] = wave_map(false);
-        if (REVERSE) maps[1][wave][lane] = wave_map(true);
-        __syncthreads();
-        if (WHAT == kSums || WHAT == kBackSums) {
-            if (wave > 0 || !live) return;
-            Map m = Map::identity();
+        __shared__ Map s_map[BACK ? 2 : 1][NW][64], s_before[NW][64];
+        s_map[0][wave][lane] = wave_map(false);
+        if (BACK) s_map[1][wave][lane] = wave_map(true);
+        // What is computed again below is not kept until then: the registers are the tokens'.
 #pragma unroll
-            for (int w = 0; w < NW; ++w) m = maps[REVERSE][REVERSE ? NW - 1 - w : w][lane].after(m);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) a.maps[tile * a.C + c + k] = floatx2{m.A[k], m.e[k]};
-            return;
+        for (int i = 0; i < L; ++i) {
+            asm volatile("" : "+v"(g[i]));
+            asm volatile("" : "+v"(x[i].v));
+            if (BACK) asm volatile("" : "+v"(dh[i].v));
         }
-        floatx4 s = *reinterpret_cast<const floatx4*>(a.states + tile * a.C + ch);
-        for (int w = 0; w < wave; ++w) s = maps[0][w][lane].of(s);
+        __syncthreads();
+        floatx4 s = zero;  // what comes into the tile
+        if (a.maps) {
+            // Tiles in the order in which this pass comes to them, in groups of NW.
+            const int64_t last = (end + TILE - 1) / TILE - 1, nth = BACK ? last - tile : tile, group = nth / NW;
+            const int in_group = (int)(nth - group * NW);
+            auto word = [&](int64_t n) { return a.maps + (BACK ? last - n : n) * a.C + ch; };
+            uint64_t* const entry = a.maps + (a.tiles + group) * a.C + ch;
+            Map own = Map::identity();
+            if (wave == 0) {
+#pragma unroll
+                for (int w = 0; w < NW; ++w) own = s_map[BACK][BACK ? NW - 1 - w : w][lane].after(own);
+                if (live) publish(word(nth), own);
+            }
+            // A wave waits for one of the maps before it in the group, the last for the
+            // group's entry: the order of the sums is always the same.
+            if (wave < in_group) s_before[wave][lane] = await(word(group * NW + wave), live);
+            if (wave == NW - 1 && group > 0) s_before[wave][lane] = await(entry, live);
+            __syncthreads();
+            if (group > 0) s = s_before[NW - 1][lane].e;
+            for (int w = 0; w < in_group; ++w) s = s_before[w][lane].of(s);
+            if (wave == 0 && in_group == NW - 1 && live) publish(entry + a.C, Map{floatx4{1.f, 1.f, 1.f, 1.f}, own.of(s)});
+        }
+        floatx4 r = s;  // the gradient, where s is the state
+        if (BACK) s = *reinterpret_cast<const floatx4*>(a.states + tile * (TILE / kCheck) * a.C + ch);
+        for (int w = 0; w < wave; ++w) s = s_map[0][w][lane].of(s);
         if (!BACK) {
+            if (a.states && live && first % kCheck == 0 && first < end) *reinterpret_cast<floatx4*>(a.states + first / kCheck * a.C + c) = s;
+            if (!a.h) return;
 #pragma unroll
             for (int i = 0; i < L; ++i) {
                 if (i >= tokens.live) continue;
@@ -233,8 +296,7 @@ __global__ __launch_bounds__(64 * NW) void scan_kernel(Scan a) {
                 s = next(s, i);
                 if (a.mix) past[i] -= x[i].f();
             }
-            floatx4 r = *reinterpret_cast<const floatx4*>(a.carry + tile * a.C + ch);
-            for (int w = NW - 1; w > wave; --w) r = maps[1][w][lane].of(r);
+            for (int w = NW - 1; w > wave; --w) r = s_map[1][w][lane].of(r);
 #pragma unroll
             for (int i = L - 1; i >= 0; --i) {
                 if (i >= tokens.live) continue;
@@ -252,90 +314,80 @@ __global__ __launch_bounds__(64 * NW) void scan_kernel(Scan a) {
     // Sequences without a token keep their state, or its gradient.
     float* const to = BACK ? a.d_init : a.final;
     const float* const from = BACK ? a.d_final : a.init;
-    if (tile > 0 || !to || !live || WHAT == kSums || WHAT == kBackSums) return;
+    if (tile > 0 || !to || !live) return;
     for (int32_t m = wave; m < a.num_seqs; m += NW)
         if (a.cu[m + 1] <= a.cu[m])
             *reinterpret_cast<floatx4*>(to + (int64_t)m * a.C + c) = from ? *reinterpret_cast<const floatx4*>(from + (int64_t)m * a.C + c) : zero;
 }
 
-// The states before the tiles, or the gradients behind them, from the tiles' maps.
-template <bool REVERSE>
-__global__ __launch_bounds__(64) void fold_kernel(Scan a, int tokens) {
-    const int32_t c = blockIdx.x * 64 + threadIdx.x;
-    if (c >= a.C) return;
-    int64_t end = a.cu[a.num_seqs];
-    end = end < a.T ? end : a.T;
-    const int64_t used = (end + tokens - 1) / tokens;
-    float s = 0.f;
-    float* const to = REVERSE ? a.carry : a.states;
-    for (int64_t j = 0; j < used; ++j) {
-        const int64_t tile = REVERSE ? used - 1 - j : j;
-        const floatx2 m = a.maps[tile * a.C + c];
-        to[tile * a.C + c] = s;
-        s = m[0] < 0.f ? m[1] : __builtin_fmaf(m[0], s, m[1]);
+// No map is there yet, and no workgroup has begun.
+__global__ __launch_bounds__(256) void begin_kernel(uint64_t* maps, uint32_t* tickets, int64_t words) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) *tickets = 0;
+    for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 2; i < words; i += (int64_t)gridDim.x * 512) {
+        typedef uint64_t two __attribute__((ext_vector_type(2)));
+        *reinterpret_cast<two*>(maps + i) = two{kNotReady, kNotReady};  // (an even number of words)
     }
 }
 
-constexpr int kL = 8, kNW = 8, kTile = kL * kNW;
+constexpr int kWaves = 8;
+template <typename TI, bool BACK>
+constexpr int kTokens = BACK || sizeof(TI) == 4 ? 8 : 16;  // of a wave
 
-int64_t tiles_of(int64_t T) { return (T + kTile - 1) / kTile; }
+int64_t up(int64_t x, int64_t y) { return (x + y - 1) / y; }
 size_t rounded(size_t bytes) { return (bytes + 255) & ~(size_t)255; }
+// Tiles of kCheck tokens at least, and their groups.
+int64_t map_words(int64_t tiles, int32_t C) { return (tiles + tiles / kWaves + 1) * C; }
+size_t maps_bytes(int64_t T, int32_t C) { return rounded((size_t)map_words(up(T, kCheck), C) * sizeof(uint64_t)) + 256; }
 
 Scan arguments(const ScanLaunch& p) {
     Scan a = {};
     a.x = p.x; a.g = p.g; a.cu = p.cu_seqlens; a.num_seqs = p.num_seqs; a.T = p.T; a.C = p.C; a.mix = p.mix;
     a.init = p.initial_state; a.final = p.final_state; a.h = p.h; a.dh = p.d_h; a.d_final = p.d_final_state;
     a.dx = p.dx; a.dg = p.dg; a.d_init = p.d_initial_state;
-    a.tiles = std::max<int64_t>(tiles_of(p.T), 1);
+    a.tickets = static_cast<uint32_t*>(p.workspace);
+    a.maps = reinterpret_cast<uint64_t*>(static_cast<char*>(p.workspace) + 256);
     return a;
 }
-template <int WHAT>
-hipError_t run(const Scan& a, bool half, hipStream_t s) {
-    const unsigned blocks = (unsigned)(a.tiles * ((a.C + kChannels - 1) / kChannels));
-    if (half) hipLaunchKernelGGL((scan_kernel<bf16, kL, kNW, WHAT>), dim3(blocks), dim3(64 * kNW), 0, s, a);
-    else hipLaunchKernelGGL((scan_kernel<float, kL, kNW, WHAT>), dim3(blocks), dim3(64 * kNW), 0, s, a);
-    return hipGetLastError();
-}
-template <bool REVERSE>
-hipError_t fold(const Scan& a, hipStream_t s) {
-    hipLaunchKernelGGL(fold_kernel<REVERSE>, dim3((a.C + 63) / 64), dim3(64), 0, s, a, kTile);
+template <typename TI, bool BACK>
+hipError_t run(Scan a, hipStream_t s) {
+    constexpr int L = kTokens<TI, BACK>;
+    a.tiles = std::max<int64_t>(up(a.T, L * kWaves), 1);
+    if (a.tiles == 1) {
+        a.maps = nullptr;
+    } else {
+        const int64_t words = map_words(a.tiles, a.C);
+        hipLaunchKernelGGL(begin_kernel, dim3((unsigned)std::min<int64_t>(up(words, 512), 4096)), dim3(256), 0, s, a.maps, a.tickets, words);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    const dim3 grid((unsigned)(a.tiles * up(a.C, kChannels)));
+    hipLaunchKernelGGL((scan_kernel<TI, L, kWaves, BACK>), grid, dim3(64 * kWaves), 0, s, a);
     return hipGetLastError();
 }
 
 }  // namespace
 
-size_t scan_checkpoint_bytes(int64_t T, int32_t C) { return (size_t)tiles_of(T) * C * sizeof(float); }
-size_t scan_workspace_bytes(int64_t T, int32_t C) {
-    return rounded((size_t)tiles_of(T) * C * sizeof(floatx2)) + rounded(scan_checkpoint_bytes(T, C));
-}
-size_t scan_backward_workspace_bytes(int64_t T, int32_t C) { return scan_workspace_bytes(T, C) + rounded(scan_checkpoint_bytes(T, C)); }
+size_t scan_checkpoint_bytes(int64_t T, int32_t C) { return (size_t)up(T, kCheck) * C * sizeof(float); }
+size_t scan_workspace_bytes(int64_t T, int32_t C) { return maps_bytes(T, C); }
+size_t scan_backward_workspace_bytes(int64_t T, int32_t C) { return maps_bytes(T, C) + rounded(scan_checkpoint_bytes(T, C)); }
 
 hipError_t launch_scan(const ScanLaunch& p, hipStream_t s) {
     if (p.num_seqs == 0) return hipSuccess;
     Scan a = arguments(p);
-    char* at = static_cast<char*>(p.workspace);
-    a.maps = reinterpret_cast<floatx2*>(at);
-    a.states = p.checkpoints ? p.checkpoints : reinterpret_cast<float*>(at + rounded((size_t)tiles_of(p.T) * p.C * sizeof(floatx2)));
-    hipError_t e;
-    if ((e = run<kSums>(a, p.bf16, s)) != hipSuccess || (e = fold<false>(a, s)) != hipSuccess) return e;
-    return run<kForward>(a, p.bf16, s);
+    a.states = p.checkpoints;
+    return p.bf16 ? run<bf16, false>(a, s) : run<float, false>(a, s);
 }
 
 hipError_t launch_scan_backward(const ScanLaunch& p, hipStream_t s) {
     if (p.num_seqs == 0) return hipSuccess;
     Scan a = arguments(p);
-    char* at = static_cast<char*>(p.workspace);
-    a.maps = reinterpret_cast<floatx2*>(at);
-    at += rounded((size_t)tiles_of(p.T) * p.C * sizeof(floatx2));
-    a.carry = reinterpret_cast<float*>(at);
-    hipError_t e;
     a.states = p.checkpoints;
     if (!p.checkpoints) {
-        a.states = reinterpret_cast<float*>(at + rounded(scan_checkpoint_bytes(p.T, p.C)));
-        if ((e = run<kSums>(a, p.bf16, s)) != hipSuccess || (e = fold<false>(a, s)) != hipSuccess) return e;
+        a.states = reinterpret_cast<float*>(static_cast<char*>(p.workspace) + maps_bytes(p.T, p.C));
+        const hipError_t e = p.bf16 ? run<bf16, false>(a, s) : run<float, false>(a, s);
+        if (e != hipSuccess) return e;
     }
-    if ((e = run<kBackSums>(a, p.bf16, s)) != hipSuccess || (e = fold<true>(a, s)) != hipSuccess) return e;
-    return run<kBackward>(a, p.bf16, s);
+    return p.bf16 ? run<bf16, true>(a, s) : run<float, true>(a, s);
 }
 
 }  // namespace gdn
