@@ -10,13 +10,15 @@ __device__ __forceinline__ float decay(float g) { return __builtin_amdgcn_exp2f(
 // 1 - e^g without the difference's loss near g = 0: there by the exponential's
 // series, whose next term is below 2^-25 of the sum.
 __device__ __forceinline__ float one_minus_decay(float g, float a) {
-    float p = 1.f + g * (1.f / 7.f);
-    p = 1.f + g * (1.f / 6.f) * p;
-    p = 1.f + g * (1.f / 5.f) * p;
-    p = 1.f + g * (1.f / 4.f) * p;
-    p = 1.f + g * (1.f / 3.f) * p;
-    p = 1.f + g * (1.f / 2.f) * p;
-    return g > -0.35f ? -g * p : 1.f - a;
+    float p = __builtin_fmaf(g, 1.f / 5040.f, 1.f / 720.f);
+    p = __builtin_fmaf(g, p, 1.f / 120.f);
+    p = __builtin_fmaf(g, p, 1.f / 24.f);
+    p = __builtin_fmaf(g, p, 1.f / 6.f);
+    p = __builtin_fmaf(g, p, 0.5f);
+    p = __builtin_fmaf(g, p, 1.f);
+    p *= -g;
+    asm("" : "+v"(p));  // (no branch around it: both sides are a few operations)
+    return g > -0.35f ? p : 1.f - a;
 }
 
 // Four neighbouring values as they are in memory.

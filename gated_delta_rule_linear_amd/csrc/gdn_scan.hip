@@ -30,7 +30,6 @@ struct Scan {
     int32_t num_seqs;
     int64_t T;
     int32_t C;
-    bool mix;
     const float* init;
     float* final;
     void* h;
@@ -39,12 +38,14 @@ struct Scan {
     void* dx;
     float *dg, *d_init;
     float* states;      // [T / kCheck][C] state before every kCheck tokens, or NULL
-    uint64_t* maps;     // [tiles][C] maps of the tiles, and [groups][C] what comes into a group of them (NULL: one tile)
+    uint64_t* maps;     // [tiles][blocks][4][64] maps of the tiles, and [groups][blocks][4][64] what comes into a group of
+                        // them: a lane's four channels are 64 words apart (NULL: one tile)
     uint32_t* tickets;  // workgroups that have begun
     int64_t tiles;
 };
 
 constexpr int kCheck = 64;
+constexpr int kEach = 1;
 constexpr uint64_t kNotReady = ~0ull;       // of a tile's map
 constexpr int32_t kMostPolls = 1 << 22;     // seconds: no wait is without end, whatever happened
 
@@ -74,58 +75,78 @@ struct Map {
 // A wave's tokens: where sequences start and end among them.
 template <int L>
 struct Tokens {
-    int64_t first;
     int32_t live;           // tokens that exist
     uint32_t starts, ends;  // bits of the tokens that begin or end a sequence
-    const int32_t* cu;
-    int32_t n;              // sequences
-    int32_t base, bound;    // the last offset at or before the first token, and a lane's of the 64 from there on
+    int32_t number;         // lane i: the sequence of token i, if there is such a bit
 
-    // The last offset's number at or before token t (offsets that decrease give some number).
-    __device__ __forceinline__ int32_t last_at(int64_t t) const {
+    // The number of the last offset at or before token t (offsets that decrease give some number).
+    __device__ __forceinline__ static int32_t last_at(const int32_t* cu, int32_t n, int64_t t) {
         int32_t lo = 0, hi = n + 1;
         const int lane = threadIdx.x & 63;
-        while (hi - lo > 64) {
+        for (;;) {
             const int32_t step = (hi - lo + 63) / 64, at = lo + lane * step;
             const int c = __popcll(__ballot(at < hi && cu[at < hi ? at : lo] <= t));
+            if (step <= 1) return lo + c - 1;
             if (c > 1) lo += (c - 1) * step;
             hi = hi < lo + step ? hi : lo + step;
         }
-        const int32_t at = lo + lane;
-        return lo + __popcll(__ballot(at < hi && cu[at < hi ? at : lo] <= t)) - 1;
     }
-    __device__ __forceinline__ Tokens(const Scan& a, int64_t first_, int64_t end) : first(first_), cu(a.cu), n(a.num_seqs) {
-        live = end - first < L ? (int32_t)(end - first) : L;
-        starts = ends = 0;
-        if (live <= 0) return;
-        base = last_at(first);
-        if (base < 0) base = 0;
-        const int32_t at = base + (int32_t)(threadIdx.x & 63);
-        bound = at <= n ? cu[at] : INT32_MAX;
-        const int64_t off = bound - first;
+    __device__ __forceinline__ Tokens(const Scan& a, int64_t first, int64_t end) {
+        const int32_t* const cu = a.cu;
+        const int32_t n = a.num_seqs, lane = threadIdx.x & 63, some = end - first < L ? (int32_t)(end - first) : L;
+        uint32_t begin = 0, stop = 0;
+        number = 0;
+        if (some > 0) {
+            int32_t base = last_at(cu, n, first);
+            if (base < 0) base = 0;
+            const int32_t at = base + lane, bound = at <= n ? cu[at] : INT32_MAX;
+            const int64_t off = bound - first;
 #pragma unroll
-        for (int i = 0; i <= L; ++i) {
-            if (__ballot(off == i) == 0) continue;
-            if (i < L) starts |= 1u << i;
-            if (i > 0) ends |= 1u << (i - 1);
-        }
-        if (__builtin_amdgcn_readlane(bound, 63) <= first + L && base + 63 < n) {  // more empty sequences than lanes
-            for (int i = 0; i <= live; ++i) {
-                const int32_t m = last_at(first + i);
-                if (m < 0 || cu[m] != first + i) continue;
-                if (i < L) starts |= 1u << i;
-                if (i > 0) ends |= 1u << (i - 1);
+            for (int i = 0; i <= L; ++i) {
+                if (__ballot(off == i) == 0) continue;
+                if (i < L) begin |= 1u << i;
+                if (i > 0) stop |= 1u << (i - 1);
             }
+            const bool crowded = __builtin_amdgcn_readlane(bound, 63) <= first + L && base + 63 < n;  // more empty sequences than lanes
+            if (crowded) {
+#pragma unroll 1
+                for (int i = 0; i <= some; ++i) {
+                    const int32_t m = last_at(cu, n, first + i);
+                    if (lane == i) number = m;
+                    if (m < 0 || cu[m] != first + i) continue;
+                    if (i < L) begin |= 1u << i;
+                    if (i > 0) stop |= 1u << (i - 1);
+                }
+            }
+            if (first + some == end) stop |= 1u << (some - 1);
+            begin &= (2u << (some - 1)) - 1;
+            stop &= (2u << (some - 1)) - 1;
+            if ((begin | stop) && !crowded) {
+#pragma unroll 1
+                for (int i = 0; i < some; ++i) {
+                    const int32_t m = base + __popcll(__ballot(off <= i)) - 1;
+                    if (lane == i) number = m;
+                }
+            }
+            number = number < 0 ? 0 : number < n ? number : n - 1;
         }
-        if (first + live == end) ends |= 1u << (live - 1);
-        starts &= live < 32 ? (1u << live) - 1 : ~0u;
-        ends &= live < 32 ? (1u << live) - 1 : ~0u;
+        live = __builtin_amdgcn_readfirstlane(some);
+        starts = __builtin_amdgcn_readfirstlane(begin);
+        ends = __builtin_amdgcn_readfirstlane(stop);
     }
-    // The sequence of token i.
-    __device__ __forceinline__ int32_t sequence(int i) const {
-        const int32_t m = last_at(first + i);
-        return m < 0 ? 0 : m < n ? m : n - 1;
+    // (Tested where it is asked: 2 L conditions known ahead would take up the scalar registers.)
+    __device__ __forceinline__ static bool bit(uint32_t bits, int i) {
+        asm volatile("" : "+s"(bits));
+        return bits >> i & 1;
     }
+    __device__ __forceinline__ bool starts_at(int i) const { return bit(starts, i); }
+    __device__ __forceinline__ bool ends_at(int i) const { return bit(ends, i); }
+    __device__ __forceinline__ bool there(int i) const {
+        int32_t n = live;
+        asm volatile("" : "+s"(n));
+        return i < n;
+    }
+    __device__ __forceinline__ int32_t sequence(int i) const { return __builtin_amdgcn_readlane(number, i); }
 };
 
 // The map of a tile, as other workgroups read it: A and e in one word, so that it is
@@ -135,35 +156,62 @@ __device__ __forceinline__ void publish(uint64_t* at, const Map& m) {
     for (int k = 0; k < 4; ++k) {
         // (No NaN of a caller's looks like a map that is not there yet.)
         const uint32_t A = m.A[k] != m.A[k] ? 0x7fc00000u : __float_as_uint(m.A[k]);
-        __hip_atomic_store(at + k, (uint64_t)__float_as_uint(m.e[k]) << 32 | A, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        __hip_atomic_store(at + 64 * k, (uint64_t)__float_as_uint(m.e[k]) << 32 | A, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
 }
-__device__ __forceinline__ Map await(const uint64_t* at, bool live) {
-    uint64_t w[4];
-    for (int32_t n = 0;; ++n) {
-        bool there = true;
+// N maps joined, `step` words apart, as they come: the first `count` of them, the
+// first of all at `one`.
+template <int N>
+__device__ __forceinline__ Map await(const uint64_t* one, int64_t step, int count, bool live) {
+    const uint64_t* const at = one + (threadIdx.x & 63);
+    uint64_t w[N][4];
+    for (int32_t polls = 0;;) {
+        int missing = N;
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            if (j < count) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) w[j][k] = __hip_atomic_load(at + j * step + 64 * k, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            }
+        }
+#pragma unroll
+        for (int j = N - 1; j >= 0; --j) {
+            bool there = true;
+            if (j < count) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) there &= (uint32_t)w[j][k] != (uint32_t)kNotReady;
+            }
+            if (__ballot(live && !there)) missing = j;
+        }
+        if (missing == N || polls >= kMostPolls) break;
+        // All lanes wait for one word, one line instead of 32: the polls of whole waves
+        // get in the way of those that write what they wait for.
+        const uint64_t* const first = one + missing * step;
+        do {
+            __builtin_amdgcn_s_sleep(1);
+        } while (++polls < kMostPolls && (uint32_t)__hip_atomic_load(first, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == (uint32_t)kNotReady);
+    }
+    Map m = Map::identity();
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        if (j >= count) continue;
+        Map next;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            w[k] = __hip_atomic_load(at + k, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            there &= (uint32_t)w[k] != (uint32_t)kNotReady;
+            next.A[k] = __uint_as_float((uint32_t)w[j][k]);
+            next.e[k] = __uint_as_float((uint32_t)(w[j][k] >> 32));  // (NaN where nothing came, as A)
         }
-        if (__ballot(live && !there) == 0 || n == kMostPolls) break;
-        __builtin_amdgcn_s_sleep(1);
-    }
-    Map m;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        m.A[k] = __uint_as_float((uint32_t)w[k]);
-        m.e[k] = __uint_as_float((uint32_t)(w[k] >> 32));  // (NaN where nothing came, as A)
+        m = next.after(m);
     }
     return m;
 }
 
-template <typename TI, int L, int NW, bool BACK>
+template <typename TI, int L, int NW, bool BACK, bool MIX>
 __global__ __launch_bounds__(64 * NW, 4) void scan_kernel(Scan a) {
-    constexpr int TILE = L * NW;
+    constexpr int TILE = L * NW, GROUP = NW * kEach;
+    static_assert(TILE % kCheck == 0, "tiles hold whole spans of checkpoints; the workspace is sized by them");
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int32_t blocks = (a.C + kChannels - 1) / kChannels;
+    const int32_t blocks = (a.C + kChannels - 1) / kChannels, held = a.cu[a.num_seqs];
     __shared__ uint32_t s_ticket;
     // A workgroup waits for tiles before its own only (behind it, in the backward
     // pass): their workgroups have begun, since tiles are dealt out in that order.
@@ -174,11 +222,10 @@ __global__ __launch_bounds__(64 * NW, 4) void scan_kernel(Scan a) {
         ticket = __builtin_amdgcn_readfirstlane(s_ticket);
     }
     const int64_t place = ticket / (uint32_t)blocks, tile = BACK ? a.tiles - 1 - place : place;
-    const int32_t c = (int32_t)(ticket - (uint32_t)place * (uint32_t)blocks) * kChannels + 4 * lane, ch = c < a.C ? c : 0;
+    const int32_t block = (int32_t)(ticket - (uint32_t)place * (uint32_t)blocks), c = block * kChannels + 4 * lane;
+    const uint32_t ch = c < a.C ? c : 0;
     const bool live = c < a.C;
-    int64_t end = a.cu[a.num_seqs];
-    end = end < a.T ? end : a.T;
-    const int64_t first = tile * TILE + wave * L;
+    const int64_t end = __builtin_amdgcn_readfirstlane(held < a.T ? held : (int32_t)a.T), first = tile * TILE + wave * L;
     const floatx4 zero = {0.f, 0.f, 0.f, 0.f};
 
     if (tile * TILE < end) {  // of the whole workgroup
@@ -186,55 +233,73 @@ __global__ __launch_bounds__(64 * NW, 4) void scan_kernel(Scan a) {
         floatx4 g[L];
 #pragma unroll
         for (int i = 0; i < L; ++i) {
-            const int64_t at = (first + i < end ? first + i : end - 1) * a.C + ch;
-            g[i] = *reinterpret_cast<const floatx4*>(a.g + at);
-            x[i].v = *reinterpret_cast<const typename Four<TI>::raw*>(static_cast<const TI*>(a.x) + at);
-            if (BACK) dh[i].v = *reinterpret_cast<const typename Four<TI>::raw*>(static_cast<const TI*>(a.dh) + at);
+            const int64_t at = (first + i < end ? first + i : end - 1) * a.C;
+            g[i] = *reinterpret_cast<const floatx4*>(a.g + at + ch);
+            x[i].v = *reinterpret_cast<const typename Four<TI>::raw*>(static_cast<const TI*>(a.x) + at + ch);
+            if (BACK) dh[i].v = *reinterpret_cast<const typename Four<TI>::raw*>(static_cast<const TI*>(a.dh) + at + ch);
         }
         const Tokens<L> tokens(a, first, end);
+        if (tokens.live < L) {  // tokens that are none change nothing
+#pragma unroll
+            for (int i = 0; i < L; ++i)
+                if (i >= tokens.live) {
+                    g[i] = zero;
+                    x[i] = {};
+                    if (BACK) dh[i] = {};
+                }
+        }
+        // (What is loaded where a sequence begins or ends is waited for there: behind it
+        // the wait would be every token's, and for the stores before it too.)
         auto vector = [&](const float* v, int i) {  // of token i's sequence
-            return v ? *reinterpret_cast<const floatx4*>(v + (int64_t)tokens.sequence(i) * a.C + ch) : zero;
+            floatx4 y = zero;
+            if (v) {
+                y = *reinterpret_cast<const floatx4*>(v + (int64_t)tokens.sequence(i) * a.C + ch);
+                asm volatile("" : "+v"(y));
+            }
+            return y;
         };
         auto put = [&](float* v, int i, floatx4 y) {
-            const int64_t m = tokens.sequence(i);  // (of all lanes)
-            if (live) *reinterpret_cast<floatx4*>(v + m * a.C + c) = y;
-        };
-        auto gate = [&](int i, floatx4& al, floatx4& om) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                al[k] = decay(g[i][k]);
-                om[k] = a.mix ? one_minus_decay(g[i][k], al[k]) : 1.f;
-            }
+            if (live) *reinterpret_cast<floatx4*>(v + (int64_t)tokens.sequence(i) * a.C + ch) = y;
         };
         auto next = [&](floatx4 s, int i) {  // the state after token i
-            floatx4 al, om;
-            gate(i, al, om);
-            if (tokens.starts >> i & 1) s = vector(a.init, i);
+            if (tokens.starts_at(i)) s = vector(a.init, i);
             const floatx4 in = x[i].f();
 #pragma unroll
-            for (int k = 0; k < 4; ++k) s[k] = __builtin_fmaf(al[k], s[k], om[k] * in[k]);
+            for (int k = 0; k < 4; ++k) {
+                const float al = decay(g[i][k]);
+                s[k] = __builtin_fmaf(al, s[k], MIX ? one_minus_decay(g[i][k], al) * in[k] : in[k]);
+            }
             return s;
         };
         auto before = [&](floatx4 s, int i, floatx4& l) {  // c of token i from the next token's
-            if (tokens.ends >> i & 1) s = vector(a.d_final, i);
+            if (tokens.ends_at(i)) s = vector(a.d_final, i);
             l = dh[i].f() + s;
 #pragma unroll
             for (int k = 0; k < 4; ++k) s[k] = decay(g[i][k]) * l[k];
             return s;
         };
+        // What is computed again for another pass over the tokens is not kept until then,
+        // nor is it computed ahead of its token: the registers are the inputs'.
+        auto forget = [&]() {
+#pragma unroll
+            for (int i = 0; i < L; ++i) {
+                asm volatile("" : "+v"(g[i]));
+                asm volatile("" : "+v"(x[i].v));
+                if (BACK) asm volatile("" : "+v"(dh[i].v));
+            }
+        };
         // What the wave's tokens do to a state, or to the gradient that comes from behind.
         auto wave_map = [&](bool reverse) {
             Map m = Map::identity();
 #pragma unroll
-            for (int i = 0; i < L; ++i)
-                if (i < tokens.live)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) m.A[k] *= decay(g[i][k]);
-#pragma unroll
             for (int j = 0; j < L; ++j) {
                 const int i = reverse ? L - 1 - j : j;
                 floatx4 l;
-                if (i < tokens.live) m.e = reverse ? before(m.e, i, l) : next(m.e, i);
+                m.e = reverse ? before(m.e, i, l) : next(m.e, i);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) m.A[k] *= decay(g[i][k]);
+                asm volatile("" : "+v"(m.A));  // (here, not where a branch needs it)
+                __builtin_amdgcn_sched_barrier(0);
             }
             const bool constant = (reverse ? tokens.ends : tokens.starts) != 0;
 #pragma unroll
@@ -242,72 +307,88 @@ __global__ __launch_bounds__(64 * NW, 4) void scan_kernel(Scan a) {
             return m;
         };
         __shared__ Map s_map[BACK ? 2 : 1][NW][64], s_before[NW][64];
+        __shared__ floatx4 s_entry[64];
         s_map[0][wave][lane] = wave_map(false);
-        if (BACK) s_map[1][wave][lane] = wave_map(true);
-        // What is computed again below is not kept until then: the registers are the tokens'.
-#pragma unroll
-        for (int i = 0; i < L; ++i) {
-            asm volatile("" : "+v"(g[i]));
-            asm volatile("" : "+v"(x[i].v));
-            if (BACK) asm volatile("" : "+v"(dh[i].v));
+        forget();
+        if (BACK) {
+            s_map[1][wave][lane] = wave_map(true);
+            forget();
         }
         __syncthreads();
         floatx4 s = zero;  // what comes into the tile
         if (a.maps) {
-            // Tiles in the order in which this pass comes to them, in groups of NW.
-            const int64_t last = (end + TILE - 1) / TILE - 1, nth = BACK ? last - tile : tile, group = nth / NW;
-            const int in_group = (int)(nth - group * NW);
-            auto word = [&](int64_t n) { return a.maps + (BACK ? last - n : n) * a.C + ch; };
-            uint64_t* const entry = a.maps + (a.tiles + group) * a.C + ch;
+            // Tiles in the order in which this pass comes to them, in groups.
+            const int64_t last = (end + TILE - 1) / TILE - 1, nth = BACK ? last - tile : tile, group = nth / GROUP, begin = group * GROUP;
+            const int in_group = (int)(nth - begin);
+            auto words = [&](int64_t n) { return a.maps + (n * blocks + block) * kChannels; };
             Map own = Map::identity();
             if (wave == 0) {
-#pragma unroll
+#pragma unroll 2
                 for (int w = 0; w < NW; ++w) own = s_map[BACK][BACK ? NW - 1 - w : w][lane].after(own);
-                if (live) publish(word(nth), own);
+                if (live) publish(words(tile) + lane, own);
             }
-            // A wave waits for one of the maps before it in the group, the last for the
-            // group's entry: the order of the sums is always the same.
-            if (wave < in_group) s_before[wave][lane] = await(word(group * NW + wave), live);
-            if (wave == NW - 1 && group > 0) s_before[wave][lane] = await(entry, live);
+            // A wave waits for kEach of the group's maps before the tile's: the order of
+            // the sums is always the same.
+            const int mine = wave * kEach;
+            if (mine < in_group) {
+                const int64_t step = (int64_t)blocks * kChannels;
+                s_before[wave][lane] = await<kEach>(words(BACK ? last - begin - mine : begin + mine), BACK ? -step : step, in_group - mine, live);
+            }
             __syncthreads();
-            if (group > 0) s = s_before[NW - 1][lane].e;
-            for (int w = 0; w < in_group; ++w) s = s_before[w][lane].of(s);
-            if (wave == 0 && in_group == NW - 1 && live) publish(entry + a.C, Map{floatx4{1.f, 1.f, 1.f, 1.f}, own.of(s)});
+            // What comes into the group matters where no sequence begins (ends) before the tile.
+            bool open = true;
+            for (int w = 0; w * kEach < in_group; ++w) open &= !(s_before[w][0].A[0] < 0.f);
+            if (open && group > 0) {
+                if (wave == 0) s_entry[lane] = await<1>(words(a.tiles + group), 0, 1, live).e;
+                __syncthreads();
+                s = s_entry[lane];
+            }
+#pragma unroll 2
+            for (int w = 0; w * kEach < in_group; ++w) s = s_before[w][lane].of(s);
+            if (wave == 0 && in_group == GROUP - 1 && live)
+                publish(words(a.tiles + group + 1) + lane, Map{floatx4{1.f, 1.f, 1.f, 1.f}, own.of(s)});
         }
         floatx4 r = s;  // the gradient, where s is the state
         if (BACK) s = *reinterpret_cast<const floatx4*>(a.states + tile * (TILE / kCheck) * a.C + ch);
+#pragma unroll 2
         for (int w = 0; w < wave; ++w) s = s_map[0][w][lane].of(s);
         if (!BACK) {
             if (a.states && live && first % kCheck == 0 && first < end) *reinterpret_cast<floatx4*>(a.states + first / kCheck * a.C + c) = s;
             if (!a.h) return;
 #pragma unroll
             for (int i = 0; i < L; ++i) {
-                if (i >= tokens.live) continue;
                 s = next(s, i);
-                if (live) *reinterpret_cast<typename Four<TI>::raw*>(static_cast<TI*>(a.h) + (first + i) * a.C + c) = Four<TI>::of(s);
-                if (a.final && (tokens.ends >> i & 1)) put(a.final, i, s);
+                if (live && tokens.there(i)) *reinterpret_cast<typename Four<TI>::raw*>(static_cast<TI*>(a.h) + (first + i) * a.C + ch) = Four<TI>::of(s);
+                if (a.final && tokens.ends_at(i)) put(a.final, i, s);
+                __builtin_amdgcn_sched_barrier(0);
             }
         } else {
-            floatx4 past[L];
+            floatx4 past[L];  // h_{t-1} (- x_t)
 #pragma unroll
             for (int i = 0; i < L; ++i) {
-                if (i >= tokens.live) continue;
-                past[i] = tokens.starts >> i & 1 ? vector(a.init, i) : s;
+                past[i] = s;
+                if (tokens.starts_at(i)) past[i] = vector(a.init, i);
                 s = next(s, i);
-                if (a.mix) past[i] -= x[i].f();
+                if (MIX) past[i] -= x[i].f();
+                __builtin_amdgcn_sched_barrier(0);
             }
+            forget();
+#pragma unroll 2
             for (int w = NW - 1; w > wave; --w) r = s_map[1][w][lane].of(r);
 #pragma unroll
             for (int i = L - 1; i >= 0; --i) {
-                if (i >= tokens.live) continue;
-                floatx4 al, om, l;
-                gate(i, al, om);
+                floatx4 l;
                 r = before(r, i, l);
-                if (live) {
-                    *reinterpret_cast<typename Four<TI>::raw*>(static_cast<TI*>(a.dx) + (first + i) * a.C + c) = Four<TI>::of(om * l);
-                    *reinterpret_cast<floatx4*>(a.dg + (first + i) * a.C + c) = r * past[i];
+                const floatx4 dg = r * past[i];
+                if (MIX)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) l[k] *= one_minus_decay(g[i][k], decay(g[i][k]));
+                if (live && tokens.there(i)) {
+                    *reinterpret_cast<typename Four<TI>::raw*>(static_cast<TI*>(a.dx) + (first + i) * a.C + ch) = Four<TI>::of(l);
+                    *reinterpret_cast<floatx4*>(a.dg + (first + i) * a.C + ch) = dg;
                 }
-                if (a.d_init && (tokens.starts >> i & 1)) put(a.d_init, i, r);
+                if (a.d_init && tokens.starts_at(i)) put(a.d_init, i, r);
+                __builtin_amdgcn_sched_barrier(0);
             }
         }
     }
@@ -336,19 +417,19 @@ constexpr int kTokens = BACK || sizeof(TI) == 4 ? 8 : 16;  // of a wave
 int64_t up(int64_t x, int64_t y) { return (x + y - 1) / y; }
 size_t rounded(size_t bytes) { return (bytes + 255) & ~(size_t)255; }
 // Tiles of kCheck tokens at least, and their groups.
-int64_t map_words(int64_t tiles, int32_t C) { return (tiles + tiles / kWaves + 1) * C; }
+int64_t map_words(int64_t tiles, int32_t C) { return (tiles + tiles / (kWaves * kEach) + 1) * up(C, kChannels) * kChannels; }
 size_t maps_bytes(int64_t T, int32_t C) { return rounded((size_t)map_words(up(T, kCheck), C) * sizeof(uint64_t)) + 256; }
 
 Scan arguments(const ScanLaunch& p) {
     Scan a = {};
-    a.x = p.x; a.g = p.g; a.cu = p.cu_seqlens; a.num_seqs = p.num_seqs; a.T = p.T; a.C = p.C; a.mix = p.mix;
+    a.x = p.x; a.g = p.g; a.cu = p.cu_seqlens; a.num_seqs = p.num_seqs; a.T = p.T; a.C = p.C;
     a.init = p.initial_state; a.final = p.final_state; a.h = p.h; a.dh = p.d_h; a.d_final = p.d_final_state;
     a.dx = p.dx; a.dg = p.dg; a.d_init = p.d_initial_state;
     a.tickets = static_cast<uint32_t*>(p.workspace);
     a.maps = reinterpret_cast<uint64_t*>(static_cast<char*>(p.workspace) + 256);
     return a;
 }
-template <typename TI, bool BACK>
+template <typename TI, bool BACK, bool MIX>
 hipError_t run(Scan a, hipStream_t s) {
     constexpr int L = kTokens<TI, BACK>;
     a.tiles = std::max<int64_t>(up(a.T, L * kWaves), 1);
@@ -361,8 +442,14 @@ hipError_t run(Scan a, hipStream_t s) {
         if (e != hipSuccess) return e;
     }
     const dim3 grid((unsigned)(a.tiles * up(a.C, kChannels)));
-    hipLaunchKernelGGL((scan_kernel<TI, L, kWaves, BACK>), grid, dim3(64 * kWaves), 0, s, a);
+    hipLaunchKernelGGL((scan_kernel<TI, L, kWaves, BACK, MIX>), grid, dim3(64 * kWaves), 0, s, a);
     return hipGetLastError();
+}
+
+template <bool BACK>
+hipError_t run(const Scan& a, const ScanLaunch& p, hipStream_t s) {
+    if (p.bf16) return p.mix ? run<bf16, BACK, true>(a, s) : run<bf16, BACK, false>(a, s);
+    return p.mix ? run<float, BACK, true>(a, s) : run<float, BACK, false>(a, s);
 }
 
 }  // namespace
@@ -375,7 +462,7 @@ hipError_t launch_scan(const ScanLaunch& p, hipStream_t s) {
     if (p.num_seqs == 0) return hipSuccess;
     Scan a = arguments(p);
     a.states = p.checkpoints;
-    return p.bf16 ? run<bf16, false>(a, s) : run<float, false>(a, s);
+    return run<false>(a, p, s);
 }
 
 hipError_t launch_scan_backward(const ScanLaunch& p, hipStream_t s) {
@@ -384,10 +471,10 @@ hipError_t launch_scan_backward(const ScanLaunch& p, hipStream_t s) {
     a.states = p.checkpoints;
     if (!p.checkpoints) {
         a.states = reinterpret_cast<float*>(static_cast<char*>(p.workspace) + maps_bytes(p.T, p.C));
-        const hipError_t e = p.bf16 ? run<bf16, false>(a, s) : run<float, false>(a, s);
+        const hipError_t e = run<false>(a, p, s);
         if (e != hipSuccess) return e;
     }
-    return p.bf16 ? run<bf16, true>(a, s) : run<float, true>(a, s);
+    return run<true>(a, p, s);
 }
 
 }  // namespace gdn
