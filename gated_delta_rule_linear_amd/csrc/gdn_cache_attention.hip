@@ -23,6 +23,7 @@
 #include <algorithm>
 #include <cmath>
 #include <limits>
+#include <type_traits>
 
 #include "gdn_e4m3.h"
 #include "gdn_lanes.h"
@@ -37,6 +38,7 @@ typedef float floatx16 __attribute__((ext_vector_type(16)));
 constexpr int kTile = 64;      // tokens of a tile
 constexpr int kFewRows = 32;   // a request with up to so many rows is one of few rows
 constexpr int kMinPart = 512;  // tokens of a part of a request's cache, at least (measured for few rows)
+constexpr int kMinShared = 256;  // of a beginning that requests share
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kInf = __builtin_inff();
 
@@ -117,7 +119,8 @@ struct Request {
         few = rows <= a.few_rows;
         const int c = few ? 0 : 1;
         chunk = ((kv + a.splits[c] - 1) / a.splits[c] + kTile - 1) / kTile * kTile;
-        if (chunk < kMinPart) chunk = kMinPart;
+        constexpr int least = REACH == kPrefix ? kMinShared : kMinPart;
+        if (chunk < least) chunk = least;
         if (!few && !a.tiled && chunk < kv) chunk = (kv + kTile - 1) / kTile * kTile;  // there is no room for its parts
     }
     __device__ __forceinline__ bool alone() const { return REACH == kAll && kv <= chunk; }
@@ -254,25 +257,31 @@ constexpr int kWaves = 4;
 // 4.7.  Requests of up to 32 rows take two workgroups side by side rather than a
 // tile of the other kernel: 5 new tokens of 16 requests over 4000 take 43 us here
 // and 47 there, in fp32 45 and 96, and 6 tokens over 300 7 and 14.
-template <typename TI, int DK, int DV, int REACH>
-__global__ __launch_bounds__(64 * kWaves, 2) void attention_rows_kernel(Attention a) {
-    constexpr int NS = sizeof(TI) == 4 ? 3 : 1;
-    constexpr int BR = 16, KS = DK / 32, VT = DV / 16;
+template <int DK, int DV>
+struct RowsShared {
+    static constexpr int BR = 16;
     // Of each wave: a tile's keys, and in the end its output.
-    constexpr int PR = DK / 16, KEYS = kTile * PR, OUT = BR * (DV + 4) / 4;
-    __shared__ uintx4 s_wave[kWaves][KEYS > OUT ? KEYS : OUT];
-    __shared__ float s_m[kWaves][BR], s_l[kWaves][BR];
+    static constexpr int PR = DK / 16, KEYS = kTile * PR, OUT = BR * (DV + 4) / 4;
+    uintx4 wave[kWaves][KEYS > OUT ? KEYS : OUT];
+    float m[kWaves][BR], l[kWaves][BR];
+};
+// `x`: rows of a request, `h`: key/value head, `z`: part of the cache.
+template <typename TI, int DK, int DV, int REACH>
+__device__ __forceinline__ void attention_rows(const Attention& a, decltype(RowsShared<DK, DV>::wave)& s_wave,
+                                               float (&s_m)[kWaves][16], float (&s_l)[kWaves][16], int32_t x, int32_t h, int32_t z) {
+    constexpr int NS = sizeof(TI) == 4 ? 3 : 1;
+    constexpr int BR = 16, KS = DK / 32, VT = DV / 16, PR = DK / 16;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
-    const int h = blockIdx.y, per = (a.few_rows + BR - 1) / BR;  // workgroups side by side along a request's rows
-    const int32_t n = blockIdx.x / per;
+    const int per = (a.few_rows + BR - 1) / BR;  // workgroups side by side along a request's rows
+    const int32_t n = x / per;
     const Request<REACH> job(a, n);
     if (a.tiled && !job.few) return;
-    const int64_t from = blockIdx.z * job.chunk;
-    if (blockIdx.z > 0 && from >= job.kv) return;
+    const int64_t from = z * job.chunk;
+    if (z > 0 && from >= job.kv) return;
     const int32_t* const table = table_of<REACH>(a, n);
     const int page_mask = (1 << a.page_log2) - 1;
     // (With a request of more rows than it was planned for, more than one turn.)
-    for (int32_t row0 = (blockIdx.x - n * per) * BR; row0 < job.rows; row0 += per * BR) {
+    for (int32_t row0 = (x - n * per) * BR; row0 < job.rows; row0 += per * BR) {
     const int32_t last_row = (row0 + BR < job.rows ? row0 + BR : job.rows) - 1;
     int64_t to = job.sees(last_row / a.G) + 1;  // no row of the tile sees more
     to = !table ? from : to < from + job.chunk ? to : from + job.chunk;
@@ -343,7 +352,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_rows_kernel(Attentio
             asm volatile("" ::: "memory");  // the wave's writes and reads of s_k stay in this order
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                floatx4 x = zero4();
+                floatx4 y = zero4();
                 const int row = 16 * (r >> 2) + 4 * c + (r & 3);
                 uintx4 k16[DK / 64];
 #pragma unroll
@@ -352,10 +361,10 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_rows_kernel(Attentio
                 for (int m = 0; m < KS; ++m) {
                     const bf16x8 k8 = e4m3_to_bf16x8(k16[m >> 1][2 * (m & 1)], k16[m >> 1][2 * (m & 1) + 1]);
 #pragma unroll
-                    for (int p = NS - 1; p >= 0; --p) x = Mma<bf16>::mma(k8, qf[m][p], x);
+                    for (int p = NS - 1; p >= 0; --p) y = Mma<bf16>::mma(k8, qf[m][p], y);
                 }
 #pragma unroll
-                for (int j = 0; j < 4; ++j) s[4 * c + j] = x[j] * c2;
+                for (int j = 0; j < 4; ++j) s[4 * c + j] = y[j] * c2;
             }
         }
         asm volatile("" ::: "memory");  // (and the next tile's writes behind them)
@@ -478,7 +487,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_rows_kernel(Attentio
                 store4(static_cast<TI*>(a.o) + orow * DV + c0 + k,
                        floatx4{out[k] * inv, out[k + 1] * inv, out[k + 2] * inv, out[k + 3] * inv});
         } else {
-            const int64_t prow = blockIdx.z * a.part_rows[0] + (REACH == kAll ? ((int64_t)n * a.Hkv + h) * a.few_rows + row0 + jr : orow);
+            const int64_t prow = z * a.part_rows[0] + (REACH == kAll ? ((int64_t)n * a.Hkv + h) * a.few_rows + row0 + jr : orow);
 #pragma unroll
             for (int k = 0; k < C; k += 4)
                 *reinterpret_cast<floatx4*>(a.ws_o[0] + prow * DV + c0 + k) = floatx4{out[k], out[k + 1], out[k + 2], out[k + 3]};
@@ -490,6 +499,12 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_rows_kernel(Attentio
     }
     __syncthreads();  // before the next turn's waves write s_o
     }
+}
+template <typename TI, int DK, int DV>
+__global__ __launch_bounds__(64 * kWaves, 2) void attention_rows_kernel(Attention a) {
+    __shared__ decltype(RowsShared<DK, DV>::wave) s_wave;
+    __shared__ float s_m[kWaves][16], s_l[kWaves][16];
+    attention_rows<TI, DK, DV, kAll>(a, s_wave, s_m, s_l, blockIdx.x, blockIdx.y, blockIdx.z);
 }
 
 // ---------------------------------------------------------------- many rows
@@ -526,22 +541,30 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_rows_kernel(Attentio
 // reaches 1.18 to 1.24; with 64 channels, where a tile's
 // products are half and its exponentials the same, 0.85.  In full precision
 // (three products for one) 0.36.
+template <int DK, int DV>
+struct TileShared {
+    static constexpr int KS = DK / 16, DT = DV / 32;
+    // A fragment's place is longer than the fragment: a wave writes pieces of the
+    // same lanes of several fragments at once, which so fall into different banks.
+    uintx4 k[2][2 * KS][65];      // [tile % 2][half-tile * KS + step][lane]
+    uintx4 v[2][2 * 2 * DT][64];  // [tile % 2][(half-tile * 2 + step) * DT + channels][lane]
+    int32_t nan[2][kWaves];       // a wave's part of the tile's values had a NaN code
+};
+// `block`: a key/value head's tile of rows and part of the cache.
 template <typename TI, int DK, int DV, int REACH>
-__global__ __launch_bounds__(64 * kWaves, sizeof(TI) == 4 ? 1 : 2) void attention_tile_kernel(Attention a) {
+__device__ __forceinline__ void attention_tile(const Attention& a, TileShared<DK, DV>& sh, int32_t block) {
     constexpr int NS = sizeof(TI) == 4 ? 3 : 1;
     constexpr int BR = 32 * kWaves, KS = DK / 16, DT = DV / 32;
     constexpr float kSlack = NS == 1 ? 0.f : 8.f;
-    // A fragment's place is longer than the fragment: a wave writes pieces of the
-    // same lanes of several fragments at once, which so fall into different banks.
-    __shared__ uintx4 s_k[2][2 * KS][65];      // [tile % 2][half-tile * KS + step][lane]
-    __shared__ uintx4 s_v[2][2 * 2 * DT][64];  // [tile % 2][(half-tile * 2 + step) * DT + channels][lane]
-    __shared__ int32_t s_nan[2][kWaves];       // a wave's part of the tile's values had a NaN code
+    auto& s_k = sh.k;
+    auto& s_v = sh.v;
+    auto& s_nan = sh.nan;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), c = lane & 31, hf = lane >> 5;
     // Key/value heads are neighbours in the grid: workgroups go to the eight XCDs in
     // turn, so with eight heads the tiles of a head share one XCD's cache.  The
     // last rows, which see most, come first, and the parts of the first last.
-    const int h = blockIdx.x % a.Hkv;
-    const int32_t id = blockIdx.x / a.Hkv, over = id - a.tiles, part = over < 0 ? 0 : 1 + over / a.tail;
+    const int h = block % a.Hkv;
+    const int32_t id = block / a.Hkv, over = id - a.tiles, part = over < 0 ? 0 : 1 + over / a.tail;
     const int32_t rtile = over < 0 ? a.tiles - 1 - id : a.tail - 1 - over % a.tail;
     const int32_t n = request_of(a, rtile, BR);
     if (n < 0) return;
@@ -905,6 +928,11 @@ __global__ __launch_bounds__(64 * kWaves, sizeof(TI) == 4 ? 1 : 2) void attentio
         a.ws_ml[1][2 * prow + 1] = sum;
     }
 }
+template <typename TI, int DK, int DV>
+__global__ __launch_bounds__(64 * kWaves, sizeof(TI) == 4 ? 1 : 2) void attention_tile_kernel(Attention a) {
+    __shared__ TileShared<DK, DV> sh;
+    attention_tile<TI, DK, DV, kAll>(a, sh, (int32_t)blockIdx.x);
+}
 
 // ---------------------------------------------------------------- joining parts
 //
@@ -1033,6 +1061,28 @@ __global__ __launch_bounds__(64) void groups_kernel(Attention a, Groups g) {
     g.row[b] = first == INT32_MAX ? -1 : a.rows ? a.rows[first] : first;
 }
 
+// The parts of the beginnings and of the requests' own tokens, in one launch: what
+// is bound by the matrix cores beside what is bound by reading the cache.
+struct PrefixBlocks {
+    int32_t tiles, rows, own_tiles;  // where the next kind of workgroups begins
+};
+template <typename TI, int DK, int DV>
+__global__ __launch_bounds__(64 * kWaves, sizeof(TI) == 4 ? 1 : 2) void prefix_parts_kernel(Attention p, Attention o, PrefixBlocks at) {
+    __shared__ union {
+        TileShared<DK, DV> tile;
+        RowsShared<DK, DV> rows;
+    } sh;
+    auto rows = [&](const Attention& a, int32_t b, auto reach) {
+        const int32_t across = a.num_seqs * ((a.few_rows + 15) / 16), y = b / across;
+        attention_rows<TI, DK, DV, decltype(reach)::value>(a, sh.rows.wave, sh.rows.m, sh.rows.l, b - y * across, y % a.Hkv, y / a.Hkv);
+    };
+    const int32_t b = blockIdx.x;
+    if (b < at.tiles) attention_tile<TI, DK, DV, kPrefix>(p, sh.tile, b);
+    else if (b < at.rows) rows(p, b - at.tiles, std::integral_constant<int, kPrefix>{});
+    else if (b < at.own_tiles) attention_tile<TI, DK, DV, kOwn>(o, sh.tile, b - at.rows);
+    else rows(o, b - at.own_tiles, std::integral_constant<int, kOwn>{});
+}
+
 // Parts of a row of request n at token t, as the kernels wrote them.
 template <int REACH>
 __device__ __forceinline__ int32_t parts_of(const Attention& a, int32_t n, int64_t t, int32_t in_group) {
@@ -1096,6 +1146,7 @@ __global__ __launch_bounds__(256) void prefix_join_kernel(Attention p, Attention
 // ---------------------------------------------------------------- planning
 
 constexpr int64_t kAtOnce = 512;  // workgroups that the device holds: two on each compute unit
+constexpr int64_t kSharedAtOnce = 256;  // of them for beginnings that requests share
 constexpr int64_t kTailCache = 2048;  // tokens in front of a call's last tiles, from which on they are cut
 
 struct Plan {
@@ -1111,7 +1162,7 @@ struct Plan {
 // parts of at least kMinPart tokens, so that there are enough workgroups when
 // every request is as long as the bound, and so that the lengths, which may
 // differ much, do not leave the device waiting for a few long parts.
-Plan plan(const CacheAttentionLaunch& p) {
+Plan plan(const CacheAttentionLaunch& p, int64_t at_once = kAtOnce, int64_t min_part = kMinPart) {
     Plan r = {};
     auto up = [](int64_t x, int64_t y) { return (x + y - 1) / y; };
     const int64_t room = (int64_t)p.max_blocks * p.page_size;
@@ -1134,8 +1185,8 @@ Plan plan(const CacheAttentionLaunch& p) {
         // of 500 is waited for, 75 us).  For the
         // workspace's sake, not more parts than 16384 in all.
         const int64_t units = (int64_t)p.num_seqs * p.H_kv * up(r.few_rows, 16);
-        int64_t splits = std::max(units >= kAtOnce / 2 ? 1 : up(kAtOnce, units), up(kv, 16384));
-        splits = std::min(splits, std::min<int64_t>(up(kv, kMinPart), std::max<int64_t>(16384 / units, 1)));
+        int64_t splits = std::max(units >= at_once / 2 ? 1 : up(at_once, units), up(kv, 16384));
+        splits = std::min(splits, std::min<int64_t>(up(kv, min_part), std::max<int64_t>(16384 / units, 1)));
         r.splits[0] = (int32_t)std::max<int64_t>(std::min<int64_t>(splits, 256), 1);
         r.part_rows[0] = (int64_t)p.num_seqs * p.H_kv * r.few_rows;
     }
@@ -1157,11 +1208,11 @@ Plan plan(const CacheAttentionLaunch& p) {
         constexpr int32_t BR = 32 * kWaves;
         r.tiles = (int32_t)(all / BR + p.num_seqs);
         const int64_t full = up(all, BR), units = std::max<int64_t>(full, p.num_seqs) * p.H_kv;
-        const int64_t rest = std::min<int64_t>(full + (int64_t)p.num_seqs * 3 / 4, r.tiles) * p.H_kv % kAtOnce;
-        if (units < kAtOnce) r.tail = r.tiles;
-        else if (rest <= kAtOnce * 3 / 8 && kv - most / G >= kTailCache) r.tail = (int32_t)up(rest, p.H_kv);
+        const int64_t rest = std::min<int64_t>(full + (int64_t)p.num_seqs * 3 / 4, r.tiles) * p.H_kv % at_once;
+        if (units < at_once) r.tail = r.tiles;
+        else if (rest <= at_once * 3 / 8 && kv - most / G >= kTailCache) r.tail = (int32_t)up(rest, p.H_kv);
         const int64_t share = std::max<int64_t>((int64_t)r.tail * p.H_kv, 1);
-        const int64_t cut = std::min(units < kAtOnce ? up(kAtOnce, units) : (kAtOnce + share / 2) / share, up(kv, kMinPart));
+        const int64_t cut = std::min(units < at_once ? up(at_once, units) : (at_once + share / 2) / share, up(kv, min_part));
         if (r.tail > 0) r.splits[1] = (int32_t)std::max<int64_t>(cut, 1);
         if (r.splits[1] == 1) r.tail = 0;
         // Rows of the first `tail` tiles are among the first (tail + 1) * BR: see first_tile.
@@ -1181,26 +1232,19 @@ Plan plan(const CacheAttentionLaunch& p) {
     return r;
 }
 
-// The kernels that form the parts.
-template <typename TI, int DK, int DV, int REACH>
-hipError_t run_parts(const Attention& a, const Plan& pl, hipStream_t s) {
+template <typename TI, int DK, int DV>
+hipError_t run(const Attention& a, const Plan& pl, hipStream_t s) {
     hipError_t e = hipSuccess;
     if (pl.many) {
         const int64_t tiles = a.tiles + (int64_t)a.tail * (a.splits[1] - 1);
-        hipLaunchKernelGGL((attention_tile_kernel<TI, DK, DV, REACH>), dim3((unsigned)(tiles * a.Hkv)), dim3(64 * kWaves), 0, s, a);
+        hipLaunchKernelGGL((attention_tile_kernel<TI, DK, DV>), dim3((unsigned)(tiles * a.Hkv)), dim3(64 * kWaves), 0, s, a);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     if (pl.few) {
         const dim3 grid((unsigned)(a.num_seqs * ((a.few_rows + 15) / 16)), (unsigned)a.Hkv, (unsigned)a.splits[0]);
-        hipLaunchKernelGGL((attention_rows_kernel<TI, DK, DV, REACH>), grid, dim3(64 * kWaves), 0, s, a);
-        e = hipGetLastError();
+        hipLaunchKernelGGL((attention_rows_kernel<TI, DK, DV>), grid, dim3(64 * kWaves), 0, s, a);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
     }
-    return e;
-}
-template <typename TI, int DK, int DV>
-hipError_t run(const Attention& a, const Plan& pl, hipStream_t s) {
-    hipError_t e = run_parts<TI, DK, DV, kAll>(a, pl, s);
-    if (e != hipSuccess) return e;
     const bool wide = a.splits[0] > 16;
     auto blocks = [&](int c, int at_once) { return a.splits[c] > 1 ? (a.part_rows[c] + at_once - 1) / at_once : 0; };
     const int64_t few = blocks(0, wide ? 1 : kWaves), all = few + blocks(1, kWaves);
@@ -1240,7 +1284,7 @@ CacheAttentionLaunch own_tokens(const CachePrefixLaunch& p) {
 }
 PrefixPlan plan(const CachePrefixLaunch& c) {
     PrefixPlan r = {};
-    r.p = plan(beginnings(c));
+    r.p = plan(beginnings(c), kSharedAtOnce, kMinShared);
     r.o = plan(own_tokens(c));
     r.parts[0] = std::max(r.p.splits[0], r.p.splits[1]);
     r.parts[1] = std::max(r.o.splits[0], r.o.splits[1]);
@@ -1290,9 +1334,15 @@ template <typename TI, int DK, int DV>
 hipError_t run_prefix(const Attention& p, const Attention& o, const PrefixPlan& pl, const Groups& g, hipStream_t s) {
     hipLaunchKernelGGL(groups_kernel, dim3((unsigned)g.count), dim3(64), 0, s, o, g);
     hipError_t e = hipGetLastError();
-    if (e != hipSuccess || (e = run_parts<TI, DK, DV, kPrefix>(p, pl.p, s)) != hipSuccess ||
-        (e = run_parts<TI, DK, DV, kOwn>(o, pl.o, s)) != hipSuccess)
-        return e;
+    if (e != hipSuccess) return e;
+    auto tiles = [](const Attention& a, const Plan& l) { return l.many ? (a.tiles + (int64_t)a.tail * (a.splits[1] - 1)) * a.Hkv : 0; };
+    auto few = [](const Attention& a, const Plan& l) { return l.few ? (int64_t)a.num_seqs * ((a.few_rows + 15) / 16) * a.Hkv * a.splits[0] : 0; };
+    PrefixBlocks at;
+    at.tiles = (int32_t)tiles(p, pl.p);
+    at.rows = at.tiles + (int32_t)few(p, pl.p);
+    at.own_tiles = at.rows + (int32_t)tiles(o, pl.o);
+    hipLaunchKernelGGL((prefix_parts_kernel<TI, DK, DV>), dim3((unsigned)(at.own_tiles + few(o, pl.o))), dim3(64 * kWaves), 0, s, p, o, at);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
     const int64_t rows = o.T * o.H;
     if (pl.parts[0] + pl.parts[1] > 16)
         hipLaunchKernelGGL((prefix_join_kernel<TI, DV, kWaves>), dim3((unsigned)rows), dim3(256), 0, s, p, o, g, pl.parts[0]);
