@@ -72,28 +72,33 @@ struct Attention {
     // and sum).  Rows: for few, (n * Hkv + h) * few_rows + row; else the first of q.
     int64_t part_rows[2];
     float *ws_o[2], *ws_ml[2];
-    const int32_t* skip;  // kOwn: tokens of each request's beginning, whole pages
+    // kPrefix: each group's first token and the one behind its last, length of the
+    // beginning, row of the table.  kOwn: of each request the beginning's length, its
+    // group, and the parts of a row at most, of the beginning and of its own.
+    const int4* info;
 };
 
 // Tiles of BR rows that the requests before n take at most: the tiles of
 // request n start here.  (floor(x / BR) grows by at least ceil(rows / BR) - 1
 // over a request's rows.)
+template <int REACH = kAll>
 __device__ __forceinline__ int64_t first_tile(const Attention& a, int64_t n, int br) {
-    return (int64_t)a.cu[n] * a.G / br + n;
+    return (int64_t)(REACH == kPrefix ? a.info[n].x : a.cu[n]) * a.G / br + n;
 }
 // The request whose tiles hold tile b: the last n with first_tile(n) <= b.
+template <int REACH = kAll>
 __device__ __forceinline__ int32_t request_of(const Attention& a, int64_t b, int br) {
     int32_t below = 0;
     for (int32_t n0 = 0; n0 < a.num_seqs; n0 += 64) {
         const int32_t n = n0 + (threadIdx.x & 63);
-        below += __popcll(__ballot(n < a.num_seqs && first_tile(a, n, br) <= b));
+        below += __popcll(__ballot(n < a.num_seqs && first_tile<REACH>(a, n, br) <= b));
     }
     return below - 1;
 }
 
 // Tokens of a request that its group has read, whatever the offsets of the groups were.
-__device__ __forceinline__ int64_t beginning(const Attention& a, int32_t n) {
-    const int64_t skip = a.skip[n] >> a.page_log2 << a.page_log2;
+__device__ __forceinline__ int64_t beginning(const Attention& a, int32_t n, int32_t tokens) {
+    const int64_t skip = tokens >> a.page_log2 << a.page_log2;
     return skip < 0 || skip > a.kv_lens[n] || skip >> a.page_log2 > a.max_blocks ? 0 : skip;
 }
 
@@ -106,11 +111,12 @@ struct Request {
     int64_t kv;       // tokens held
     int64_t chunk;    // tokens of a part of its cache
     bool few;
-    __device__ __forceinline__ Request(const Attention& a, int32_t n) {
-        int64_t t1 = a.cu[n + 1];
-        t0 = a.cu[n];
-        const int64_t begin = REACH == kOwn ? beginning(a, n) : 0;
-        const int64_t most = ((int64_t)a.max_blocks << a.page_log2) - begin, held = a.kv_lens[n] - begin;
+    __device__ __forceinline__ Request(const Attention& a, int32_t n) : Request(a, n, REACH == kAll ? int4{} : a.info[n]) {}
+    __device__ __forceinline__ Request(const Attention& a, int32_t n, int4 info) {
+        int64_t t1 = REACH == kPrefix ? info.y : a.cu[n + 1];
+        t0 = REACH == kPrefix ? info.x : a.cu[n];
+        const int64_t begin = REACH == kOwn ? beginning(a, n, info.x) : 0;
+        const int64_t most = ((int64_t)a.max_blocks << a.page_log2) - begin, held = (REACH == kPrefix ? info.z : a.kv_lens[n]) - begin;
         t0 = t0 < 0 ? 0 : t0;
         t1 = t1 < a.T ? t1 : a.T;
         len = t1 > t0 ? (int32_t)(t1 - t0) : 0;
@@ -131,8 +137,8 @@ struct Request {
 
 template <int REACH = kAll>
 __device__ __forceinline__ const int32_t* table_of(const Attention& a, int32_t n) {
-    const int32_t row = a.rows ? a.rows[n] : n;
-    const int64_t begin = REACH == kOwn ? beginning(a, n) >> a.page_log2 : 0;
+    const int32_t row = REACH == kPrefix ? a.info[n].w : a.rows ? a.rows[n] : n;
+    const int64_t begin = REACH == kOwn ? beginning(a, n, a.info[n].x) >> a.page_log2 : 0;
     return row >= 0 && row < a.num_rows && a.num_pages > 0 ? a.table + (int64_t)row * a.max_blocks + begin : nullptr;
 }
 
@@ -566,11 +572,11 @@ __device__ __forceinline__ void attention_tile(const Attention& a, TileShared<DK
     const int h = block % a.Hkv;
     const int32_t id = block / a.Hkv, over = id - a.tiles, part = over < 0 ? 0 : 1 + over / a.tail;
     const int32_t rtile = over < 0 ? a.tiles - 1 - id : a.tail - 1 - over % a.tail;
-    const int32_t n = request_of(a, rtile, BR);
+    const int32_t n = request_of<REACH>(a, rtile, BR);
     if (n < 0) return;
     Request<REACH> job(a, n);
     if (rtile >= a.tail) job.chunk = job.kv;
-    const int64_t row0_ = (rtile - first_tile(a, n, BR)) * BR;
+    const int64_t row0_ = (rtile - first_tile<REACH>(a, n, BR)) * BR;
     if (job.few || row0_ < 0 || row0_ >= job.rows) return;
     const int32_t row0 = (int32_t)row0_, last_row = (row0 + BR < job.rows ? row0 + BR : job.rows) - 1;
     const int64_t from = part * job.chunk;
@@ -909,6 +915,36 @@ __device__ __forceinline__ void attention_tile(const Attention& a, TileShared<DK
         const bool some = sees_some(a, table, from, to, kTile, from + sees);
         if (mx == -kInf && some) sum += 1.f;
     }
+    if constexpr (REACH != kAll) {
+        // Rows of the output lie whole in memory, where a lane has pieces of one: they
+        // change places through LDS, which the last tile has left (64 requests behind
+        // 4,096 tokens).  Piece p of row c goes to place p ^ c.
+        constexpr int P = DV / 4;
+        floatx4* const s_o = reinterpret_cast<floatx4*>(&sh) + wave * 32 * P;
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                s_o[c * P + ((8 * d + 2 * q + hf) ^ (c & (P - 1)))] = floatx4{O[d][4 * q], O[d][4 * q + 1], O[d][4 * q + 2], O[d][4 * q + 3]};
+        asm volatile("" ::: "memory");  // the wave's writes and reads of s_o stay in this order
+        constexpr int AT_ONCE = 64 / P;  // rows
+        const int piece = lane % P;
+#pragma unroll 4
+        for (int j = 0; j < 32; j += AT_ONCE) {
+            const int k = j + lane / P, at = row0 + 32 * wave + k;
+            const floatx4 z = s_o[k * P + (piece ^ (k & (P - 1)))];
+            if (at >= job.rows) continue;
+            const int32_t ti = at / a.G;
+            const int64_t prow = part * a.part_rows[1] + (job.t0 + ti) * a.H + h * a.G + (at - ti * a.G);
+            *reinterpret_cast<floatx4*>(a.ws_o[1] + prow * DV + 4 * piece) = z;
+        }
+        if (live && hf == 0) {
+            const int64_t prow = part * a.part_rows[1] + orow;
+            a.ws_ml[1][2 * prow] = mx == -kInf ? mx : ref;
+            a.ws_ml[1][2 * prow + 1] = sum;
+        }
+        return;
+    }
     if (!live) return;
     const bool alone = job.alone();
     const float inv = alone ? reciprocal_sum(sum, mx) : 1.f;
@@ -1021,44 +1057,45 @@ __global__ __launch_bounds__(256) void attention_join_kernel(Attention a, int32_
 struct Groups {
     const int32_t *offsets, *shared;
     int32_t count;
-    int32_t *cu, *kv, *row;  // of each group, as a request: tokens, length of the beginning, row of the table
-    int32_t *skip, *of;      // of each request: tokens of the beginning and its group, or 0 and -1
+    int4 *group, *request;  // `info` of the beginnings and of the requests
 };
 // A wave to a group.  A request that does not hold the whole beginning before its
 // new tokens (a refused one, say) takes no part: all its tokens are its own.
-__global__ __launch_bounds__(64) void groups_kernel(Attention a, Groups g) {
+__global__ __launch_bounds__(64) void groups_kernel(Attention p, Attention o, Groups g) {
     const int lane = threadIdx.x, b = blockIdx.x;
     auto offset = [&](int32_t i) {
         const int32_t x = g.offsets[i];
-        return x < 0 ? 0 : x < a.num_seqs ? x : a.num_seqs;
+        return x < 0 ? 0 : x < o.num_seqs ? x : o.num_seqs;
     };
     const int32_t n0 = offset(b), n1 = offset(b + 1);
-    const int64_t room = (int64_t)a.max_blocks << a.page_log2, most = g.shared[b] < room ? g.shared[b] : room;
-    const int32_t shared = most < 0 ? 0 : (int32_t)(most >> a.page_log2 << a.page_log2);
+    const int64_t room = (int64_t)o.max_blocks << o.page_log2, most = g.shared[b] < room ? g.shared[b] : room;
+    const int32_t shared = most < 0 ? 0 : (int32_t)(most >> o.page_log2 << o.page_log2);
     int32_t first = INT32_MAX;
     for (int32_t n = n0 + lane; n < n1; n += 64) {
-        const int64_t len = (int64_t)a.cu[n + 1] - a.cu[n];
-        const bool takes = shared > 0 && len > 0 && a.kv_lens[n] - len >= shared;
-        g.skip[n] = takes ? shared : 0;
-        g.of[n] = takes ? b : -1;
-        if (takes && n < first) first = n;
+        const int64_t len = (int64_t)o.cu[n + 1] - o.cu[n];
+        if (shared > 0 && len > 0 && o.kv_lens[n] - len >= shared && n < first) first = n;
     }
     for (int d = 32; d > 0; d /= 2) first = min(first, __shfl_xor(first, d));
+    const bool some = first < INT32_MAX;
+    const int4 group = {o.cu[n0], o.cu[n1], some ? shared : 0, !some ? -1 : o.rows ? o.rows[first] : first};
+    if (lane == 0) g.group[b] = group;
+    const Request<kPrefix> whole(p, b, group);
+    const int32_t parts = whole.kv > 0 ? (int32_t)whole.parts() : 0;
+    auto put = [&](int32_t n, bool takes) {
+        int4 info = {takes ? shared : 0, takes ? b : -1, takes ? parts : 0, 0};
+        const Request<kOwn> own(o, n, info);
+        if (own.kv > 0) info.w = (int32_t)own.parts();
+        g.request[n] = info;
+    };
+    for (int32_t n = n0 + lane; n < n1; n += 64) {
+        const int64_t len = (int64_t)o.cu[n + 1] - o.cu[n];
+        put(n, shared > 0 && len > 0 && o.kv_lens[n] - len >= shared);
+    }
+    // requests in front of the first group and behind the last
     if (b == 0)
-        for (int32_t n = lane; n < n0; n += 64) {
-            g.skip[n] = 0;
-            g.of[n] = -1;
-        }
+        for (int32_t n = lane; n < n0; n += 64) put(n, false);
     if (b == g.count - 1)
-        for (int32_t n = n1 + lane; n < a.num_seqs; n += 64) {
-            g.skip[n] = 0;
-            g.of[n] = -1;
-        }
-    if (lane > 0) return;
-    g.cu[b] = a.cu[n0];
-    if (b == g.count - 1) g.cu[g.count] = a.cu[n1];
-    g.kv[b] = first < INT32_MAX ? shared : 0;
-    g.row[b] = first == INT32_MAX ? -1 : a.rows ? a.rows[first] : first;
+        for (int32_t n = n1 + lane; n < o.num_seqs; n += 64) put(n, false);
 }
 
 // The parts of the beginnings and of the requests' own tokens, in one launch: what
@@ -1071,6 +1108,7 @@ __global__ __launch_bounds__(64 * kWaves, sizeof(TI) == 4 ? 1 : 2) void prefix_p
     __shared__ union {
         TileShared<DK, DV> tile;
         RowsShared<DK, DV> rows;
+        floatx4 out[kWaves * 32 * DV / 4];  // of the tile kernel's waves
     } sh;
     auto rows = [&](const Attention& a, int32_t b, auto reach) {
         const int32_t across = a.num_seqs * ((a.few_rows + 15) / 16), y = b / across;
@@ -1083,18 +1121,17 @@ __global__ __launch_bounds__(64 * kWaves, sizeof(TI) == 4 ? 1 : 2) void prefix_p
     else rows(o, b - at.own_tiles, std::integral_constant<int, kOwn>{});
 }
 
-// Parts of a row of request n at token t, as the kernels wrote them.
+// Parts of a row of request n at token t: of its `parts`, unless its tile is whole.
 template <int REACH>
-__device__ __forceinline__ int32_t parts_of(const Attention& a, int32_t n, int64_t t, int32_t in_group) {
+__device__ __forceinline__ int32_t parts_of(const Attention& a, int32_t n, int64_t t, int32_t in_group, int32_t parts) {
+    if (!a.tiled || a.tail == a.tiles || parts < 2) return parts;
     const Request<REACH> q(a, n);
-    if (q.kv == 0) return 0;
-    if (!q.few && first_tile(a, n, 32 * kWaves) + ((t - q.t0) * a.G + in_group) / (32 * kWaves) >= a.tail) return 1;
-    return (int32_t)q.parts();
+    return !q.few && first_tile<REACH>(a, n, 32 * kWaves) + ((t - q.t0) * a.G + in_group) / (32 * kWaves) >= a.tail ? 1 : parts;
 }
 // W waves to a row, as in join_rows: `p` of the groups, `o` of the requests, whose
 // parts lie behind those of `p`.
 template <typename TI, int DV, int W>
-__global__ __launch_bounds__(256) void prefix_join_kernel(Attention p, Attention o, Groups g, int32_t first_own) {
+__global__ __launch_bounds__(256) void prefix_join_kernel(Attention p, Attention o, int32_t groups, int32_t first_own, int32_t most_own) {
     constexpr int L = DV / 4, STEP = 64 * W / L, ROWS = kWaves / W;
     __shared__ floatx4 s_o[STEP * ROWS][L];
     __shared__ float s_l[STEP * ROWS], s_m[kWaves];
@@ -1106,9 +1143,10 @@ __global__ __launch_bounds__(256) void prefix_join_kernel(Attention p, Attention
     const bool mine = r < step && n >= 0 && n < o.num_seqs;  // (not behind the last request)
     int32_t shared = 0, parts = 0;
     if (mine) {
-        const int32_t in_group = (int32_t)(r - t * o.H) % o.G, of = g.of[n];
-        if (of >= 0 && of < g.count) shared = parts_of<kPrefix>(p, of, t, in_group);
-        parts = shared + parts_of<kOwn>(o, n, t, in_group);
+        const int32_t in_group = (int32_t)(r - t * o.H) % o.G;
+        const int4 info = o.info[n];  // (of offsets that are none, anything)
+        if (info.y >= 0 && info.y < groups) shared = parts_of<kPrefix>(p, info.y, t, in_group, min(max(info.z, 0), first_own));
+        parts = shared + parts_of<kOwn>(o, n, t, in_group, min(max(info.w, 0), most_own));
     }
     auto at = [&](int32_t s) { return (s < shared ? s : first_own + s - shared) * step + r; };
     const float *ml = p.ws_ml[0], *wo = p.ws_o[0];
@@ -1296,7 +1334,7 @@ PrefixPlan plan(const CachePrefixLaunch& c) {
     const size_t rows = (size_t)(r.parts[0] + r.parts[1]) * (size_t)(c.all.T_total * c.all.H);
     take(rows * c.all.dv * sizeof(float));
     r.ml = take(rows * 2 * sizeof(float));
-    r.groups = take(((size_t)c.num_groups * 3 + 1 + (size_t)c.all.num_seqs * 2) * sizeof(int32_t));
+    r.groups = take(((size_t)c.num_groups + (size_t)c.all.num_seqs) * sizeof(int4));
     return r;
 }
 // Requests that share nothing with others are gdn_cache_attention's.
@@ -1332,7 +1370,7 @@ Attention arguments(const CacheAttentionLaunch& p, const Plan& pl) {
 }
 template <typename TI, int DK, int DV>
 hipError_t run_prefix(const Attention& p, const Attention& o, const PrefixPlan& pl, const Groups& g, hipStream_t s) {
-    hipLaunchKernelGGL(groups_kernel, dim3((unsigned)g.count), dim3(64), 0, s, o, g);
+    hipLaunchKernelGGL(groups_kernel, dim3((unsigned)g.count), dim3(64), 0, s, p, o, g);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     auto tiles = [](const Attention& a, const Plan& l) { return l.many ? (a.tiles + (int64_t)a.tail * (a.splits[1] - 1)) * a.Hkv : 0; };
@@ -1345,9 +1383,9 @@ hipError_t run_prefix(const Attention& p, const Attention& o, const PrefixPlan& 
     if ((e = hipGetLastError()) != hipSuccess) return e;
     const int64_t rows = o.T * o.H;
     if (pl.parts[0] + pl.parts[1] > 16)
-        hipLaunchKernelGGL((prefix_join_kernel<TI, DV, kWaves>), dim3((unsigned)rows), dim3(256), 0, s, p, o, g, pl.parts[0]);
+        hipLaunchKernelGGL((prefix_join_kernel<TI, DV, kWaves>), dim3((unsigned)rows), dim3(256), 0, s, p, o, g.count, pl.parts[0], pl.parts[1]);
     else
-        hipLaunchKernelGGL((prefix_join_kernel<TI, DV, 1>), dim3((unsigned)((rows + kWaves - 1) / kWaves)), dim3(256), 0, s, p, o, g, pl.parts[0]);
+        hipLaunchKernelGGL((prefix_join_kernel<TI, DV, 1>), dim3((unsigned)((rows + kWaves - 1) / kWaves)), dim3(256), 0, s, p, o, g.count, pl.parts[0], pl.parts[1]);
     return hipGetLastError();
 }
 template <typename TI>
@@ -1383,11 +1421,10 @@ hipError_t launch_cache_prefix(const CachePrefixLaunch& c, hipStream_t s) {
         o.ws_o[k] = ws_o + pl.parts[0] * rows * c.all.dv;
         o.ws_ml[k] = ws_ml + pl.parts[0] * rows * 2;
     }
-    int32_t* const ints = reinterpret_cast<int32_t*>(at + pl.groups);
-    Groups g = {c.group_offsets, c.prefix_lens, c.num_groups, ints, ints + c.num_groups + 1, ints + 2 * c.num_groups + 1,
-                ints + 3 * c.num_groups + 1, ints + 3 * c.num_groups + 1 + c.all.num_seqs};
-    o.skip = g.skip;
-    p.cu = g.cu; p.kv_lens = g.kv; p.rows = g.row;
+    int4* const info = reinterpret_cast<int4*>(at + pl.groups);
+    const Groups g = {c.group_offsets, c.prefix_lens, c.num_groups, info, info + c.num_groups};
+    p.info = g.group;
+    o.info = g.request;
     return c.all.bf16 ? run_prefix_t<bf16>(p, o, c.all.dk, c.all.dv, pl, g, s) : run_prefix_t<float>(p, o, c.all.dk, c.all.dv, pl, g, s);
 }
 

@@ -23,8 +23,10 @@ namespace gdn {
 namespace {
 
 constexpr int kWaves = 4;         // of a workgroup
-constexpr int kUnroll = 2;        // steps of heads whose loads are in flight together
+template <bool BACK>
+constexpr int kUnroll = BACK ? 1 : 2;  // steps of heads whose loads are in flight together
 constexpr int64_t kUnits = 8192;  // waves' worth of work from which on a wave takes all heads of a token
+constexpr int64_t kCaches = 256 << 20;
 constexpr int64_t kMostBlocks = 1024;  // of the backward pass: partial sums of the weights' gradients
 
 enum Rotation { kNone, kHalves, kPairs };
@@ -99,57 +101,62 @@ struct Lane {
     }
 };
 
-template <typename T, int ROT>
-__device__ __forceinline__ void load8(const T* at, int c0, int c1, float* v) {
-    if constexpr (sizeof(T) == 2 && ROT != kHalves) {
-        const bf16x8 a = *reinterpret_cast<const bf16x8*>(at + c0);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = (float)a[j];
-    } else if constexpr (sizeof(T) == 2) {
-        const bf16x4 a = *reinterpret_cast<const bf16x4*>(at + c0), b = *reinterpret_cast<const bf16x4*>(at + c1);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            v[j] = (float)a[j];
-            v[j + 4] = (float)b[j];
-        }
-    } else {
-        const floatx4 a = *reinterpret_cast<const floatx4*>(at + c0), b = *reinterpret_cast<const floatx4*>(at + c1);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            v[j] = a[j];
-            v[j + 4] = b[j];
+// A lane's eight values, in one load where they are neighbours of two bytes.
+// PASSING: by the caches, for a call whose tensors are far larger than these.
+template <typename V, bool PASSING>
+__device__ __forceinline__ V load(const void* at) {
+    const V* const p = static_cast<const V*>(at);
+    if constexpr (PASSING) return __builtin_nontemporal_load(p);
+    else return *p;
+}
+template <bool PASSING, typename V>
+__device__ __forceinline__ void store(void* at, V x) {
+    V* const p = static_cast<V*>(at);
+    if constexpr (PASSING) __builtin_nontemporal_store(x, p);
+    else *p = x;
+}
+template <typename T, int ROT, bool PASSING>
+struct Eight {
+    static constexpr bool ONE = sizeof(T) == 2 && ROT != kHalves;
+    typedef T four __attribute__((ext_vector_type(4)));
+    typedef T eight __attribute__((ext_vector_type(8)));
+    eight v;
+    __device__ __forceinline__ void load8(const T* at, int c0, int c1) {
+        if constexpr (ONE) {
+            v = load<eight, PASSING>(at + c0);
+        } else {
+            const four a = load<four, PASSING>(at + c0), b = load<four, PASSING>(at + c1);
+            v = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
         }
     }
-}
-template <typename T, int ROT>
-__device__ __forceinline__ void store8(T* at, int c0, int c1, const float* v) {
-    if constexpr (sizeof(T) == 2 && ROT != kHalves) {
-        bf16x8 a;
+    __device__ __forceinline__ static void store8(T* at, int c0, int c1, const float* x) {
+        eight y;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) a[j] = (bf16)v[j];
-        *reinterpret_cast<bf16x8*>(at + c0) = a;
-    } else if constexpr (sizeof(T) == 2) {
-        *reinterpret_cast<bf16x4*>(at + c0) = bf16x4{(bf16)v[0], (bf16)v[1], (bf16)v[2], (bf16)v[3]};
-        *reinterpret_cast<bf16x4*>(at + c1) = bf16x4{(bf16)v[4], (bf16)v[5], (bf16)v[6], (bf16)v[7]};
-    } else {
-        *reinterpret_cast<floatx4*>(at + c0) = floatx4{v[0], v[1], v[2], v[3]};
-        *reinterpret_cast<floatx4*>(at + c1) = floatx4{v[4], v[5], v[6], v[7]};
+        for (int j = 0; j < 8; ++j) y[j] = from_f32<T>(x[j]);
+        if constexpr (ONE) {
+            store<PASSING>(at + c0, y);
+        } else {
+            store<PASSING>(at + c0, __builtin_shufflevector(y, y, 0, 1, 2, 3));
+            store<PASSING>(at + c1, __builtin_shufflevector(y, y, 4, 5, 6, 7));
+        }
     }
-}
+};
 
 // One step: the D / 8 lanes of each head at `head` of kind s, of token t.
-template <typename T, int D, int ROT, bool BACK>
+template <typename T, int D, int ROT, bool BACK, bool PASSING>
 struct Step {
-    float x[8], dy[8];
+    Eight<T, ROT, PASSING> in, back;
     __device__ __forceinline__ void load(const Norm& a, const Lane<D, ROT>& l, int s, int64_t t, int32_t head) {
         head = head < a.heads[s] ? head : 0;  // lanes without a head work on the first, unseen
-        load8<T, ROT>(static_cast<const T*>(a.x[s]) + t * a.stride[s] + head * D, l.c0, l.c1, x);
-        if (BACK) load8<T, ROT>(static_cast<const T*>(a.dy[s]) + (t * a.heads[s] + head) * D, l.c0, l.c1, dy);
+        in.load8(static_cast<const T*>(a.x[s]) + t * a.stride[s] + head * D, l.c0, l.c1);
+        if (BACK) back.load8(static_cast<const T*>(a.dy[s]) + (t * a.heads[s] + head) * D, l.c0, l.c1);
     }
     __device__ __forceinline__ void store(const Norm& a, const Lane<D, ROT>& l, int s, int64_t t, int32_t head, const float* w,
                                           float* dw) {
         const bool live = head < a.heads[s];
-        float r = 1.f;
+        float x[8], r = 1.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = to_f32(in.v[j]);
         if (a.norm) {
             float sum = 0.f;
 #pragma unroll
@@ -166,7 +173,7 @@ struct Step {
         } else {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                v[j] = dy[j] * a.scale[s];
+                v[j] = to_f32(back.v[j]) * a.scale[s];
                 x[j] *= r;
             }
             l.template turn<-1>(v);
@@ -183,11 +190,11 @@ struct Step {
                 for (int j = 0; j < 8; ++j) v[j] = r * (v[j] - x[j] * dot);
             }
         }
-        if (live) store8<T, ROT>(static_cast<T*>(a.out[s]) + t * a.out_stride[s] + head * D, l.c0, l.c1, v);
+        if (live) in.store8(static_cast<T*>(a.out[s]) + t * a.out_stride[s] + head * D, l.c0, l.c1, v);
     }
 };
 
-template <typename T, int D, int ROT, bool BACK>
+template <typename T, int D, int ROT, bool BACK, bool PASSING>
 __global__ __launch_bounds__(64 * kWaves) void qk_norm_kernel(Norm a) {
     constexpr int HEADS = 64 / (D / 8);  // of a step
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -211,15 +218,15 @@ __global__ __launch_bounds__(64 * kWaves) void qk_norm_kernel(Norm a) {
         for (int s = 0; s < 2; ++s) {
             int32_t i = s == 0 ? from : (from > a.steps[0] ? from - a.steps[0] : 0);
             const int32_t end = s == 0 ? (to < a.steps[0] ? to : a.steps[0]) : to - a.steps[0];
-            for (; i + kUnroll <= end; i += kUnroll) {
-                Step<T, D, ROT, BACK> step[kUnroll];
+            for (; i + kUnroll<BACK> <= end; i += kUnroll<BACK>) {
+                Step<T, D, ROT, BACK, PASSING> step[kUnroll<BACK>];
 #pragma unroll
-                for (int k = 0; k < kUnroll; ++k) step[k].load(a, l, s, t, (i + k) * HEADS + l.group);
+                for (int k = 0; k < kUnroll<BACK>; ++k) step[k].load(a, l, s, t, (i + k) * HEADS + l.group);
 #pragma unroll
-                for (int k = 0; k < kUnroll; ++k) step[k].store(a, l, s, t, (i + k) * HEADS + l.group, w[s], dw[s]);
+                for (int k = 0; k < kUnroll<BACK>; ++k) step[k].store(a, l, s, t, (i + k) * HEADS + l.group, w[s], dw[s]);
             }
             for (; i < end; ++i) {
-                Step<T, D, ROT, BACK> step;
+                Step<T, D, ROT, BACK, PASSING> step;
                 step.load(a, l, s, t, i * HEADS + l.group);
                 step.store(a, l, s, t, i * HEADS + l.group, w[s], dw[s]);
             }
@@ -300,19 +307,26 @@ Norm arguments(const QkNormLaunch& p) {
     return a;
 }
 
-template <bool BACK, typename T, int D>
+template <bool BACK, bool PASSING, typename T, int D>
 void run_rotation(const Norm& a, const QkNormLaunch& p, unsigned blocks, hipStream_t s) {
     const dim3 grid(blocks), block(64 * kWaves);
-    if (p.rotary == 0) hipLaunchKernelGGL((qk_norm_kernel<T, D, kNone, BACK>), grid, block, 0, s, a);
-    else if (p.interleaved) hipLaunchKernelGGL((qk_norm_kernel<T, D, kPairs, BACK>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((qk_norm_kernel<T, D, kHalves, BACK>), grid, block, 0, s, a);
+    if (p.rotary == 0) hipLaunchKernelGGL((qk_norm_kernel<T, D, kNone, BACK, PASSING>), grid, block, 0, s, a);
+    else if (p.interleaved) hipLaunchKernelGGL((qk_norm_kernel<T, D, kPairs, BACK, PASSING>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((qk_norm_kernel<T, D, kHalves, BACK, PASSING>), grid, block, 0, s, a);
+}
+// Outputs that the caches cannot hold pass them by (1.1 GB: 370 us, through them
+// 406); smaller ones stay for whoever reads them next.
+template <bool BACK, typename T, int D>
+void run_size(const Norm& a, const QkNormLaunch& p, unsigned blocks, hipStream_t s) {
+    if (p.T * ((int64_t)p.heads[0] + p.heads[1]) * D * (int64_t)sizeof(T) > kCaches) run_rotation<BACK, true, T, D>(a, p, blocks, s);
+    else run_rotation<BACK, false, T, D>(a, p, blocks, s);
 }
 template <bool BACK>
 hipError_t run(const Norm& a, const QkNormLaunch& p, int64_t blocks, hipStream_t s) {
-    if (p.bf16 && p.d == 128) run_rotation<BACK, bf16, 128>(a, p, (unsigned)blocks, s);
-    else if (p.bf16) run_rotation<BACK, bf16, 64>(a, p, (unsigned)blocks, s);
-    else if (p.d == 128) run_rotation<BACK, float, 128>(a, p, (unsigned)blocks, s);
-    else run_rotation<BACK, float, 64>(a, p, (unsigned)blocks, s);
+    if (p.bf16 && p.d == 128) run_size<BACK, bf16, 128>(a, p, (unsigned)blocks, s);
+    else if (p.bf16) run_size<BACK, bf16, 64>(a, p, (unsigned)blocks, s);
+    else if (p.d == 128) run_size<BACK, float, 128>(a, p, (unsigned)blocks, s);
+    else run_size<BACK, float, 64>(a, p, (unsigned)blocks, s);
     return hipGetLastError();
 }
 
