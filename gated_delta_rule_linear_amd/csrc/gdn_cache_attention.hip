@@ -22,6 +22,7 @@
 // power of two, is applied exactly, to the scores and p or in the conversion.
 #include <algorithm>
 #include <cmath>
+#include <cstdlib>
 #include <limits>
 #include <type_traits>
 
@@ -1337,8 +1338,29 @@ PrefixPlan plan(const CachePrefixLaunch& c) {
     r.groups = take(((size_t)c.num_groups + (size_t)c.all.num_seqs) * sizeof(int4));
     return r;
 }
-// Requests that share nothing with others are gdn_cache_attention's.
-bool shares(const CachePrefixLaunch& p) { return p.num_groups < p.all.num_seqs && p.num_groups > 0; }
+// Whether the beginnings are worth reading apart: else the call is
+// gdn_cache_attention's, whose requests read the same pages out of the caches, at
+// some 8 TB/s.  Reading them apart costs 7 us of launches and dependent loads where a group
+// is of few rows and 15 else, and the beginning's products with all rows of the
+// group, at some 0.55 PFLOP/s (0.18 in full precision).  Both sides, in us, shared and
+// not, bf16, 32 heads, 8 for keys, of 128 channels, 64 tokens of their own: 4
+// requests behind 16,384 tokens 18.6 and 29.1, 64 behind them 54 and 213, behind
+// 4,096 37 and 51, behind 1,024 22.4 and 17.5; 4 new tokens of 64 behind 16,384 137
+// and 230, of 16 behind 4,096 37 and 27.  Requests of many rows keep the matrix
+// cores busy either way: 32 new tokens (128 rows) of 64 behind 16,384 568 and 855, of 16 242 and 243,
+// of 64 behind 1,024 100 and 89; 256 new tokens of 8 behind 16,384 541 and 526, of 2 241 and 162.
+bool shares(const CachePrefixLaunch& p) {
+    const CacheAttentionLaunch& a = p.all;
+    if (p.num_groups <= 0 || p.num_groups >= a.num_seqs) return false;  // no request shares with another
+    if (const char* e = std::getenv("GDN_PREFIX_SHARE")) return e[0] != '0';
+    auto bound = [&](int64_t hint, int64_t most) { return hint > 0 && hint < most ? hint : most; };
+    const int64_t G = a.H / a.H_kv, rows = bound(a.max_new, (a.T_total + a.num_seqs - 1) / a.num_seqs) * G;
+    const double prefix = (double)bound(p.max_prefix, bound(a.max_kv, (int64_t)a.max_blocks * a.page_size));
+    const double saved = (double)(a.num_seqs - p.num_groups) * prefix * a.H_kv * (a.dk + a.dv);
+    if (rows > kFewRows) return rows <= 32 * kWaves && saved > 256e6;
+    const double products = 2. * (double)a.T_total * a.H * prefix * (a.dk + a.dv);
+    return saved / 8e6 > (a.T_total * G <= (int64_t)p.num_groups * kFewRows ? 7. : 15.) + products / (a.bf16 ? 5.5e8 : 1.8e8);
+}
 
 }  // namespace
 
@@ -1404,7 +1426,14 @@ hipError_t launch_cache_attention(const CacheAttentionLaunch& p, hipStream_t s) 
     return p.bf16 ? run_t<bf16>(a, p, pl, s) : run_t<float>(a, p, pl, s);
 }
 
-size_t cache_prefix_workspace_bytes(const CachePrefixLaunch& p) { return shares(p) ? plan(p).bytes : plan(p.all).bytes; }
+// The type is not asked for, so the room is for either: with bf16, whose products
+// cost less, every call shares that does in full precision.
+size_t cache_prefix_workspace_bytes(const CachePrefixLaunch& p) {
+    CachePrefixLaunch c = p;
+    c.all.bf16 = true;
+    const size_t apart = plan(c.all).bytes;
+    return shares(c) ? std::max(plan(c).bytes, apart) : apart;
+}
 
 hipError_t launch_cache_prefix(const CachePrefixLaunch& c, hipStream_t s) {
     if (!shares(c)) return launch_cache_attention(c.all, s);

@@ -294,11 +294,11 @@ __global__ __launch_bounds__(64 * NW, BACK ? 2 : 4) void scan_kernel(Scan a) {
         };
         // What is computed again for another pass over the tokens is not kept until then,
         // nor is it computed ahead of its token: the registers are the inputs'.
-        auto forget = [&]() {
+        auto forget = [&](bool inputs) {
 #pragma unroll
             for (int i = 0; i < L; ++i) {
                 asm volatile("" : "+v"(g[i]));
-                asm volatile("" : "+v"(x[i].v));
+                if (inputs) asm volatile("" : "+v"(x[i].v));
                 if (BACK) asm volatile("" : "+v"(dh[i].v));
             }
         };
@@ -323,10 +323,10 @@ __global__ __launch_bounds__(64 * NW, BACK ? 2 : 4) void scan_kernel(Scan a) {
         __shared__ Map s_map[BACK ? 2 : 1][NW][64], s_before[NW][64];
         __shared__ floatx4 s_entry[64];
         s_map[0][wave][lane] = wave_map(false);
-        forget();
+        forget(true);
         if (BACK) {
             s_map[1][wave][lane] = wave_map(true);
-            forget();
+            forget(true);
         }
         __syncthreads();
         floatx4 s = zero;  // what comes into the tile
@@ -387,7 +387,7 @@ __global__ __launch_bounds__(64 * NW, BACK ? 2 : 4) void scan_kernel(Scan a) {
                 if (MIX) past[i] -= x[i].f();
                 __builtin_amdgcn_sched_barrier(0);
             }
-            forget();
+            forget(false);  // (x is not needed any more)
 #pragma unroll 2
             for (int w = NW - 1; w > wave; --w) r = s_map[1][w][lane].of(r);
 #pragma unroll

@@ -135,6 +135,26 @@ def test_norm_in_place():
     assert got[0] is a["q"] and torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
+@pytest.mark.parametrize("dtype,T", [(BF16, 30001), (F32, 15000)])
+def test_norm_larger_than_the_caches(dtype, T):
+    # (as the first half and the second by themselves, which are not)
+    H, hk, d = 32, 8, 128
+    x = torch.randn((T, H + hk, d), device="cuda").to(dtype)
+    dy = torch.randn((T, H + hk, d), device="cuda").to(dtype)
+    pos = torch.arange(T, dtype=torch.int32, device="cuda")
+    kw = dict(norm=gdn.GDN_NORM_RMS, q_weight=torch.rand(d, device="cuda") + 0.5, inv_freq=torch.rand(32, device="cuda"))
+    assert T * (H + hk) * d * x.element_size() > 1 << 28
+    half = T // 2
+    whole = gdn.gdn_qk_norm(x[:, :H], x[:, H:], positions=pos, **kw)
+    g = dy[:, :H].contiguous(), dy[:, H:].contiguous()
+    back = gdn.gdn_qk_norm_backward(x[:, :H], x[:, H:], *g, positions=pos, **kw)
+    for sl in (slice(0, half), slice(half, T)):
+        part = gdn.gdn_qk_norm(x[sl, :H], x[sl, H:], positions=pos[sl], **kw)
+        assert torch.equal(part[0], whole[0][sl]) and torch.equal(part[1], whole[1][sl])
+        part = gdn.gdn_qk_norm_backward(x[sl, :H], x[sl, H:], g[0][sl], g[1][sl], positions=pos[sl], **kw)
+        assert torch.equal(part[0], back[0][sl]) and torch.equal(part[1], back[1][sl])
+
+
 @pytest.mark.parametrize("position", [0, 1, (1 << 20) + 1, (1 << 31) - 1, -(1 << 31)])
 def test_norm_far_positions(position):
     a = norm_case(4, 2, 1, 128, 0, False, 128, False, F32, True, seed=7)
@@ -297,6 +317,22 @@ def test_scan_nan_and_inf_stay_in_their_sequence():
         assert not math.isfinite(float(d0[1, 2])) and int((~torch.isfinite(d0)).sum()) == 1
 
 
+def test_scan_past_32_bits():
+    # more than 2^32 elements: a part of the channels is as by itself
+    T, C = 1100003, 4096
+    x = torch.randn((T, C), device="cuda", dtype=BF16)
+    g = torch.empty((T, C), device="cuda").uniform_(-0.3, 0.0)
+    cu = i32([0, 700001, T])
+    h, final = gdn.gdn_scan(x, g, cu, mix=True)
+    for c in (0, C - 8):
+        part, last = gdn.gdn_scan(x[:, c:c + 8].contiguous(), g[:, c:c + 8].contiguous(), cu, mix=True)
+        assert torch.equal(part, h[:, c:c + 8]) and torch.equal(last, final[:, c:c + 8])
+    dx, dg, d0 = gdn.gdn_scan_backward(x, g, cu, h, mix=True)
+    for c in (0, C - 8):
+        part = gdn.gdn_scan_backward(*(t[:, c:c + 8].contiguous() for t in (x, g)), cu, h[:, c:c + 8].contiguous(), mix=True)
+        assert all(torch.equal(p, w[:, c:c + 8]) for p, w in zip(part, (dx, dg, d0)))
+
+
 def test_scan_offsets_that_are_none():
     # outputs are then no one's, but nothing outside the arrays is touched and the call ends
     a, (dh, df) = scan_case([300, 300], 64, False, True, F32, seed=13)
@@ -367,6 +403,21 @@ def shared_server(groups, page, hkv, dk, dv, seed, rows=True):
     return server, [new for _, reqs in groups for _, new in reqs], [0] + [int(x) for x in np.cumsum(sizes)], [p for p, _ in groups]
 
 
+@pytest.fixture(params=["1", "0", None], ids=["shared", "apart", "planned"])
+def share(request, monkeypatch):
+    """The beginnings read once, by each request, or as the library plans."""
+    if request.param is None:
+        monkeypatch.delenv("GDN_PREFIX_SHARE", raising=False)
+    else:
+        monkeypatch.setenv("GDN_PREFIX_SHARE", request.param)
+    return request.param
+
+
+@pytest.fixture
+def always(monkeypatch):
+    monkeypatch.setenv("GDN_PREFIX_SHARE", "1")
+
+
 def prefix_check(server, lens, offsets, shared, H, dtype, seed=0, extra=2, **kw):
     gen = torch.Generator().manual_seed(seed + 100)
     dk, dv, T = server.k.shape[3], server.v.shape[3], sum(lens)
@@ -402,7 +453,7 @@ def prefix_check(server, lens, offsets, shared, H, dtype, seed=0, extra=2, **kw)
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("dk,dv", [(64, 64), (128, 128), (64, 128), (128, 64)])
 @pytest.mark.parametrize("page,hkv,G", [(64, 2, 1), (128, 1, 7), (256, 2, 4), (64, 1, 20)])
-def test_prefix(dtype, dk, dv, page, hkv, G):
+def test_prefix(always, dtype, dk, dv, page, hkv, G):
     groups = [(1300, [(5, 1), (64, 1), (0, 1), (300, 2)]), (0, [(10, 1), (700, 1)]), (257, [(1, 3)]),
               (64, [(63, 1), (1, 0), (128, 40)]), (page - 1, [(3, 1), (9, 1)])]
     log(f"prefix page={page} H_kv={hkv} G={G} dk={dk} dv={dv} {dtype}")
@@ -412,7 +463,7 @@ def test_prefix(dtype, dk, dv, page, hkv, G):
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("hints", [{}, dict(max_new=1, max_kv=10240, max_prefix=9000), dict(max_new=1, max_kv=64, max_prefix=64),
                                    dict(max_new=4000, max_prefix=100000)])
-def test_prefix_long(dtype, hints):
+def test_prefix_long(share, dtype, hints):
     groups = [(9000, [(i * 37 % 700, 1) for i in range(40)])]
     prefix_check(*shared_server(groups, 64, 2, 128, 128, seed=3), 8, dtype, **hints)
 
@@ -422,11 +473,11 @@ def test_prefix_long(dtype, hints):
     [(4096, [(0, 300), (17, 1), (0, 129)])], [(1000, [(0, 1)] * 3), (2000, [(5, 2)] * 2), (3000, [(9, 200), (0, 7)])],
     [(640, [(0, 1)] * 33), (64, [(0, 33), (0, 1)])], [(300, [(0, 0), (0, 0)]), (300, [(1, 1), (2, 0), (3, 5)])],
     [(70, [(0, 1), (0, 1)])] * 70, [(6000, [(3000, 1), (1, 1), (9000, 1)])]])
-def test_prefix_of_many_and_few_rows(dtype, groups):
+def test_prefix_of_many_and_few_rows(share, dtype, groups):
     prefix_check(*shared_server(groups, 64, 1, 64, 64, seed=4), 4, dtype)
 
 
-def test_prefix_requests_that_take_no_part():
+def test_prefix_requests_that_take_no_part(share):
     # of the second group one request holds less than the beginning and one has been refused (it holds fewer tokens than it
     # adds); requests behind the last group are in none
     server, lens, offsets, shared = shared_server([(640, [(0, 1), (70, 2)]), (700, [(5, 1), (5, 1), (40, 3), (0, 1)]),
@@ -444,7 +495,7 @@ def test_prefix_requests_that_take_no_part():
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
-def test_prefix_bad_pages_and_nan(dtype):
+def test_prefix_bad_pages_and_nan(share, dtype):
     groups = [(1024, [(100, 1), (0, 1), (30, 70)]), (128, [(0, 1), (64, 2)])]
     for what in ("gone", "all gone", "nan value", "nan key", "past"):
         server, lens, offsets, shared = shared_server(groups, 64, 2, 64, 64, seed=6, rows=False)
@@ -468,14 +519,14 @@ def test_prefix_bad_pages_and_nan(dtype):
         prefix_check(server, lens, offsets, shared, 6, dtype)
 
 
-def test_prefix_rows_that_see_nothing():
+def test_prefix_rows_that_see_nothing(share):
     server, lens, offsets, shared = shared_server([(128, [(3, 1), (0, 1)])], 64, 1, 64, 64, seed=7, rows=False)
     server.rows = torch.tensor([5, -1], dtype=torch.int32)
     _, o = prefix_check(server, lens, offsets, shared, 2, BF16)
     assert bool((o[:2] == 0).all())
 
 
-def test_prefix_infinite_queries():
+def test_prefix_infinite_queries(share):
     # a row whose scores are all -Inf is NaN, as without a common beginning
     server, lens, offsets, shared = shared_server([(320, [(10, 1), (99, 1), (5, 1)])], 64, 1, 64, 64, seed=8, rows=False)
     server.k[..., 0] = 8.0
@@ -489,11 +540,11 @@ def test_prefix_infinite_queries():
 
 
 @pytest.mark.parametrize("scale", [0.0, -0.3, 4.0])
-def test_prefix_scale(scale):
+def test_prefix_scale(always, scale):
     prefix_check(*shared_server([(700, [(100, 1), (0, 3), (64, 1)])], 64, 2, 64, 64, seed=9), 6, BF16, scale=scale)
 
 
-def test_prefix_offsets_that_are_none():
+def test_prefix_offsets_that_are_none(always):
     # outputs are then no one's, but nothing outside the arrays is touched and the call ends
     server, lens, offsets, shared = shared_server([(640, [(9, 1)] * 4), (128, [(9, 2)] * 3)], 64, 2, 64, 64, seed=10)
     kc, vc, ks, vs, table, kv_lens, rows = server.to("cuda")
@@ -508,7 +559,26 @@ def test_prefix_offsets_that_are_none():
     torch.cuda.synchronize()
 
 
-def test_prefix_two_graphs_and_other_streams():
+def test_prefix_equals_requests_apart(monkeypatch):
+    # for the same call both ways: a call that the plan reads apart gives gdn_cache_attention's bits
+    server, lens, offsets, shared = shared_server([(640, [(9, 1)] * 4)], 64, 2, 64, 64, seed=12)
+    kc, vc, ks, vs, table, kv_lens, rows = server.to("cuda")
+    q = torch.randn((4, 4, 64), device="cuda").to(BF16)
+    cu = i32([0, 1, 2, 3, 4])
+    plain = gdn.gdn_cache_attention(q, kc, vc, ks, vs, table, kv_lens, cu, rows=rows, max_new=1, max_kv=650)
+    got = []
+    for how in ("1", "0", None):
+        monkeypatch.delenv("GDN_PREFIX_SHARE", raising=False)
+        if how:
+            monkeypatch.setenv("GDN_PREFIX_SHARE", how)
+        got.append(gdn.gdn_cache_attention_prefix(q, kc, vc, ks, vs, table, kv_lens, cu, i32(offsets), i32(shared), rows=rows,
+                                                  max_new=1, max_kv=650, max_prefix=640))
+    assert torch.equal(got[1], plain) and torch.equal(got[2], plain)
+    # each rounds p and o of its own sums
+    assert float((got[0].double() - plain.double()).norm() / plain.double().norm()) <= 2 * ref.E16
+
+
+def test_prefix_two_graphs_and_other_streams(share):
     server, lens, offsets, shared = shared_server([(3000, [(i, 1) for i in range(20)]), (640, [(0, 70), (9, 1)])], 64, 2, 128, 128,
                                                   seed=11)
     kc, vc, ks, vs, table, kv_lens, rows = server.to("cuda")
@@ -538,7 +608,7 @@ def test_prefix_two_graphs_and_other_streams():
             assert torch.equal(o, want), rep
 
 
-def test_a_server_behind_one_prompt():
+def test_a_server_behind_one_prompt(share):
     """Steps of a server: a prompt written once, its pages put into the rows of twelve requests, then tokens of each: tables,
     norm and rotation, cache write, attention behind the prompt, recurrence on a pool."""
     torch.manual_seed(31)
@@ -698,7 +768,7 @@ def test_a_training_step():
         assert abs(slope - want) <= 2e-2 * want, name
 
 
-def test_binding_refusals():
+def test_binding_refusals(always):
     x = torch.zeros((4, 2, 64), device="cuda")
     w = torch.ones(64, device="cuda")
     for kw in (dict(q=x[:, :, :32]), dict(q=x.transpose(0, 1)), dict(q=x[..., ::2]), dict(k=x[:3]), dict(positions=i32([0] * 4)),

@@ -132,16 +132,28 @@ def _prefix(lib, q=FAKE, kc=FAKE, vc=FAKE, ks=FAKE, vs=FAKE, table=FAKE, rows=NU
     (dict(table=NUL), INVALID), (dict(kc=BAD), INVALID), (dict(vs=NUL), INVALID), (dict(go=NUL), INVALID),
     (dict(go=BAD), INVALID), (dict(pl=NUL), INVALID), (dict(ws=NUL), INVALID), (dict(wb=16), INVALID),
     (dict(T=0, n=0, q=NUL, go=NUL), OK)])
-def test_prefix_refusals(lib, kw, want):
+def test_prefix_refusals(lib, monkeypatch, kw, want):
+    monkeypatch.setenv("GDN_PREFIX_SHARE", "1")  # (so small a call would not be planned to need a workspace)
     assert _prefix(lib, **kw) == want
 
 
-def test_prefix_workspace_sizes():
+def test_prefix_workspace_sizes(monkeypatch):
+    monkeypatch.delenv("GDN_PREFIX_SHARE", raising=False)
     size = gdn.gdn_cache_attention_prefix_workspace_bytes
     sizes = (64, 1024, 32, 8, 128, 128)
     plain = gdn.gdn_cache_attention_workspace_bytes(8, 8, 1, 9000, *sizes)
     assert size(8, 8, 8, 1, 9000, 4096, *sizes) == plain and size(8, 0, 8, 1, 9000, 4096, *sizes) == plain
-    assert size(8, 1, 8, 1, 9000, 4096, *sizes) > 0
+    # one new token of each: little to save, then much; and forced either way
+    assert size(8, 1, 8, 1, 1100, 1024, *sizes) == gdn.gdn_cache_attention_workspace_bytes(8, 8, 1, 1100, *sizes)
+    assert size(64, 1, 64, 1, 17000, 16384, *sizes) > gdn.gdn_cache_attention_workspace_bytes(64, 64, 1, 17000, *sizes)
+    # 256 new tokens keep the matrix cores busy by themselves
+    assert size(8, 1, 2048, 256, 17000, 16384, *sizes) == gdn.gdn_cache_attention_workspace_bytes(8, 2048, 256, 17000, *sizes)
+    monkeypatch.setenv("GDN_PREFIX_SHARE", "1")
+    assert size(8, 1, 8, 1, 1100, 1024, *sizes) > gdn.gdn_cache_attention_workspace_bytes(8, 8, 1, 1100, *sizes)
+    assert size(8, 8, 8, 1, 9000, 4096, *sizes) == plain
+    monkeypatch.setenv("GDN_PREFIX_SHARE", "0")
+    assert size(64, 1, 64, 1, 17000, 16384, *sizes) == gdn.gdn_cache_attention_workspace_bytes(64, 64, 1, 17000, *sizes)
+    monkeypatch.delenv("GDN_PREFIX_SHARE")
     assert size(8, 1, 0, 1, 9000, 4096, *sizes) == 0 and size(8, -1, 8, 1, 9000, 4096, *sizes) == 0
 
 
