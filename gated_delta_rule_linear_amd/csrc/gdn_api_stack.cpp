@@ -105,7 +105,7 @@ int32_t norm_arguments(const gdn::QkNormLaunch& p, int32_t norm, int32_t dtype) 
 int32_t scan_sizes(int64_t T, int32_t C) {
     if (T < 0 || T > INT32_MAX || C < 1) return GDN_ERR_INVALID_ARG;
     if (C % 4 != 0) return GDN_ERR_UNSUPPORTED;
-    if ((double)T * C > (double)((int64_t)1 << 36)) return GDN_ERR_UNSUPPORTED;  // grids of less than 2^24 workgroups
+    if ((T + 63) / 64 * (((int64_t)C + 255) / 256) >= 1 << 23) return GDN_ERR_UNSUPPORTED;  // grids of less than 2^32 threads
     return GDN_OK;
 }
 int32_t scan_arguments(const gdn::ScanLaunch& p, int32_t dtype) {

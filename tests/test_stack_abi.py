@@ -77,7 +77,8 @@ def _scan(lib, x=FAKE, g=FAKE, cu=FAKE, n=2, T=9, C=64, mix=0, s0=NUL, s1=NUL, h
 
 SCAN = [
     (dict(T=-1), INVALID), (dict(T=1 << 31), INVALID), (dict(C=0), INVALID), (dict(C=-4), INVALID), (dict(C=6), UNSUPPORTED),
-    (dict(T=(1 << 31) - 1, C=1 << 10), UNSUPPORTED), (dict(n=-1), INVALID), (dict(n=0), INVALID), (dict(dt=7), UNSUPPORTED),
+    (dict(T=(1 << 31) - 1, C=1 << 10), UNSUPPORTED), (dict(T=1 << 29, C=4), UNSUPPORTED),
+    (dict(T=1 << 20, C=1 << 19), UNSUPPORTED), (dict(n=-1), INVALID), (dict(n=0), INVALID), (dict(dt=7), UNSUPPORTED),
     (dict(x=BAD), INVALID), (dict(g=NUL), INVALID), (dict(cu=NUL), INVALID), (dict(cu=BAD), INVALID), (dict(s0=BAD), INVALID),
     (dict(ck=BAD), INVALID), (dict(ws=NUL), INVALID), (dict(ws=BAD), INVALID), (dict(wb=64), INVALID)]
 
