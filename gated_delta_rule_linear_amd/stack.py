@@ -17,6 +17,7 @@ import gated_delta_rule_linear_amd as _gdn
 from .serve import _cache, _device_of, _elsewhere, _On, _space, _stream, _take
 
 GDN_NORM_NONE, GDN_NORM_L2, GDN_NORM_RMS = range(3)
+_DENSE = torch.contiguous_format
 
 
 def bind(lib):
@@ -50,17 +51,18 @@ def bind(lib):
 
 def _heads(t, name, dtype, tokens, d, device):
     """Address, token stride and heads of a [tokens, heads, d] tensor whose heads lie side by side."""
-    if t.dim() != 3 or t.shape[0] != tokens or t.shape[2] != d:
-        raise ValueError(f"{name} must be [{tokens}, heads, {d}], got {list(t.shape)}")
+    if t.dim() == 3:
+        (n, heads, channels), (stride, head, channel) = t.shape, t.stride()
+        if n == tokens and channels == d and channel == 1 and (head == d or heads < 2) and t.dtype is dtype \
+                and t.get_device() == device:
+            return t.data_ptr(), stride if n > 1 else max(stride, heads * d), heads
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 3 or t.shape[0] != tokens or t.shape[2] != d:
+        raise ValueError(f"{name} must be [{tokens}, heads, {d}], got {list(t.shape)}")
     if t.get_device() != device:
         raise ValueError(f"{name} must be on the device of the call's first tensor")
-    stride, head, channel = t.stride()
-    heads = t.shape[1]
-    if channel != 1 or (head != d and heads > 1):
-        raise ValueError(f"the heads of a token of {name} must lie side by side")
-    return t.data_ptr(), stride if tokens > 1 else max(stride, heads * d), heads
+    raise ValueError(f"the heads of a token of {name} must lie side by side")
 
 
 def _norm_arguments(q, k, q_weight, k_weight, positions, inv_freq, dev):
@@ -72,16 +74,15 @@ def _norm_arguments(q, k, q_weight, k_weight, positions, inv_freq, dev):
     f32 = torch.float32
     wq = None if q_weight is None else _take(q_weight, "q_weight", f32, (d,), dev)
     wk = None if k_weight is None else _take(k_weight, "k_weight", f32, (d,), dev)
-    if (positions is None) != (inv_freq is None):
-        raise ValueError("positions and inv_freq go together")
     pos = freq = None
     rotary = 0
-    if positions is not None:
+    if positions is not None and inv_freq is not None:
+        (pairs,) = inv_freq.shape
         pos = _take(positions, "positions", torch.int32, (T,), dev)
-        if inv_freq.dim() != 1:
-            raise ValueError("inv_freq must have 1 dimension")
-        freq = _take(inv_freq, "inv_freq", f32, (inv_freq.shape[0],), dev)
-        rotary = 2 * inv_freq.shape[0]
+        freq = _take(inv_freq, "inv_freq", f32, (pairs,), dev)
+        rotary = 2 * pairs
+    elif positions is not None or inv_freq is not None:
+        raise ValueError("positions and inv_freq go together")
     return T, H, hk, d, qp, qs, kp, ks, wq, wk, pos, freq, rotary
 
 
@@ -100,7 +101,7 @@ def gdn_qk_norm(q, k=None, norm: int = GDN_NORM_RMS, eps: float = 1e-6, q_weight
     T, H, hk, d, qp, qs, kp, ks, wq, wk, pos, freq, rotary = _norm_arguments(q, k, q_weight, k_weight, positions, inv_freq,
                                                                              dev)
     if q_out is None:
-        q_out = q.new_empty((T, H, d))
+        q_out = torch.empty_like(q, memory_format=_DENSE)
         qo = q_out.data_ptr()
     else:
         qo = _take(q_out, "q_out", q.dtype, (T, H, d), dev)
@@ -109,7 +110,7 @@ def gdn_qk_norm(q, k=None, norm: int = GDN_NORM_RMS, eps: float = 1e-6, q_weight
         if k_out is not None:
             raise ValueError("k_out without k")
     elif k_out is None:
-        k_out = q.new_empty((T, hk, d))
+        k_out = torch.empty_like(k, memory_format=_DENSE)
         ko = k_out.data_ptr()
     else:
         ko = _take(k_out, "k_out", q.dtype, (T, hk, d), dev)
@@ -142,12 +143,12 @@ def gdn_qk_norm_backward(q, k, d_q_out, d_k_out, norm: int = GDN_NORM_RMS, eps: 
     gq = _take(d_q_out, "d_q_out", q.dtype, (T, H, d), dev)
     gk = None if k is None else _take(d_k_out, "d_k_out", q.dtype, (T, hk, d), dev)
     if dq is None:
-        dq = q.new_empty((T, H, d))
+        dq = torch.empty_like(q, memory_format=_DENSE)
     dqp, dqs, h2 = _heads(dq, "dq", q.dtype, T, d, dev)
     dkp, dks, h3 = None, 0, 0
     if k is not None:
         if dk is None:
-            dk = q.new_empty((T, hk, d))
+            dk = torch.empty_like(k, memory_format=_DENSE)
         dkp, dks, h3 = _heads(dk, "dk", q.dtype, T, d, dev)
     if h2 != H or h3 != hk:
         raise ValueError("dq and dk must have the heads of q and k")
@@ -226,7 +227,9 @@ def gdn_scan(x, g, cu_seqlens, mix: bool = False, initial_state=None, final_stat
     T, C, n, xp, gp, cu, s0, kept = _scan_arguments(x, g, cu_seqlens, initial_state, checkpoints, lib, dev)
     if h is None:
         h = torch.empty_like(x)
-    hp = _take(h, "h", x.dtype, (T, C), dev)
+        hp = h.data_ptr()
+    else:
+        hp = _take(h, "h", x.dtype, (T, C), dev)
     if final_state is None and output_final_state:
         final_state = g.new_empty((n, C))
     sp = None if final_state is None else _take(final_state, "final_state", torch.float32, (n, C), dev)
