@@ -39,7 +39,8 @@ typedef float floatx16 __attribute__((ext_vector_type(16)));
 constexpr int kTile = 64;      // tokens of a tile
 constexpr int kFewRows = 32;   // a request with up to so many rows is one of few rows
 constexpr int kMinPart = 512;  // tokens of a part of a request's cache, at least (measured for few rows)
-constexpr int kMinShared = 256;  // of a beginning that requests share
+constexpr int kMinShared = 256;  // of a beginning that requests share (24 requests in four groups behind up to 4,224, in full
+                                 // precision, read apart: 24.6 us, with 128 24.5, with 512 28.5)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kInf = __builtin_inff();
 
@@ -917,9 +918,10 @@ __device__ __forceinline__ void attention_tile(const Attention& a, TileShared<DK
         if (mx == -kInf && some) sum += 1.f;
     }
     if constexpr (REACH != kAll) {
-        // Rows of the output lie whole in memory, where a lane has pieces of one: they
-        // change places through LDS, which the last tile has left (64 requests behind
-        // 4,096 tokens).  Piece p of row c goes to place p ^ c.
+        // A row of the output is contiguous in the workspace, and a lane holds pieces of
+        // one row: the rows change places through LDS, free behind the last step's
+        // barrier, so that whole rows are written (64 requests behind 4,096 tokens: 27.0
+        // to 25.4 us).  Piece p of row c goes to place p ^ c, which spreads the banks.
         constexpr int P = DV / 4;
         floatx4* const s_o = reinterpret_cast<floatx4*>(&sh) + wave * 32 * P;
 #pragma unroll
@@ -1055,6 +1057,18 @@ __global__ __launch_bounds__(256) void attention_join_kernel(Attention a, int32_
 // mask, which the kernels above take as such (kPrefix); what is behind it is a
 // request each (kOwn).  All parts go to the workspace at their row of o and are
 // joined in one launch.
+//
+// Three launches: groups, parts, join.  The lengths and groups are on the device, so a
+// small kernel makes one record of each for the other two, which would each find it by a
+// search.  What a beginning takes is products, 4 operations a code and row, at
+// 0.72 to 0.82 PFLOP/s where it is long; what the own tokens take is reading them.
+// 64 requests of 32 heads, 8 for keys, of 128 channels, behind 16,384 tokens and 1 to
+// 1,024 of their own, bf16: 52 us, of which 43 go to the parts, 7 to the join (it
+// reads the 17.6 MB of partial rows) and 3 to 5 to the groups; the cache read once
+// would be 104 MB and the products 17.7 GFLOP, 15 us each.  About 15 us do not
+// depend on the lengths: launches, loads that wait for loads (record, page, codes) and
+// the partial rows.  The two kinds of parts as launches after each other: 71 where one
+// launch took 60.
 struct Groups {
     const int32_t *offsets, *shared;
     int32_t count;
@@ -1185,7 +1199,10 @@ __global__ __launch_bounds__(256) void prefix_join_kernel(Attention p, Attention
 // ---------------------------------------------------------------- planning
 
 constexpr int64_t kAtOnce = 512;  // workgroups that the device holds: two on each compute unit
-constexpr int64_t kSharedAtOnce = 256;  // of them for beginnings that requests share
+// Of them for beginnings that requests share, whose parts run beside those of the own
+// tokens, and each of which is a row of the workspace for every row of o (64 requests
+// behind 16,384 tokens: 59 us; 128 and 384 61, 512 67).
+constexpr int64_t kSharedAtOnce = 256;
 constexpr int64_t kTailCache = 2048;  // tokens in front of a call's last tiles, from which on they are cut
 
 struct Plan {

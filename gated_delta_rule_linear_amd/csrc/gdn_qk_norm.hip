@@ -13,6 +13,15 @@
 // their partners from the second, or 8 neighbours, so nothing is exchanged for the
 // rotation.  The angles of a token are the same for all its heads: a lane forms
 // its four once and goes through the heads, two loads at a time.
+//
+// Measured, bf16 (a copy reaches 5.1 TB/s, and 5.95 where it overwrites its input):
+// unit vectors of 65,536 tokens of 64 heads of 128 channels, 2.147 GB in 361 to 373 us,
+// 5.8 TB/s, and no byte moves twice (FETCH_SIZE and WRITE_SIZE 1.074 GB each).
+// Gradients of 32,768 tokens of 40 heads with weights and rotation, 1.007 GB in 180 to
+// 189 us, 5.5 TB/s, of which the weights' sums are 4.5.  64 tokens take 3.8 us, about an
+// empty launch.  Heads in steps of one load or four, and half or twice as many
+// workgroups, are slower or the same.  Tensors that the caches cannot hold are read
+// and written past them: 380 us where it was 406, the gradients 189 where it was 200.
 #include <algorithm>
 
 #include "gdn_device.h"
