@@ -184,9 +184,10 @@ int32_t validate_prefix(const gdn::CachePrefixLaunch& p, hipStream_t s) {
         !to_host(table, p.all.block_table, (int64_t)p.all.num_rows * p.all.max_blocks, s) ||
         (p.all.rows && !to_host(rows, p.all.rows, p.all.num_seqs, s)))
         return GDN_ERR_HIP;
-    if (offsets.front() != 0 || offsets.back() > p.all.num_seqs) return GDN_ERR_DOMAIN;
+    if (offsets.front() != 0) return GDN_ERR_DOMAIN;
     for (int32_t g = 0; g < p.num_groups; ++g) {
-        if (offsets[(size_t)g + 1] < offsets[(size_t)g] || shared[(size_t)g] < 0) return GDN_ERR_DOMAIN;
+        if (offsets[(size_t)g + 1] < offsets[(size_t)g] || offsets[(size_t)g + 1] > p.all.num_seqs || shared[(size_t)g] < 0)
+            return GDN_ERR_DOMAIN;
         const int64_t blocks = std::min<int64_t>(shared[(size_t)g] / p.all.page_size, p.all.max_blocks);
         const int32_t* first = nullptr;
         for (int32_t n = offsets[(size_t)g]; n < offsets[(size_t)g + 1]; ++n) {

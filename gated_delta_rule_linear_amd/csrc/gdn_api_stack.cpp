@@ -30,13 +30,14 @@ bool to_host(std::vector<T>& to, const T* from, int64_t n, hipStream_t s) {
     return n == 0 || (hipMemcpyAsync(to.data(), from, sizeof(T) * (size_t)n, hipMemcpyDeviceToHost, s) == hipSuccess &&
                       hipStreamSynchronize(s) == hipSuccess);
 }
-// Offsets that rise from 0 to T, or to at most T; log-decays of at most 0.
-int32_t check_offsets(const int32_t* cu_seqlens, int32_t num_seqs, int64_t T, bool whole, hipStream_t s) {
+// Offsets that rise from 0 to T, or to at most T, and where they end; log-decays of at most 0.
+int32_t check_offsets(const int32_t* cu_seqlens, int32_t num_seqs, int64_t T, bool whole, hipStream_t s, int64_t* end) {
     std::vector<int32_t> cu;
     if (!to_host(cu, cu_seqlens, (int64_t)num_seqs + 1, s)) return GDN_ERR_HIP;
     if (cu.front() != 0 || cu.back() > T || (whole && cu.back() != T)) return GDN_ERR_DOMAIN;
     for (size_t n = 1; n < cu.size(); ++n)
         if (cu[n] < cu[n - 1]) return GDN_ERR_DOMAIN;
+    *end = cu.back();
     return GDN_OK;
 }
 int32_t check_gates(const float* gates, int64_t n, hipStream_t s) {
@@ -49,8 +50,9 @@ int32_t check_gates(const float* gates, int64_t n, hipStream_t s) {
     return GDN_OK;
 }
 int32_t validate_scan(const gdn::ScanLaunch& p, hipStream_t s) {
-    const int32_t st = check_offsets(p.cu_seqlens, p.num_seqs, p.T, false, s);
-    return st != GDN_OK ? st : check_gates(p.g, p.T * p.C, s);
+    int64_t end = 0;
+    const int32_t st = check_offsets(p.cu_seqlens, p.num_seqs, p.T, false, s, &end);
+    return st != GDN_OK ? st : check_gates(p.g, end * p.C, s);  // (rows behind the sequences hold anything)
 }
 int32_t validate_pool(const gdn::ScanPoolLaunch& p, hipStream_t s) {
     std::vector<int32_t> slots;
@@ -61,8 +63,9 @@ int32_t validate_pool(const gdn::ScanPoolLaunch& p, hipStream_t s) {
         if (seen[(size_t)x]) return GDN_ERR_DOMAIN;
         seen[(size_t)x] = 1;
     }
-    const int32_t st = p.cu_seqlens ? check_offsets(p.cu_seqlens, p.num_seqs, p.T, true, s) : GDN_OK;
-    return st != GDN_OK ? st : check_gates(p.g, p.T * p.C, s);
+    int64_t end = p.T;
+    const int32_t st = p.cu_seqlens ? check_offsets(p.cu_seqlens, p.num_seqs, p.T, true, s, &end) : GDN_OK;
+    return st != GDN_OK ? st : check_gates(p.g, end * p.C, s);
 }
 
 // The host checks allocate: no exception leaves a C entry point.
@@ -88,7 +91,8 @@ int32_t norm_arguments(const gdn::QkNormLaunch& p, int32_t norm, int32_t dtype) 
     const int32_t st = norm_sizes(p.T, p.heads[0], p.heads[1], p.d);
     if (st != GDN_OK) return st;
     if (!supported_dtype(dtype) || norm < GDN_NORM_NONE || norm > GDN_NORM_RMS) return GDN_ERR_UNSUPPORTED;
-    if (!std::isfinite(p.q_scale) || (norm != GDN_NORM_NONE && !(p.eps > 0.f && std::isfinite(p.eps)))) return GDN_ERR_INVALID_ARG;
+    // (below its least normal number the hardware's reciprocal root takes an eps as 0)
+    if (!std::isfinite(p.q_scale) || (norm != GDN_NORM_NONE && !(p.eps > 0.f && std::isnormal(p.eps)))) return GDN_ERR_INVALID_ARG;
     if (p.rotary < 0 || p.rotary > p.d || p.rotary % 8 != 0) return GDN_ERR_INVALID_ARG;
     if (p.T > 0 && p.rotary > 0 && (!aligned(p.positions, 4) || !aligned(p.inv_freq, 16))) return GDN_ERR_INVALID_ARG;
     for (int s = 0; s < 2; ++s) {
@@ -105,7 +109,8 @@ int32_t norm_arguments(const gdn::QkNormLaunch& p, int32_t norm, int32_t dtype) 
 int32_t scan_sizes(int64_t T, int32_t C) {
     if (T < 0 || T > INT32_MAX || C < 1) return GDN_ERR_INVALID_ARG;
     if (C % 4 != 0) return GDN_ERR_UNSUPPORTED;
-    if ((T + 63) / 64 * (((int64_t)C + 255) / 256) >= 1 << 23) return GDN_ERR_UNSUPPORTED;  // grids of less than 2^32 threads
+    const int64_t tiles = T > 0 ? (T + 63) / 64 : 1;  // (one without a token too: it writes the final states)
+    if (tiles * (((int64_t)C + 255) / 256) >= 1 << 23) return GDN_ERR_UNSUPPORTED;  // grids of less than 2^32 threads
     return GDN_OK;
 }
 int32_t scan_arguments(const gdn::ScanLaunch& p, int32_t dtype) {

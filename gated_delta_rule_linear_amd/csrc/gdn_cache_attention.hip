@@ -1075,7 +1075,8 @@ struct Groups {
     int4 *group, *request;  // `info` of the beginnings and of the requests
 };
 // A wave to a group.  A request that does not hold the whole beginning before its
-// new tokens (a refused one, say) takes no part: all its tokens are its own.
+// new tokens (a refused one, say), or that has no row of the table, takes no part: all
+// its tokens are its own.
 __global__ __launch_bounds__(64) void groups_kernel(Attention p, Attention o, Groups g) {
     const int lane = threadIdx.x, b = blockIdx.x;
     auto offset = [&](int32_t i) {
@@ -1085,11 +1086,14 @@ __global__ __launch_bounds__(64) void groups_kernel(Attention p, Attention o, Gr
     const int32_t n0 = offset(b), n1 = offset(b + 1);
     const int64_t room = (int64_t)o.max_blocks << o.page_log2, most = g.shared[b] < room ? g.shared[b] : room;
     const int32_t shared = most < 0 ? 0 : (int32_t)(most >> o.page_log2 << o.page_log2);
+    auto takes_part = [&](int32_t n) {
+        const int64_t len = (int64_t)o.cu[n + 1] - o.cu[n], held = o.kv_lens[n] < room ? o.kv_lens[n] : room;
+        const int32_t row = o.rows ? o.rows[n] : n;
+        return shared > 0 && len > 0 && held - len >= shared && row >= 0 && row < o.num_rows;
+    };
     int32_t first = INT32_MAX;
-    for (int32_t n = n0 + lane; n < n1; n += 64) {
-        const int64_t len = (int64_t)o.cu[n + 1] - o.cu[n];
-        if (shared > 0 && len > 0 && o.kv_lens[n] - len >= shared && n < first) first = n;
-    }
+    for (int32_t n = n0 + lane; n < n1; n += 64)
+        if (takes_part(n) && n < first) first = n;
     for (int d = 32; d > 0; d /= 2) first = min(first, __shfl_xor(first, d));
     const bool some = first < INT32_MAX;
     const int4 group = {o.cu[n0], o.cu[n1], some ? shared : 0, !some ? -1 : o.rows ? o.rows[first] : first};
@@ -1102,10 +1106,7 @@ __global__ __launch_bounds__(64) void groups_kernel(Attention p, Attention o, Gr
         if (own.kv > 0) info.w = (int32_t)own.parts();
         g.request[n] = info;
     };
-    for (int32_t n = n0 + lane; n < n1; n += 64) {
-        const int64_t len = (int64_t)o.cu[n + 1] - o.cu[n];
-        put(n, shared > 0 && len > 0 && o.kv_lens[n] - len >= shared);
-    }
+    for (int32_t n = n0 + lane; n < n1; n += 64) put(n, takes_part(n));
     // requests in front of the first group and behind the last
     if (b == 0)
         for (int32_t n = lane; n < n0; n += 64) put(n, false);
@@ -1369,6 +1370,7 @@ PrefixPlan plan(const CachePrefixLaunch& c) {
 bool shares(const CachePrefixLaunch& p) {
     const CacheAttentionLaunch& a = p.all;
     if (p.num_groups <= 0 || p.num_groups >= a.num_seqs) return false;  // no request shares with another
+    if (a.T_total * a.H >= 1 << 24) return false;  // a workgroup for each row of o in the join: grids of less than 2^32 threads
     if (const char* e = std::getenv("GDN_PREFIX_SHARE")) return e[0] != '0';
     auto bound = [&](int64_t hint, int64_t most) { return hint > 0 && hint < most ? hint : most; };
     const int64_t G = a.H / a.H_kv, rows = bound(a.max_new, (a.T_total + a.num_seqs - 1) / a.num_seqs) * G;

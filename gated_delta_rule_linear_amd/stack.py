@@ -55,7 +55,7 @@ def _heads(t, name, dtype, tokens, d, device):
         (n, heads, channels), (stride, head, channel) = t.shape, t.stride()
         if n == tokens and channels == d and channel == 1 and (head == d or heads < 2) and t.dtype is dtype \
                 and t.get_device() == device:
-            return t.data_ptr(), stride if n > 1 else max(stride, heads * d), heads
+            return t.data_ptr(), stride if n > 1 else heads * d, heads
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.dim() != 3 or t.shape[0] != tokens or t.shape[2] != d:
@@ -219,7 +219,8 @@ def gdn_scan(x, g, cu_seqlens, mix: bool = False, initial_state=None, final_stat
     """The gated linear recurrence h_t = e^g_t h_{t-1} + x_t of every channel (with `mix`: + (1 - e^g_t) x_t) over packed
     sequences; returns (h, final_state or None).  x [T, C] in bf16 or fp32, C a multiple of 4; g [T, C] in fp32, at most 0;
     cu_seqlens int32 [num_seqs + 1]; initial_state and final_state fp32 [num_seqs, C], which must not overlap.  checkpoints,
-    from gdn_scan_checkpoints(x), receives what gdn_scan_backward takes.  Rows behind cu_seqlens[-1] are not written."""
+    from gdn_scan_checkpoints(x), receives what gdn_scan_backward takes.  h may be x.  Rows behind cu_seqlens[-1] are not
+    written."""
     lib, dt, dev = _gdn._load(), _gdn._dtype_code(x), _device_of(x, "x")
     if _elsewhere(dev, stream):
         with _On(dev, stream):

@@ -58,7 +58,7 @@ typedef enum gdn_norm { GDN_NORM_NONE = 0, GDN_NORM_L2 = 1, GDN_NORM_RMS = 2 } g
  *               NULL with rotary 0
  *   inv_freq    device fp32 [rotary / 2]; NULL with rotary 0
  *   rotary      a multiple of 8 from 0 to d
- *   eps         > 0 (of any value with GDN_NORM_NONE)
+ *   eps         a normal number > 0 (of any value with GDN_NORM_NONE)
  *   q_out, k_out  device [T_total, H, d] and [T_total, H_k, d], dtype, contiguous.
  *               q_out may be q where q_stride is H * d, k_out k likewise; else
  *               outputs and inputs do not overlap.
@@ -110,8 +110,8 @@ size_t gdn_qk_norm_backward_workspace_bytes(int64_t T_total, int32_t H, int32_t 
  *   final_state    device fp32 [num_seqs, C], written (a sequence without a token
  *               keeps its initial state), or NULL.  It must not overlap
  *               initial_state.
- *   h           device [T_total, C], dtype.  Rows behind cu_seqlens[num_seqs] are
- *               left as they were.
+ *   h           device [T_total, C], dtype; it may be x, and else overlaps no
+ *               input.  Rows behind cu_seqlens[num_seqs] are left as they were.
  *   checkpoints device, gdn_scan_checkpoint_bytes(T_total, C) bytes, written, or
  *               NULL: states along the sequences, for gdn_scan_backward
  *   workspace   gdn_scan_workspace_bytes(T_total, C) bytes, 16-byte aligned
@@ -119,7 +119,7 @@ size_t gdn_qk_norm_backward_workspace_bytes(int64_t T_total, int32_t H, int32_t 
  * States are fp32; h is rounded once.  Alignment: 16 bytes, cu_seqlens 4.  The
  * result does not depend on timing.  Below 2^23 tiles of 64 tokens and 256 channels.
  * GDN_VALIDATE=1 returns GDN_ERR_DOMAIN for offsets that decrease, do not begin
- * at 0 or end behind T_total, and for g above 0 or NaN. */
+ * at 0 or end behind T_total, and for g of a sequence above 0 or NaN. */
 int32_t gdn_scan(const void* x, const float* g, const int32_t* cu_seqlens, int32_t num_seqs, int64_t T_total, int32_t C,
                  int32_t mix, const float* initial_state, float* final_state, void* h, float* checkpoints,
                  int32_t dtype, void* workspace, size_t workspace_bytes, void* stream);
@@ -137,8 +137,10 @@ size_t gdn_scan_backward_workspace_bytes(int64_t T_total, int32_t C);
  *   d_final_state  device fp32 [num_seqs, C], or NULL for 0
  *   checkpoints    what gdn_scan wrote for the same inputs, or NULL: the states
  *                  are computed again, for one more reading of x and g
- *   dx             device [T_total, C], dtype, written
- *   dg             device fp32 [T_total, C], written
+ *   dx             device [T_total, C], dtype, written; it may be d_h, and else
+ *                  overlaps no input
+ *   dg             device fp32 [T_total, C], written.  Rows of dx and dg behind
+ *                  cu_seqlens[num_seqs] are left as they were.
  *   d_initial_state  device fp32 [num_seqs, C], written (the final state's
  *                  gradient for a sequence without a token), or NULL.  It must not
  *                  overlap d_final_state.
@@ -166,7 +168,7 @@ int32_t gdn_scan_backward(const void* x, const float* g, const int32_t* cu_seqle
  *   commit      device int32 [num_seqs], or NULL for all: the state that is stored
  *               is the one after the first commit[n] tokens (cut to the request's
  *               tokens; 0 or less: the state stays).  h is written for every token.
- *   h           device [T_total, C], dtype
+ *   h           device [T_total, C], dtype; it may be x, and else overlaps no input
  *
  * Alignment: 16 bytes, index arrays 4.
  * GDN_VALIDATE=1 returns GDN_ERR_DOMAIN for offsets that decrease or do not end
@@ -192,8 +194,8 @@ int32_t gdn_scan_pool(const void* x, const float* g, float* states, const int32_
  * The other arguments and the result are gdn_cache_attention's: the rows of the
  * block table that a group's requests have agree in the blocks of the beginning,
  * and these are read through one of them.  A request that holds fewer than
- * prefix_lens tokens before its new ones (a refused one, say) takes no part and
- * reads all of its own.  Where the bounds say that reading the beginnings apart
+ * prefix_lens tokens before its new ones (a refused one, say), or whose row is
+ * outside the table, takes no part and reads all of its own.  Where the bounds say that reading the beginnings apart
  * would cost more than it saves (short beginnings, few requests, requests of more
  * than 128 rows) the call is gdn_cache_attention itself.  Sums of parts are joined
  * in an order that sizes, lengths and groups decide; outputs differ from

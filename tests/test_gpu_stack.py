@@ -333,6 +333,45 @@ def test_scan_past_32_bits():
         assert all(torch.equal(p, w[:, c:c + 8]) for p, w in zip(part, (dx, dg, d0)))
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("mix", [False, True])
+def test_scan_in_place(dtype, mix):
+    a, (dh, df) = scan_case([700, 0, 3, 601, 64], 260, mix, True, dtype, seed=16, extra=5)
+    end, x = 1368, a["x"].clone()
+    want, final = gdn.gdn_scan(**a)
+    back = gdn.gdn_scan_backward(**a, d_h=dh, d_final_state=df)
+    h, got = gdn.gdn_scan(**{**a, "x": x}, h=x)
+    assert h is x and torch.equal(x[:end], want[:end]) and torch.equal(x[end:], a["x"][end:]) and torch.equal(got, final)
+    # dx over d_h, by the library's own entry point
+    lib, (T, C) = gdn._load(), a["x"].shape
+    dx, dg, d0 = dh.clone(), torch.full_like(a["g"], 7.0), torch.empty_like(df)
+    space = torch.empty(gdn.gdn_scan_backward_workspace_bytes(T, C), dtype=torch.uint8, device="cuda")
+    st = lib.gdn_scan_backward(a["x"].data_ptr(), a["g"].data_ptr(), a["cu_seqlens"].data_ptr(), 5, T, C, mix,
+                               a["initial_state"].data_ptr(), None, dx.data_ptr(), df.data_ptr(), dx.data_ptr(), dg.data_ptr(),
+                               d0.data_ptr(), gdn._dtype_code(dx), space.data_ptr(), space.numel(),
+                               torch.cuda.current_stream().cuda_stream)
+    assert st == gdn.GDN_OK
+    assert torch.equal(dx[:end], back[0][:end]) and torch.equal(dg[:end], back[1][:end]) and torch.equal(d0, back[2])
+    assert torch.equal(dx[end:], dh[end:]) and bool((dg[end:] == 7.0).all())
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_scan_pool_in_place(dtype):
+    a, _ = scan_case([3, 1, 0, 5], 516, True, False, dtype, seed=17)
+    cu, slots = a["cu_seqlens"], i32([2, 0, 1, 4])
+    pools = [torch.ones((5, 516), device="cuda") for _ in range(2)]
+    want = gdn.gdn_scan_pool(a["x"], a["g"], pools[0], slots, cu_seqlens=cu, mix=True)
+    got = gdn.gdn_scan_pool(a["x"], a["g"], pools[1], slots, cu_seqlens=cu, mix=True, h=a["x"])
+    assert got is a["x"] and torch.equal(got, want) and torch.equal(*pools)
+
+
+def test_norm_of_one_token_of_an_odd_row():
+    # one token: how far the next would be does not matter
+    wide = torch.randn((1, 8 * 64 + 3), device="cuda").to(BF16)
+    q = wide.as_strided((1, 8, 64), (515, 64, 1))
+    assert torch.equal(gdn.gdn_qk_norm(q)[0], gdn.gdn_qk_norm(q.contiguous())[0])
+
+
 def test_scan_offsets_that_are_none():
     # outputs are then no one's, but nothing outside the arrays is touched and the call ends
     a, (dh, df) = scan_case([300, 300], 64, False, True, F32, seed=13)
@@ -492,6 +531,32 @@ def test_prefix_requests_that_take_no_part(share):
         kc, vc, ks, vs, table, kv_lens, rows = server.to("cuda")
         cu = i32([0] + [int(x) for x in np.cumsum(lens)])
         assert torch.equal(gdn.gdn_cache_attention(q, kc, vc, ks, vs, table, kv_lens, cu, rows=rows), o)
+
+
+@pytest.mark.parametrize("bad", [-1, 1 << 30])
+def test_prefix_requests_without_a_row(share, bad):
+    # the first and the last request of a group have no row of the table: they see nothing, and the others all they hold
+    server, lens, offsets, shared = shared_server([(640, [(4, 1), (70, 2), (0, 1), (9, 1)]), (200, [(0, 1), (5, 70)])], 64, 2, 64,
+                                                  64, seed=14)
+    for n in (0, 3, 4):
+        server.rows[n] = bad
+    prefix_check(server, lens, offsets, shared, 6, BF16)
+
+
+def test_prefix_lengths_past_the_table(share):
+    # requests that say to hold more than the table has room for hold what it has
+    server, lens, offsets, shared = shared_server([(640, [(4, 1), (0, 2), (10, 1)]), (128, [(500, 1), (7, 1)])], 64, 2, 64, 64,
+                                                  seed=15)
+    kc, vc, ks, vs, table, kv_lens, rows = server.to("cuda")
+    room = server.table.shape[1] * 64
+    shared = [room, 128]
+    q = torch.randn((sum(lens), 4, 64), device="cuda").to(BF16)
+    cu, most = i32([0] + [int(x) for x in np.cumsum(lens)]), kv_lens.clamp(max=room)
+    outs = []
+    for kv in (most.clone(), most.clone()):
+        kv[1] = room if not outs else 1 << 30
+        outs.append(gdn.gdn_cache_attention_prefix(q, kc, vc, ks, vs, table, kv, cu, i32(offsets), i32(shared), rows=rows))
+    assert torch.equal(outs[0], outs[1])
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
@@ -819,12 +884,26 @@ def test_binding_refusals(always):
         gdn.gdn_cache_attention_prefix(q, kc, vc, ks, vs, **{**fine, "prefix_lens": i32([1]).long()})
 
 
+def test_validation_of_group_offsets(monkeypatch):
+    # one offset in the middle is past the requests
+    monkeypatch.setenv("GDN_VALIDATE", "1")
+    server, lens, offsets, shared = shared_server([(128, [(3, 1), (0, 1)]), (0, [(0, 1)])], 64, 1, 64, 64, seed=7, rows=False)
+    kc, vc, ks, vs, table, kv_lens, _ = server.to("cuda")
+    with pytest.raises(gdn.GdnError) as e:
+        gdn.gdn_cache_attention_prefix(torch.randn((3, 2, 64), device="cuda"), kc, vc, ks, vs, table, kv_lens, i32([0, 1, 2, 3]),
+                                       i32([0, 1 << 20, 3]), i32(shared))
+    assert e.value.status == gdn.GDN_ERR_DOMAIN
+
+
 def test_validation_mode(monkeypatch):
     monkeypatch.setenv("GDN_VALIDATE", "1")
     y = torch.zeros((9, 8), device="cuda")
     s, good = torch.zeros((4, 8), device="cuda"), i32([0, 4, 9])
     gdn.gdn_scan(y, y, good)
     gdn.gdn_scan(y, y, i32([0, 4, 8]))
+    behind = y.clone()
+    behind[8] = math.nan
+    gdn.gdn_scan(y, behind, i32([0, 4, 8]))
     gdn.gdn_scan_pool(y, y, s, i32([3, 1]), cu_seqlens=good)
     bad = y.clone()
     bad[3, 2] = 1e-3

@@ -42,7 +42,7 @@ NORM = [
     (dict(T=-1), INVALID), (dict(T=1 << 31), INVALID), (dict(H=-1), INVALID), (dict(hk=-1), INVALID),
     (dict(d=96), UNSUPPORTED), (dict(d=0), UNSUPPORTED), (dict(H=1 << 20), UNSUPPORTED), (dict(dt=2), UNSUPPORTED),
     (dict(norm=3), UNSUPPORTED), (dict(norm=-1), UNSUPPORTED), (dict(eps=0.0), INVALID), (dict(eps=-1e-6), INVALID),
-    (dict(eps=math.inf), INVALID), (dict(eps=math.nan), INVALID), (dict(scale=math.nan), INVALID),
+    (dict(eps=1e-42), INVALID), (dict(eps=math.inf), INVALID), (dict(eps=math.nan), INVALID), (dict(scale=math.nan), INVALID),
     (dict(rot=12), INVALID), (dict(rot=-8), INVALID), (dict(rot=136), INVALID), (dict(pos=NUL), INVALID),
     (dict(freq=NUL), INVALID), (dict(freq=BAD), INVALID), (dict(pos=BAD), INVALID), (dict(wq=BAD), INVALID),
     (dict(wk=BAD), INVALID), (dict(q=BAD), INVALID), (dict(k=NUL), INVALID), (dict(qs=511), INVALID),
@@ -78,7 +78,7 @@ def _scan(lib, x=FAKE, g=FAKE, cu=FAKE, n=2, T=9, C=64, mix=0, s0=NUL, s1=NUL, h
 SCAN = [
     (dict(T=-1), INVALID), (dict(T=1 << 31), INVALID), (dict(C=0), INVALID), (dict(C=-4), INVALID), (dict(C=6), UNSUPPORTED),
     (dict(T=(1 << 31) - 1, C=1 << 10), UNSUPPORTED), (dict(T=1 << 29, C=4), UNSUPPORTED),
-    (dict(T=1 << 20, C=1 << 19), UNSUPPORTED), (dict(n=-1), INVALID), (dict(n=0), INVALID), (dict(dt=7), UNSUPPORTED),
+    (dict(T=1 << 20, C=1 << 19), UNSUPPORTED), (dict(T=0, C=(1 << 31) - 4), UNSUPPORTED), (dict(n=-1), INVALID), (dict(n=0), INVALID), (dict(dt=7), UNSUPPORTED),
     (dict(x=BAD), INVALID), (dict(g=NUL), INVALID), (dict(cu=NUL), INVALID), (dict(cu=BAD), INVALID), (dict(s0=BAD), INVALID),
     (dict(ck=BAD), INVALID), (dict(ws=NUL), INVALID), (dict(ws=BAD), INVALID), (dict(wb=64), INVALID)]
 
@@ -154,6 +154,11 @@ def test_prefix_workspace_sizes(monkeypatch):
     assert size(8, 8, 8, 1, 9000, 4096, *sizes) == plain
     monkeypatch.setenv("GDN_PREFIX_SHARE", "0")
     assert size(64, 1, 64, 1, 17000, 16384, *sizes) == gdn.gdn_cache_attention_workspace_bytes(64, 64, 1, 17000, *sizes)
+    # more rows than a grid has workgroups are not joined, whatever is asked for
+    monkeypatch.setenv("GDN_PREFIX_SHARE", "1")
+    apart = gdn.gdn_cache_attention_workspace_bytes(8192, 1 << 20, 64, 17000, *sizes)
+    assert size(8192, 1, 1 << 20, 64, 17000, 16384, *sizes) == apart
+    assert size(8192, 1, 1 << 18, 32, 17000, 16384, *sizes) > gdn.gdn_cache_attention_workspace_bytes(8192, 1 << 18, 32, 17000, *sizes)
     monkeypatch.delenv("GDN_PREFIX_SHARE")
     assert size(8, 1, 0, 1, 9000, 4096, *sizes) == 0 and size(8, -1, 8, 1, 9000, 4096, *sizes) == 0
 
