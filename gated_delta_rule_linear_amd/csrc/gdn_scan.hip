@@ -24,13 +24,13 @@
 // before it waits: what is waited for has begun, and comes.  A map's A and e are one
 // word, written and read as such, so nothing else orders them.
 //
-// Measured, bf16 (GB/s of what has to be read and written): 65,536 tokens of 4,096
-// channels 393 us, 5.5 TB/s, where a copy reaches 5.1; four sequences of 8,192 207 us
-// forward and 347 backward (5.2 and 5.4), with `mix`, whose 1 - e^g is formed for every
-// pass over the registers, 223 and 378.  A forward pass for the maps, a fold and a
-// pass for the outputs took 1,196 us for the first; without the waits (and wrong) it
-// would take 380.  8,300 tokens of 1,028 channels in 8 sequences, fp32, 41 us: 650
-// workgroups for 512 places, and a chain of ticket, inputs, maps and outputs.  What counts:
+// Measured, bf16 (of what has to be read and written): 65,536 tokens of 4,096
+// channels 372 us, 5.8 TB/s, where a copy reaches 5.1; four sequences of 8,192 191 us
+// forward and 339 backward (5.6 and 5.6), with `mix`, whose 1 - e^g is formed for every
+// pass over the registers, 209 and 379.  A forward pass for the maps, a fold and a
+// pass for the outputs took 1,196 us for the first.  8,300 tokens of 1,028 channels in 8
+// sequences, fp32, 39 us: 650 workgroups for 512 places, and a chain of ticket, inputs,
+// maps and outputs.  What counts:
 // nothing that the rare first and last tokens need may be waited for in the tokens'
 // loop (the stores before it would be waited for too: 422 against 492 us), maps
 // that are read in whole lines (482 against 550 us with 64 tokens to a tile), and
@@ -298,13 +298,28 @@ __global__ __launch_bounds__(64 * NW, BACK ? 2 : 4) void scan_kernel(Scan a) {
         auto put = [&](float* v, int i, floatx4 y) {
             if (live) *reinterpret_cast<floatx4*>(v + (int64_t)tokens.sequence(i) * a.C + ch) = y;
         };
+        // The first pass leaves decays and inputs where the registers had g and x (346 to 339
+        // us backward, with `mix` and fp32 164 to 158 forward), but where 1 - e^g is wanted
+        // later, and where x is of half their width.
+        constexpr bool KEPT = !MIX || (!BACK && sizeof(TI) == 4);
+        auto keep = [&](int i) {
+            if constexpr (KEPT) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float al = decay(g[i][k]);
+                    if constexpr (MIX) x[i].v[k] *= one_minus_decay(g[i][k], al);
+                    g[i][k] = al;
+                }
+            }
+        };
+        auto decay_of = [&](int i, int k) { return KEPT ? g[i][k] : decay(g[i][k]); };
         auto next = [&](floatx4 s, int i) {  // the state after token i
             if (tokens.starts_at(i)) s = vector(a.init, i);
             const floatx4 in = x[i].f();
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const float al = decay(g[i][k]);
-                s[k] = __builtin_fmaf(al, s[k], MIX ? one_minus_decay(g[i][k], al) * in[k] : in[k]);
+                const float al = decay_of(i, k);
+                s[k] = __builtin_fmaf(al, s[k], KEPT ? in[k] : one_minus_decay(g[i][k], al) * in[k]);
             }
             return s;
         };
@@ -312,7 +327,7 @@ __global__ __launch_bounds__(64 * NW, BACK ? 2 : 4) void scan_kernel(Scan a) {
             if (tokens.ends_at(i)) s = vector(a.d_final, i);
             l = dh[i].f() + s;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) s[k] = decay(g[i][k]) * l[k];
+            for (int k = 0; k < 4; ++k) s[k] = decay_of(i, k) * l[k];
             return s;
         };
         // What is computed again for another pass over the tokens is not kept until then,
@@ -332,9 +347,10 @@ __global__ __launch_bounds__(64 * NW, BACK ? 2 : 4) void scan_kernel(Scan a) {
             for (int j = 0; j < L; ++j) {
                 const int i = reverse ? L - 1 - j : j;
                 floatx4 l;
+                if (!reverse) keep(i);
                 m.e = reverse ? before(m.e, i, l) : next(m.e, i);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) m.A[k] *= decay(g[i][k]);
+                for (int k = 0; k < 4; ++k) m.A[k] *= decay_of(i, k);
                 asm volatile("" : "+v"(m.A));  // (here, not where a branch needs it)
                 __builtin_amdgcn_sched_barrier(0);
             }
@@ -345,12 +361,19 @@ __global__ __launch_bounds__(64 * NW, BACK ? 2 : 4) void scan_kernel(Scan a) {
         };
         __shared__ Map s_map[BACK ? 2 : 1][NW][64], s_before[NW][64];
         __shared__ floatx4 s_entry[64];
+        // The last tokens' gates wait in LDS, where the maps are joined, whose registers they
+        // would take (the compiler spills to memory else, a ninth more to read and write:
+        // 394 us for the 372 above).
+        constexpr int PARKED = L > 8 ? 3 : 0;
+        __shared__ floatx4 s_gate[PARKED > 0 ? PARKED : 1][NW][64];
         s_map[0][wave][lane] = wave_map(false);
         forget(true);
         if (BACK) {
             s_map[1][wave][lane] = wave_map(true);
             forget(true);
         }
+#pragma unroll
+        for (int i = 0; i < PARKED; ++i) s_gate[i][wave][lane] = g[L - 1 - i];
         __syncthreads();
         floatx4 s = zero;  // what comes into the tile
         if (a.maps) {
@@ -385,6 +408,8 @@ __global__ __launch_bounds__(64 * NW, BACK ? 2 : 4) void scan_kernel(Scan a) {
             if (wave == 0 && in_group == GROUP - 1 && live)
                 publish(words(a.tiles + group + 1) + lane, Map{floatx4{1.f, 1.f, 1.f, 1.f}, own.of(s)});
         }
+#pragma unroll
+        for (int i = 0; i < PARKED; ++i) g[L - 1 - i] = s_gate[i][wave][lane];
         floatx4 r = s;  // the gradient, where s is the state
         if (BACK) s = *reinterpret_cast<const floatx4*>(a.states + tile * (TILE / kCheck) * a.C + ch);
 #pragma unroll 2
