@@ -229,22 +229,19 @@ __device__ __forceinline__ Map await(const uint64_t* one, int64_t step, int coun
     return m;
 }
 
-template <bool PASSING, typename T>
+// What is far larger than the caches passes them by: 4 to 7% of time. (x and dh are
+// read as usual: by the caches too it is the same or slower.)
+template <typename T>
 __device__ __forceinline__ T load(const T* p) {
-    if constexpr (PASSING) return __builtin_nontemporal_load(p);
-    else return *p;
+    return __builtin_nontemporal_load(p);
 }
-template <bool PASSING, typename T>
+template <typename T>
 __device__ __forceinline__ void store(T* p, T x) {
-    if constexpr (PASSING) __builtin_nontemporal_store(x, p);
-    else *p = x;
+    __builtin_nontemporal_store(x, p);
 }
 
 template <typename TI, int L, int NW, bool BACK, bool MIX>
-__global__ __launch_bounds__(64 * NW, BACK ? 2 : 4) void scan_kernel(Scan a) {
-    // What is far larger than the caches passes them by: 4 to 7% of time with bf16,
-    // nothing or less in the fp32 backward pass.
-    constexpr bool PASSING = !BACK || sizeof(TI) == 2;
+__global__ __launch_bounds__(64 * NW, 4) void scan_kernel(Scan a) {
     constexpr int TILE = L * NW, GROUP = NW * kEach;
     static_assert(TILE % kCheck == 0, "tiles hold whole spans of checkpoints; the workspace is sized by them");
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -271,7 +268,7 @@ __global__ __launch_bounds__(64 * NW, BACK ? 2 : 4) void scan_kernel(Scan a) {
 #pragma unroll
         for (int i = 0; i < L; ++i) {
             const int64_t at = (first + i < end ? first + i : end - 1) * a.C;
-            g[i] = load<PASSING>(reinterpret_cast<const floatx4*>(a.g + at + ch));
+            g[i] = load(reinterpret_cast<const floatx4*>(a.g + at + ch));
             x[i].v = *reinterpret_cast<const typename Four<TI>::raw*>(static_cast<const TI*>(a.x) + at + ch);
             if (BACK) dh[i].v = *reinterpret_cast<const typename Four<TI>::raw*>(static_cast<const TI*>(a.dh) + at + ch);
         }
@@ -332,12 +329,12 @@ __global__ __launch_bounds__(64 * NW, BACK ? 2 : 4) void scan_kernel(Scan a) {
         };
         // What is computed again for another pass over the tokens is not kept until then,
         // nor is it computed ahead of its token: the registers are the inputs'.
-        auto forget = [&](bool inputs) {
+        auto forget = [&](bool inputs, int from) {
 #pragma unroll
             for (int i = 0; i < L; ++i) {
                 asm volatile("" : "+v"(g[i]));
                 if (inputs) asm volatile("" : "+v"(x[i].v));
-                if (BACK) asm volatile("" : "+v"(dh[i].v));
+                if (BACK && i >= from) asm volatile("" : "+v"(dh[i].v));
             }
         };
         // What the wave's tokens do to a state, or to the gradient that comes from behind.
@@ -359,21 +356,27 @@ __global__ __launch_bounds__(64 * NW, BACK ? 2 : 4) void scan_kernel(Scan a) {
             for (int k = 0; k < 4; ++k) m.A[k] = constant ? -1.f : m.A[k] < 0x1p-149f ? 0x1p-149f : m.A[k];
             return m;
         };
-        __shared__ Map s_map[BACK ? 2 : 1][NW][64], s_before[NW][64];
+        __shared__ Map s_map[BACK ? 2 : 1][NW][64], s_before[(GROUP - 1 + kEach - 1) / kEach][64];  // (before the group's last tile)
         __shared__ floatx4 s_entry[64];
-        // The last tokens' gates wait in LDS, where the maps are joined, whose registers they
-        // would take (the compiler spills to memory else, a ninth more to read and write:
-        // 394 us for the 372 above).
-        constexpr int PARKED = L > 8 ? 3 : 0;
-        __shared__ floatx4 s_gate[PARKED > 0 ? PARKED : 1][NW][64];
+        // 128 registers are two workgroups to a compute unit.  What does not fit waits in LDS:
+        // where the maps are joined, gates of bf16's 16 tokens (spilled to memory, a ninth more
+        // to read and write, 394 us for the 372 above); up to the outputs, gradients of the
+        // first tokens in fp32 (with 142 registers and one workgroup 280 us for 238, with
+        // `mix` 307 for 250, 4 sequences of 8,192 tokens of 2,048 channels).
+        constexpr int PARKED = L > 8 ? 3 : 0, WAITING = BACK && sizeof(TI) == 4 ? 4 : 0;
+        __shared__ floatx4 s_wait[PARKED + WAITING > 0 ? PARKED + WAITING : 1][NW][64];
         s_map[0][wave][lane] = wave_map(false);
-        forget(true);
+        forget(true, 0);
         if (BACK) {
             s_map[1][wave][lane] = wave_map(true);
-            forget(true);
+            forget(true, 0);
         }
 #pragma unroll
-        for (int i = 0; i < PARKED; ++i) s_gate[i][wave][lane] = g[L - 1 - i];
+        for (int i = 0; i < PARKED; ++i) s_wait[i][wave][lane] = g[L - 1 - i];
+        if constexpr (WAITING > 0) {
+#pragma unroll
+            for (int i = 0; i < WAITING; ++i) s_wait[i][wave][lane] = dh[i].v;
+        }
         __syncthreads();
         floatx4 s = zero;  // what comes into the tile
         if (a.maps) {
@@ -409,7 +412,7 @@ __global__ __launch_bounds__(64 * NW, BACK ? 2 : 4) void scan_kernel(Scan a) {
                 publish(words(a.tiles + group + 1) + lane, Map{floatx4{1.f, 1.f, 1.f, 1.f}, own.of(s)});
         }
 #pragma unroll
-        for (int i = 0; i < PARKED; ++i) g[L - 1 - i] = s_gate[i][wave][lane];
+        for (int i = 0; i < PARKED; ++i) g[L - 1 - i] = s_wait[i][wave][lane];
         floatx4 r = s;  // the gradient, where s is the state
         if (BACK) s = *reinterpret_cast<const floatx4*>(a.states + tile * (TILE / kCheck) * a.C + ch);
 #pragma unroll 2
@@ -421,7 +424,7 @@ __global__ __launch_bounds__(64 * NW, BACK ? 2 : 4) void scan_kernel(Scan a) {
             for (int i = 0; i < L; ++i) {
                 s = next(s, i);
                 if (live && tokens.there(i))
-                    store<PASSING>(reinterpret_cast<typename Four<TI>::raw*>(static_cast<TI*>(a.h) + (first + i) * a.C + ch), Four<TI>::of(s));
+                    store(reinterpret_cast<typename Four<TI>::raw*>(static_cast<TI*>(a.h) + (first + i) * a.C + ch), Four<TI>::of(s));
                 if (a.final && tokens.ends_at(i)) put(a.final, i, s);
                 __builtin_amdgcn_sched_barrier(0);
             }
@@ -432,23 +435,28 @@ __global__ __launch_bounds__(64 * NW, BACK ? 2 : 4) void scan_kernel(Scan a) {
                 past[i] = s;
                 if (tokens.starts_at(i)) past[i] = vector(a.init, i);
                 s = next(s, i);
-                if (MIX) past[i] -= x[i].f();
+                if (MIX) {
+                    past[i] -= x[i].f();
+                    asm volatile("" : "+v"(past[i]));  // (here: x is not needed any more)
+                }
                 __builtin_amdgcn_sched_barrier(0);
             }
-            forget(false);  // (x is not needed any more)
+            forget(false, WAITING);
 #pragma unroll 2
             for (int w = NW - 1; w > wave; --w) r = s_map[1][w][lane].of(r);
 #pragma unroll
             for (int i = L - 1; i >= 0; --i) {
                 floatx4 l;
+                if constexpr (WAITING > 0)
+                    if (i < WAITING) dh[i].v = s_wait[i][wave][lane];
                 r = before(r, i, l);
                 const floatx4 dg = r * past[i];
                 if (MIX)
 #pragma unroll
                     for (int k = 0; k < 4; ++k) l[k] *= one_minus_decay(g[i][k], decay(g[i][k]));
                 if (live && tokens.there(i)) {
-                    store<PASSING>(reinterpret_cast<typename Four<TI>::raw*>(static_cast<TI*>(a.dx) + (first + i) * a.C + ch), Four<TI>::of(l));
-                    store<PASSING>(reinterpret_cast<floatx4*>(a.dg + (first + i) * a.C + ch), dg);
+                    store(reinterpret_cast<typename Four<TI>::raw*>(static_cast<TI*>(a.dx) + (first + i) * a.C + ch), Four<TI>::of(l));
+                    store(reinterpret_cast<floatx4*>(a.dg + (first + i) * a.C + ch), dg);
                 }
                 if (a.d_init && tokens.starts_at(i)) put(a.d_init, i, r);
                 __builtin_amdgcn_sched_barrier(0);
