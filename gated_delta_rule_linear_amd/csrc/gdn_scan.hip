@@ -26,15 +26,14 @@
 //
 // Measured, bf16 (of what has to be read and written): 65,536 tokens of 4,096
 // channels 372 us, 5.8 TB/s, where a copy reaches 5.1; four sequences of 8,192 191 us
-// forward and 339 backward (5.6 and 5.6), with `mix`, whose 1 - e^g is formed for every
-// pass over the registers, 209 and 379.  A forward pass for the maps, a fold and a
+// forward and 339 backward (5.6 and 5.6), with `mix` 209 (1 - e^g is formed for both
+// passes over the registers) and 347.  A forward pass for the maps, a fold and a
 // pass for the outputs took 1,196 us for the first.  8,300 tokens of 1,028 channels in 8
 // sequences, fp32, 39 us: 650 workgroups for 512 places, and a chain of ticket, inputs,
-// maps and outputs.  What counts:
-// nothing that the rare first and last tokens need may be waited for in the tokens'
-// loop (the stores before it would be waited for too: 422 against 492 us), maps
-// that are read in whole lines (482 against 550 us with 64 tokens to a tile), and
-// waiting on one word (461 against 493).
+// maps and outputs.  What counts: nothing that the rare first and last tokens need may
+// be waited for in the tokens' loop (the stores before it would be waited for too: 422
+// against 492 us), maps that are read in whole lines (482 against 550 us with 64 tokens
+// to a tile), and waiting on one word (461 against 493).
 #include <algorithm>
 
 #include "gdn_device.h"
@@ -295,24 +294,37 @@ __global__ __launch_bounds__(64 * NW, 4) void scan_kernel(Scan a) {
         auto put = [&](float* v, int i, floatx4 y) {
             if (live) *reinterpret_cast<floatx4*>(v + (int64_t)tokens.sequence(i) * a.C + ch) = y;
         };
-        // The first pass leaves decays and inputs where the registers had g and x (346 to 339
-        // us backward, with `mix` and fp32 164 to 158 forward), but where 1 - e^g is wanted
-        // later, and where x is of half their width.
-        constexpr bool KEPT = !MIX || (!BACK && sizeof(TI) == 4);
-        auto keep = [&](int i) {
-            if constexpr (KEPT) {
+        // The first pass leaves decays where the registers had g (346 to 339 us backward), and
+        // with `mix` b where they had fp32's x (164 to 158 forward) or, for bf16's gradients,
+        // 1 - e^g in LDS and in registers that are free (379 to 347).  Else there is no room for
+        // 1 - e^g, and all is formed again in every pass (bf16 forward with 8 tokens to a wave,
+        // where there is: 228 us for 209).
+        constexpr bool KEPT = !MIX || (BACK ? sizeof(TI) == 2 : sizeof(TI) == 4);
+        constexpr int IN_LDS = BACK && MIX && KEPT ? L / 2 : 0, OWN = IN_LDS > 0 ? L - IN_LDS : 0;
+        __shared__ floatx4 s_rest[IN_LDS > 0 ? IN_LDS : 1][NW][64];
+        floatx4 rest[OWN > 0 ? OWN : 1];
+        auto rest_of = [&](int i) { return i < IN_LDS ? s_rest[i][wave][lane] : rest[OWN > 0 ? i - IN_LDS : 0]; };
+        auto decay_of = [&](int i, int k) { return KEPT ? g[i][k] : decay(g[i][k]); };
+        auto next = [&](floatx4 s, int i, bool first) {  // the state after token i
+            if (tokens.starts_at(i)) s = vector(a.init, i);
+            floatx4 in = x[i].f();
+            if (KEPT && first) {
+                floatx4 y;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const float al = decay(g[i][k]);
-                    if constexpr (MIX) x[i].v[k] *= one_minus_decay(g[i][k], al);
+                    if (MIX) y[k] = one_minus_decay(g[i][k], al);
                     g[i][k] = al;
                 }
+                if (MIX) {
+                    in *= y;
+                    if constexpr (!BACK && sizeof(TI) == 4) x[i].v = in;
+                    if (i < IN_LDS) s_rest[i][wave][lane] = y;
+                    else if (OWN > 0) rest[OWN > 0 ? i - IN_LDS : 0] = y;
+                }
+            } else if (IN_LDS > 0) {
+                in *= rest_of(i);
             }
-        };
-        auto decay_of = [&](int i, int k) { return KEPT ? g[i][k] : decay(g[i][k]); };
-        auto next = [&](floatx4 s, int i) {  // the state after token i
-            if (tokens.starts_at(i)) s = vector(a.init, i);
-            const floatx4 in = x[i].f();
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const float al = decay_of(i, k);
@@ -333,6 +345,7 @@ __global__ __launch_bounds__(64 * NW, 4) void scan_kernel(Scan a) {
 #pragma unroll
             for (int i = 0; i < L; ++i) {
                 asm volatile("" : "+v"(g[i]));
+                if (OWN > 0 && i >= IN_LDS) asm volatile("" : "+v"(rest[OWN > 0 ? i - IN_LDS : 0]));
                 if (inputs) asm volatile("" : "+v"(x[i].v));
                 if (BACK && i >= from) asm volatile("" : "+v"(dh[i].v));
             }
@@ -344,8 +357,7 @@ __global__ __launch_bounds__(64 * NW, 4) void scan_kernel(Scan a) {
             for (int j = 0; j < L; ++j) {
                 const int i = reverse ? L - 1 - j : j;
                 floatx4 l;
-                if (!reverse) keep(i);
-                m.e = reverse ? before(m.e, i, l) : next(m.e, i);
+                m.e = reverse ? before(m.e, i, l) : next(m.e, i, true);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) m.A[k] *= decay_of(i, k);
                 asm volatile("" : "+v"(m.A));  // (here, not where a branch needs it)
@@ -422,7 +434,7 @@ __global__ __launch_bounds__(64 * NW, 4) void scan_kernel(Scan a) {
             if (!a.h) return;
 #pragma unroll
             for (int i = 0; i < L; ++i) {
-                s = next(s, i);
+                s = next(s, i, false);
                 if (live && tokens.there(i))
                     store(reinterpret_cast<typename Four<TI>::raw*>(static_cast<TI*>(a.h) + (first + i) * a.C + ch), Four<TI>::of(s));
                 if (a.final && tokens.ends_at(i)) put(a.final, i, s);
@@ -434,7 +446,7 @@ __global__ __launch_bounds__(64 * NW, 4) void scan_kernel(Scan a) {
             for (int i = 0; i < L; ++i) {
                 past[i] = s;
                 if (tokens.starts_at(i)) past[i] = vector(a.init, i);
-                s = next(s, i);
+                s = next(s, i, false);
                 if (MIX) {
                     past[i] -= x[i].f();
                     asm volatile("" : "+v"(past[i]));  // (here: x is not needed any more)
@@ -451,7 +463,8 @@ __global__ __launch_bounds__(64 * NW, 4) void scan_kernel(Scan a) {
                     if (i < WAITING) dh[i].v = s_wait[i][wave][lane];
                 r = before(r, i, l);
                 const floatx4 dg = r * past[i];
-                if (MIX)
+                if (MIX && KEPT) l *= rest_of(i);
+                if (MIX && !KEPT)
 #pragma unroll
                     for (int k = 0; k < 4; ++k) l[k] *= one_minus_decay(g[i][k], decay(g[i][k]));
                 if (live && tokens.there(i)) {
