@@ -38,9 +38,8 @@ typedef float floatx16 __attribute__((ext_vector_type(16)));
 
 constexpr int kTile = 64;      // tokens of a tile
 constexpr int kFewRows = 32;   // a request with up to so many rows is one of few rows
-constexpr int kMinPart = 512;  // tokens of a part of a request's cache, at least (measured for few rows)
-constexpr int kMinShared = 256;  // of a beginning that requests share (24 requests in four groups behind up to 4,224, in full
-                                 // precision, read apart: 24.6 us, with 128 24.5, with 512 28.5)
+constexpr int kMinPart = 512;  // tokens of a part of a request's cache, at least (measured for few rows; beginnings: 64
+                               // requests behind 4,096 35 us, in parts of 256 46, of 1,024 40)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kInf = __builtin_inff();
 
@@ -127,8 +126,7 @@ struct Request {
         few = rows <= a.few_rows;
         const int c = few ? 0 : 1;
         chunk = ((kv + a.splits[c] - 1) / a.splits[c] + kTile - 1) / kTile * kTile;
-        constexpr int least = REACH == kPrefix ? kMinShared : kMinPart;
-        if (chunk < least) chunk = least;
+        if (chunk < kMinPart) chunk = kMinPart;
         if (!few && !a.tiled && chunk < kv) chunk = (kv + kTile - 1) / kTile * kTile;  // there is no room for its parts
     }
     __device__ __forceinline__ bool alone() const { return REACH == kAll && kv <= chunk; }
@@ -558,6 +556,45 @@ struct TileShared {
     uintx4 v[2][2 * 2 * DT][64];  // [tile % 2][(half-tile * 2 + step) * DT + channels][lane]
     int32_t nan[2][kWaves];       // a wave's part of the tile's values had a NaN code
 };
+// Where all tiles of the beginnings are cut, those that have rows are dealt out first, and
+// all their parts: with workgroups that end at once among them, a compute unit here
+// and there received two and others none (64 requests behind 16,384 tokens: 55 us for
+// 51, 256 of them 144 for 127).  Returns the group of tile id % (tiles that have rows) and
+// the group's first, -1 where there is none; `id` becomes the tile, `part` its part.
+__device__ __forceinline__ int32_t group_of(const Attention& a, int br, int32_t& id, int32_t& part, int32_t& first) {
+    const int lane = threadIdx.x & 63;
+    auto upto = [&](int32_t n0) {  // tiles of the groups n0 .. n0 + lane
+        const int32_t n = n0 + lane;
+        int32_t x = 0;
+        if (n < a.num_seqs) {
+            const int4 info = a.info[n];
+            const Request<kPrefix> job(a, n, info);
+            x = job.kv > 0 && !job.few ? (job.rows + br - 1) / br : 0;
+        }
+        for (int d = 1; d < 64; d *= 2) {
+            const int32_t y = __shfl_up(x, d);
+            x += lane >= d ? y : 0;
+        }
+        return x;
+    };
+    int32_t all = 0;
+    for (int32_t n0 = 0; n0 < a.num_seqs; n0 += 64) all += __builtin_amdgcn_readlane(upto(n0), 63);
+    if (all <= 0 || id / all >= a.splits[1]) return -1;
+    part = id / all;
+    id -= part * all;
+    first = 0;
+    for (int32_t n0 = 0; n0 < a.num_seqs; n0 += 64) {
+        const int32_t x = upto(n0);
+        const uint64_t behind = __ballot(first + x > id);
+        if (behind) {
+            const int at = __ffsll((unsigned long long)behind) - 1;
+            if (at > 0) first += __builtin_amdgcn_readlane(x, at - 1);
+            return n0 + at;
+        }
+        first += __builtin_amdgcn_readlane(x, 63);
+    }
+    return -1;  // (of offsets that are none)
+}
 // `block`: a key/value head's tile of rows and part of the cache.
 template <typename TI, int DK, int DV, int REACH>
 __device__ __forceinline__ void attention_tile(const Attention& a, TileShared<DK, DV>& sh, int32_t block) {
@@ -572,13 +609,15 @@ __device__ __forceinline__ void attention_tile(const Attention& a, TileShared<DK
     // turn, so with eight heads the tiles of a head share one XCD's cache.  The
     // last rows, which see most, come first, and the parts of the first last.
     const int h = block % a.Hkv;
-    const int32_t id = block / a.Hkv, over = id - a.tiles, part = over < 0 ? 0 : 1 + over / a.tail;
-    const int32_t rtile = over < 0 ? a.tiles - 1 - id : a.tail - 1 - over % a.tail;
-    const int32_t n = request_of<REACH>(a, rtile, BR);
+    const int32_t id = block / a.Hkv, over = id - a.tiles;
+    int32_t part = over < 0 ? 0 : 1 + over / a.tail, rtile = over < 0 ? a.tiles - 1 - id : a.tail - 1 - over % a.tail, n = 0, first = 0;
+    const bool packed = REACH == kPrefix && a.num_seqs > 1 && a.tail == a.tiles;
+    if (packed) n = group_of(a, BR, rtile = id, part, first);
+    else n = request_of<REACH>(a, rtile, BR);
     if (n < 0) return;
     Request<REACH> job(a, n);
     if (rtile >= a.tail) job.chunk = job.kv;
-    const int64_t row0_ = (rtile - first_tile<REACH>(a, n, BR)) * BR;
+    const int64_t row0_ = (rtile - (packed ? first : first_tile<REACH>(a, n, BR))) * BR;
     if (job.few || row0_ < 0 || row0_ >= job.rows) return;
     const int32_t row0 = (int32_t)row0_, last_row = (row0 + BR < job.rows ? row0 + BR : job.rows) - 1;
     const int64_t from = part * job.chunk;
@@ -1061,10 +1100,10 @@ __global__ __launch_bounds__(256) void attention_join_kernel(Attention a, int32_
 // Three launches: groups, parts, join.  The lengths and groups are on the device, so a
 // small kernel makes one record of each for the other two, which would each find it by a
 // search.  What a beginning takes is products, 4 operations a code and row, at
-// 0.72 to 0.82 PFLOP/s where it is long; what the own tokens take is reading them.
+// 0.7 to 0.8 PFLOP/s where it is long; what the own tokens take is reading them.
 // 64 requests of 32 heads, 8 for keys, of 128 channels, behind 16,384 tokens and 1 to
-// 1,024 of their own, bf16: 52 us, of which 43 go to the parts, 7 to the join (it
-// reads the 17.6 MB of partial rows) and 3 to 5 to the groups; the cache read once
+// 1,024 of their own, bf16: 51 us, of which 38 go to the parts, 7 to the join (it
+// reads the 17.7 MB of partial rows) and 5 to the groups; the cache read once
 // would be 104 MB and the products 17.7 GFLOP, 15 us each.  About 15 us do not
 // depend on the lengths: launches, loads that wait for loads (record, page, codes) and
 // the partial rows.  The two kinds of parts as launches after each other: 71 where one
@@ -1202,7 +1241,7 @@ __global__ __launch_bounds__(256) void prefix_join_kernel(Attention p, Attention
 constexpr int64_t kAtOnce = 512;  // workgroups that the device holds: two on each compute unit
 // Of them for beginnings that requests share, whose parts run beside those of the own
 // tokens, and each of which is a row of the workspace for every row of o (64 requests
-// behind 16,384 tokens: 59 us; 128 and 384 61, 512 67).
+// behind 16,384 tokens: 52 us; with 128 and 384 59, with 512 65).
 constexpr int64_t kSharedAtOnce = 256;
 constexpr int64_t kTailCache = 2048;  // tokens in front of a call's last tiles, from which on they are cut
 
@@ -1219,7 +1258,7 @@ struct Plan {
 // parts of at least kMinPart tokens, so that there are enough workgroups when
 // every request is as long as the bound, and so that the lengths, which may
 // differ much, do not leave the device waiting for a few long parts.
-Plan plan(const CacheAttentionLaunch& p, int64_t at_once = kAtOnce, int64_t min_part = kMinPart) {
+Plan plan(const CacheAttentionLaunch& p, int64_t at_once = kAtOnce) {
     Plan r = {};
     auto up = [](int64_t x, int64_t y) { return (x + y - 1) / y; };
     const int64_t room = (int64_t)p.max_blocks * p.page_size;
@@ -1243,7 +1282,7 @@ Plan plan(const CacheAttentionLaunch& p, int64_t at_once = kAtOnce, int64_t min_
         // workspace's sake, not more parts than 16384 in all.
         const int64_t units = (int64_t)p.num_seqs * p.H_kv * up(r.few_rows, 16);
         int64_t splits = std::max(units >= at_once / 2 ? 1 : up(at_once, units), up(kv, 16384));
-        splits = std::min(splits, std::min<int64_t>(up(kv, min_part), std::max<int64_t>(16384 / units, 1)));
+        splits = std::min(splits, std::min<int64_t>(up(kv, kMinPart), std::max<int64_t>(16384 / units, 1)));
         r.splits[0] = (int32_t)std::max<int64_t>(std::min<int64_t>(splits, 256), 1);
         r.part_rows[0] = (int64_t)p.num_seqs * p.H_kv * r.few_rows;
     }
@@ -1269,7 +1308,7 @@ Plan plan(const CacheAttentionLaunch& p, int64_t at_once = kAtOnce, int64_t min_
         if (units < at_once) r.tail = r.tiles;
         else if (rest <= at_once * 3 / 8 && kv - most / G >= kTailCache) r.tail = (int32_t)up(rest, p.H_kv);
         const int64_t share = std::max<int64_t>((int64_t)r.tail * p.H_kv, 1);
-        const int64_t cut = std::min(units < at_once ? up(at_once, units) : (at_once + share / 2) / share, up(kv, min_part));
+        const int64_t cut = std::min(units < at_once ? up(at_once, units) : (at_once + share / 2) / share, up(kv, kMinPart));
         if (r.tail > 0) r.splits[1] = (int32_t)std::max<int64_t>(cut, 1);
         if (r.splits[1] == 1) r.tail = 0;
         // Rows of the first `tail` tiles are among the first (tail + 1) * BR: see first_tile.
@@ -1341,7 +1380,11 @@ CacheAttentionLaunch own_tokens(const CachePrefixLaunch& p) {
 }
 PrefixPlan plan(const CachePrefixLaunch& c) {
     PrefixPlan r = {};
-    r.p = plan(beginnings(c), kSharedAtOnce, kMinShared);
+    r.p = plan(beginnings(c), kSharedAtOnce);
+    if (c.num_groups == 1 && r.p.many) {  // whose tiles are known: see group_of
+        r.p.tiles = (int32_t)((c.all.T_total * (c.all.H / c.all.H_kv) + 32 * kWaves - 1) / (32 * kWaves));
+        r.p.tail = std::min(r.p.tail, r.p.tiles);
+    }
     r.o = plan(own_tokens(c));
     r.parts[0] = std::max(r.p.splits[0], r.p.splits[1]);
     r.parts[1] = std::max(r.o.splits[0], r.o.splits[1]);
@@ -1358,15 +1401,17 @@ PrefixPlan plan(const CachePrefixLaunch& c) {
 }
 // Whether the beginnings are worth reading apart: else the call is
 // gdn_cache_attention's, whose requests read the same pages out of the caches, at
-// some 8 TB/s.  Reading them apart costs 7 us of launches and dependent loads where a group
+// some 8 TB/s.  Reading them apart costs 6 us of launches and dependent loads where a group
 // is of few rows and 15 else, and the beginning's products with all rows of the
-// group, at some 0.55 PFLOP/s (0.18 in full precision).  Both sides, in us, shared and
+// group, at some 0.7 PFLOP/s (0.18 in full precision).  Both sides, in us, shared and
 // not, bf16, 32 heads, 8 for keys, of 128 channels, 64 tokens of their own: 4
-// requests behind 16,384 tokens 18.6 and 29.1, 64 behind them 54 and 213, behind
-// 4,096 37 and 51, behind 1,024 22.4 and 17.5; 4 new tokens of 64 behind 16,384 137
-// and 230, of 16 behind 4,096 37 and 27.  Requests of many rows keep the matrix
-// cores busy either way: 32 new tokens (128 rows) of 64 behind 16,384 568 and 855, of 16 242 and 243,
-// of 64 behind 1,024 100 and 89; 256 new tokens of 8 behind 16,384 541 and 526, of 2 241 and 162.
+// requests behind 16,384 tokens 19 and 29, 64 behind them 46 and 217, behind
+// 4,096 29 and 49, behind 1,024 26 and 18; 4 new tokens of 64 behind 16,384 105
+// and 232, of 8 35 and 51, of 16 behind 4,096 28 and 28.  A request of more than
+// kFewRows rows and up to one tile of them fills that tile less than the group fills its
+// own, which pays behind long beginnings: 32 new tokens (128 rows) of 64 behind 16,384
+// 574 and 875, of 4 64 and 91, of 8 behind 4,096 44 and 63, but of 64 behind 1,024 102
+// and 87.  With more rows it does not: 256 new tokens of 8 behind 16,384 540 and 528.
 bool shares(const CachePrefixLaunch& p) {
     const CacheAttentionLaunch& a = p.all;
     if (p.num_groups <= 0 || p.num_groups >= a.num_seqs) return false;  // no request shares with another
@@ -1376,9 +1421,9 @@ bool shares(const CachePrefixLaunch& p) {
     const int64_t G = a.H / a.H_kv, rows = bound(a.max_new, (a.T_total + a.num_seqs - 1) / a.num_seqs) * G;
     const double prefix = (double)bound(p.max_prefix, bound(a.max_kv, (int64_t)a.max_blocks * a.page_size));
     const double saved = (double)(a.num_seqs - p.num_groups) * prefix * a.H_kv * (a.dk + a.dv);
-    if (rows > kFewRows) return rows <= 32 * kWaves && saved > 256e6;
+    if (rows > kFewRows) return rows <= 32 * kWaves && prefix >= 2048. && saved > 20e6;
     const double products = 2. * (double)a.T_total * a.H * prefix * (a.dk + a.dv);
-    return saved / 8e6 > (a.T_total * G <= (int64_t)p.num_groups * kFewRows ? 7. : 15.) + products / (a.bf16 ? 5.5e8 : 1.8e8);
+    return saved / 8e6 > (a.T_total * G <= (int64_t)p.num_groups * kFewRows ? 6. : 15.) + products / (a.bf16 ? 7e8 : 1.8e8);
 }
 
 }  // namespace
