@@ -20,7 +20,7 @@
 // for what comes into the group, which the last tile of the group before hands on.
 // So the order of the sums is always the same, and bits do not depend on timing.  A
 // group in which a sequence begins waits for nothing before it.  Tiles are dealt
-// out by a counter in the order of the pass, and a workgroup publishes its map
+// out by counters in the order of the pass, and a workgroup publishes its map
 // before it waits: what is waited for has begun, and comes.  A map's A and e are one
 // word, written and read as such, so nothing else orders them.
 //
@@ -29,7 +29,7 @@
 // forward and 339 backward (5.6 and 5.6), with `mix` 209 (1 - e^g is formed for both
 // passes over the registers) and 347.  A forward pass for the maps, a fold and a
 // pass for the outputs took 1,196 us for the first.  8,300 tokens of 1,028 channels in 8
-// sequences, fp32, 39 us: 650 workgroups for 512 places, and a chain of ticket, inputs,
+// sequences, fp32, 37 us: 650 workgroups for 512 places, and a chain of ticket, inputs,
 // maps and outputs.  What counts: nothing that the rare first and last tokens need may
 // be waited for in the tokens' loop (the stores before it would be waited for too: 422
 // against 492 us), maps that are read in whole lines (482 against 550 us with 64 tokens
@@ -62,11 +62,19 @@ struct Scan {
     float* states;      // [T / kCheck][C] state before every kCheck tokens, or NULL
     uint64_t* maps;     // [tiles][blocks][4][64] maps of the tiles, and [groups][blocks][4][64] what comes into a group of
                         // them: a lane's four channels are 64 words apart (NULL: one tile)
-    uint32_t* tickets;  // workgroups that have begun
+    uint64_t* counters;  // of workgroups that have begun, a line each
     int64_t tiles;
+    bool apart;  // the blocks of channels have counters of their own
 };
 
 constexpr int kCheck = 64;  // tokens
+// Workgroups up to which blocks of channels have counters of their own.  Those that begin
+// together, 512 of them, wait for each other at one counter (2,048 tokens of 4,096
+// channels, fp32: 30.0 us, apart 24.1; 8,192, bf16: 67 and 60).  Where most begin one by
+// one, one counter keeps the blocks of a tile together, which are neighbours in memory
+// (32,768, bf16: 191 us, apart 199).
+constexpr int64_t kApart = 2048;
+constexpr int kLine = 16;   // words
 constexpr int kEach = 1;    // maps that a wave waits for (2: 435 us where 1 takes 422; 4: 567)
 constexpr uint64_t kNotReady = ~0ull;       // of a tile's map
 constexpr int32_t kMostPolls = 1 << 17;     // 0.1 s: no wait is without end, whatever happened to a workspace
@@ -246,16 +254,20 @@ __global__ __launch_bounds__(64 * NW, 4) void scan_kernel(Scan a) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int32_t blocks = (a.C + kChannels - 1) / kChannels, held = a.cu[a.num_seqs];
     __shared__ uint32_t s_ticket;
-    // A workgroup waits for tiles before its own only (behind it, in the backward
-    // pass): their workgroups have begun, since tiles are dealt out in that order.
-    uint32_t ticket = blockIdx.x;
+    // A workgroup waits for tiles of its channels before its own only (behind it, in the
+    // backward pass): their workgroups have begun, since tiles are dealt out in that order,
+    // by one counter or by one for each block of channels.
+    uint32_t place = 0, block = blockIdx.x;
     if (a.maps) {
-        if (threadIdx.x == 0) s_ticket = atomicAdd(a.tickets, 1u);
+        const uint32_t counter = a.apart ? blockIdx.x % (uint32_t)blocks : 0;
+        if (threadIdx.x == 0) s_ticket = atomicAdd(reinterpret_cast<uint32_t*>(a.counters + counter * kLine), 1u) + 1;
         __syncthreads();
-        ticket = __builtin_amdgcn_readfirstlane(s_ticket);
+        const uint32_t ticket = __builtin_amdgcn_readfirstlane(s_ticket);
+        place = a.apart ? ticket : ticket / (uint32_t)blocks;
+        block = a.apart ? counter : ticket - place * (uint32_t)blocks;
     }
-    const int64_t place = ticket / (uint32_t)blocks, tile = BACK ? a.tiles - 1 - place : place;
-    const int32_t block = (int32_t)(ticket - (uint32_t)place * (uint32_t)blocks), c = block * kChannels + 4 * lane;
+    const int64_t tile = BACK ? a.tiles - 1 - place : place;
+    const int32_t c = (int32_t)block * kChannels + 4 * lane;
     const uint32_t ch = c < a.C ? c : 0;
     const bool live = c < a.C;
     const int64_t end = __builtin_amdgcn_readfirstlane(held < a.T ? held : (int32_t)a.T), first = tile * TILE + wave * L;
@@ -485,12 +497,11 @@ __global__ __launch_bounds__(64 * NW, 4) void scan_kernel(Scan a) {
             *reinterpret_cast<floatx4*>(to + (int64_t)m * a.C + c) = from ? *reinterpret_cast<const floatx4*>(from + (int64_t)m * a.C + c) : zero;
 }
 
-// No map is there yet, and no workgroup has begun.
-__global__ __launch_bounds__(256) void begin_kernel(uint64_t* maps, uint32_t* tickets, int64_t words) {
-    if (blockIdx.x == 0 && threadIdx.x == 0) *tickets = 0;
+// No map is there yet, and no workgroup has begun (a counter's first value is all ones too).
+__global__ __launch_bounds__(256) void begin_kernel(uint64_t* counters_and_maps, int64_t words) {
     for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 2; i < words; i += (int64_t)gridDim.x * 512) {
         typedef uint64_t two __attribute__((ext_vector_type(2)));
-        *reinterpret_cast<two*>(maps + i) = two{kNotReady, kNotReady};  // (an even number of words)
+        *reinterpret_cast<two*>(counters_and_maps + i) = two{kNotReady, kNotReady};  // (an even number of words)
     }
 }
 
@@ -504,15 +515,16 @@ int64_t up(int64_t x, int64_t y) { return (x + y - 1) / y; }
 size_t rounded(size_t bytes) { return (bytes + 255) & ~(size_t)255; }
 // Tiles of kCheck tokens at least, and their groups.
 int64_t map_words(int64_t tiles, int32_t C) { return (tiles + tiles / (kWaves * kEach) + 1) * up(C, kChannels) * kChannels; }
-size_t maps_bytes(int64_t T, int32_t C) { return rounded((size_t)map_words(up(T, kCheck), C) * sizeof(uint64_t)) + 256; }
+int64_t counter_words(int32_t C) { return std::min(up(C, kChannels), kApart / 2) * kLine; }  // (of two tiles or more)
+size_t maps_bytes(int64_t T, int32_t C) { return rounded((size_t)(counter_words(C) + map_words(up(T, kCheck), C)) * sizeof(uint64_t)); }
 
 Scan arguments(const ScanLaunch& p) {
     Scan a = {};
     a.x = p.x; a.g = p.g; a.cu = p.cu_seqlens; a.num_seqs = p.num_seqs; a.T = p.T; a.C = p.C;
     a.init = p.initial_state; a.final = p.final_state; a.h = p.h; a.dh = p.d_h; a.d_final = p.d_final_state;
     a.dx = p.dx; a.dg = p.dg; a.d_init = p.d_initial_state;
-    a.tickets = static_cast<uint32_t*>(p.workspace);
-    a.maps = reinterpret_cast<uint64_t*>(static_cast<char*>(p.workspace) + 256);
+    a.counters = static_cast<uint64_t*>(p.workspace);
+    a.maps = a.counters + counter_words(p.C);
     return a;
 }
 template <typename TI, bool BACK, bool MIX>
@@ -522,12 +534,14 @@ hipError_t run(Scan a, hipStream_t s) {
     if (a.tiles == 1) {
         a.maps = nullptr;
     } else {
-        const int64_t words = map_words(a.tiles, a.C);
-        hipLaunchKernelGGL(begin_kernel, dim3((unsigned)std::min<int64_t>(up(words, 512), 4096)), dim3(256), 0, s, a.maps, a.tickets, words);
+        const int64_t words = counter_words(a.C) + map_words(a.tiles, a.C);
+        hipLaunchKernelGGL(begin_kernel, dim3((unsigned)std::min<int64_t>(up(words, 512), 4096)), dim3(256), 0, s, a.counters, words);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    const dim3 grid((unsigned)(a.tiles * up(a.C, kChannels)));
+    const int64_t all = a.tiles * up(a.C, kChannels);
+    a.apart = all <= kApart;
+    const dim3 grid((unsigned)all);
     hipLaunchKernelGGL((scan_kernel<TI, L, kWaves, BACK, MIX>), grid, dim3(64 * kWaves), 0, s, a);
     return hipGetLastError();
 }
