@@ -516,6 +516,16 @@ def test_prefix_of_many_and_few_rows(share, dtype, groups):
     prefix_check(*shared_server(groups, 64, 1, 64, 64, seed=4), 4, dtype)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_prefix_of_more_groups_than_lanes(always, dtype):
+    # groups of many rows, of few, without a beginning, and without a request that takes part, in turn
+    groups = [[(1100, [(i % 5, 1)] * 9), (700, [(3, 1)] * 2), (0, [(5, 1)] * 10), (640, [(1, 1)] * 11)][i % 4] for i in range(131)]
+    server, lens, offsets, shared = shared_server(groups, 64, 1, 64, 64, seed=18)
+    for g in range(3, 131, 8):
+        shared[g] = 1 << 20
+    prefix_check(server, lens, offsets, shared, 4, dtype)
+
+
 def test_prefix_requests_that_take_no_part(share):
     # of the second group one request holds less than the beginning and one has been refused (it holds fewer tokens than it
     # adds); requests behind the last group are in none
