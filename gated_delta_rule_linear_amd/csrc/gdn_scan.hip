@@ -79,6 +79,15 @@ constexpr int kEach = 1;    // maps that a wave waits for (2: 435 us where 1 tak
 constexpr uint64_t kNotReady = ~0ull;       // of a tile's map
 constexpr int32_t kMostPolls = 1 << 17;     // 0.1 s: no wait is without end, whatever happened to a workspace
 
+// The decay of two runs: the product, and where it falls below fp32's numbers the least
+// of them, so that an infinite state stays infinite behind runs as it does from token to
+// token.  It is 0 where one of the two is, and 0 Inf is NaN from there on.
+// (As integers, which numbers from 0 up are ordered as; NaN stays NaN.)
+constexpr float kLeast = 0x1p-149f;
+__device__ __forceinline__ float joined_decay(float a, float b) {
+    return __uint_as_float(max(__float_as_uint(a * b), min(min(__float_as_uint(a), __float_as_uint(b)), 1u)));
+}
+
 // A run's map per channel.  A constant map has A < 0: e alone counts, whatever
 // the state before (Inf and NaN among it).
 struct Map {
@@ -90,15 +99,20 @@ struct Map {
         for (int k = 0; k < 4; ++k) r[k] = A[k] < 0.f ? e[k] : __builtin_fmaf(A[k], s[k], e[k]);
         return r;
     }
-    // This map after `first`.
+    // This map after `first`.  (ROUGH: a decay of 0 may also be a product of others.)
+    template <bool ROUGH = false>
     __device__ __forceinline__ Map after(const Map& first) const {
         Map r;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            r.A[k] = A[k] < 0.f || first.A[k] < 0.f ? -1.f : A[k] * first.A[k];
+            r.A[k] = A[k] < 0.f || first.A[k] < 0.f ? -1.f : ROUGH ? A[k] * first.A[k] : joined_decay(A[k], first.A[k]);
             r.e[k] = A[k] < 0.f ? e[k] : __builtin_fmaf(A[k], first.e[k], e[k]);
         }
         return r;
+    }
+    // Whether a decay of some lane is 0.
+    __device__ __forceinline__ bool some_zero() const {
+        return __builtin_expect(__ballot(fminf(fminf(A[0], A[1]), fminf(A[2], A[3])) == 0.f) != 0, 0);
     }
 };
 
@@ -231,7 +245,7 @@ __device__ __forceinline__ Map await(const uint64_t* one, int64_t step, int coun
             next.A[k] = __uint_as_float((uint32_t)w[j][k]);
             next.e[k] = __uint_as_float((uint32_t)(w[j][k] >> 32));  // (NaN where nothing came, as A)
         }
-        m = next.after(m);
+        m = j == 0 ? next : next.after(m);
     }
     return m;
 }
@@ -375,19 +389,33 @@ __global__ __launch_bounds__(64 * NW, 4) void scan_kernel(Scan a) {
                 asm volatile("" : "+v"(m.A));  // (here, not where a branch needs it)
                 __builtin_amdgcn_sched_barrier(0);
             }
+            // A product of 0 is put right by itself: it is rare, and joined_decay for each
+            // token costs the bf16 kernels registers that they lack.
+            if (m.some_zero()) {
+                bool some[4] = {};  // of the decays is 0
+#pragma unroll
+                for (int i = 0; i < L; ++i) {
+                    asm volatile("" : "+v"(g[i]));
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) some[k] |= decay_of(i, k) == 0.f;
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) m.A[k] = m.A[k] == 0.f && !some[k] ? kLeast : m.A[k];
+            }
             const bool constant = (reverse ? tokens.ends : tokens.starts) != 0;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) m.A[k] = constant ? -1.f : m.A[k] < 0x1p-149f ? 0x1p-149f : m.A[k];
+            for (int k = 0; k < 4; ++k) m.A[k] = constant ? -1.f : m.A[k];
             return m;
         };
         __shared__ Map s_map[BACK ? 2 : 1][NW][64], s_before[(GROUP - 1 + kEach - 1) / kEach][64];  // (before the group's last tile)
         __shared__ floatx4 s_entry[64];
         // 128 registers are two workgroups to a compute unit.  What does not fit waits in LDS:
-        // where the maps are joined, gates of bf16's 16 tokens (spilled to memory, a ninth more
+        // where the maps are joined, four gates of bf16's 16 tokens (spilled to memory, a ninth more
         // to read and write, 394 us for the 372 above); up to the outputs, gradients of the
         // first tokens in fp32 (with 142 registers and one workgroup 280 us for 238, with
         // `mix` 307 for 250, 4 sequences of 8,192 tokens of 2,048 channels).
-        constexpr int PARKED = L > 8 ? 3 : 0, WAITING = BACK && sizeof(TI) == 4 ? 4 : 0;
+        constexpr int PARKED = L > 8 ? 4 : 0, WAITING = BACK && sizeof(TI) == 4 ? 4 : 0;
         __shared__ floatx4 s_wait[PARKED + WAITING > 0 ? PARKED + WAITING : 1][NW][64];
         s_map[0][wave][lane] = wave_map(false);
         forget(true, 0);
@@ -411,7 +439,19 @@ __global__ __launch_bounds__(64 * NW, 4) void scan_kernel(Scan a) {
             Map own = Map::identity();
             if (wave == 0) {
 #pragma unroll 2
-                for (int w = 0; w < NW; ++w) own = s_map[BACK][BACK ? NW - 1 - w : w][lane].after(own);
+                for (int w = 0; w < NW; ++w) own = s_map[BACK][BACK ? NW - 1 - w : w][lane].template after<true>(own);
+                // (Put right by itself too: with joined_decay in each join the chunks of 37 us above
+                // take 1 us more, and 65,536 tokens 3.)
+                if (own.some_zero()) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        float A = 1.f;  // (no map is constant where own's A is 0)
+#pragma unroll 1
+                        for (int w = 0; w < NW; ++w) A = joined_decay(A, s_map[BACK][w][lane].A[k]);
+                        own.A[k] = own.A[k] == 0.f ? A : own.A[k];
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+                }
                 if (live) publish(words(tile) + lane, own);
             }
             // A wave waits for kEach of the group's maps before the tile's: the order of

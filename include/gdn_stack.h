@@ -116,7 +116,10 @@ size_t gdn_qk_norm_backward_workspace_bytes(int64_t T_total, int32_t H, int32_t 
  *               NULL: states along the sequences, for gdn_scan_backward
  *   workspace   gdn_scan_workspace_bytes(T_total, C) bytes, 16-byte aligned
  *
- * States are fp32; h is rounded once.  Alignment: 16 bytes, cu_seqlens 4.  The
+ * States are fp32; h is rounded once.  e^g is fp32's, and 0 below its normal numbers
+ * (g under -87.3).  An infinite state stays infinite however small the product of
+ * decays above 0, and a decay of 0 makes it NaN; a finite one it ends, to the last
+ * bit.  gdn_scan_backward's l is as the state is.  Alignment: 16 bytes, cu_seqlens 4.  The
  * result does not depend on timing.  Below 2^23 tiles of 64 tokens and 256 channels.
  * GDN_VALIDATE=1 returns GDN_ERR_DOMAIN for offsets that decrease, do not begin
  * at 0 or end behind T_total, and for g of a sequence above 0 or NaN. */

@@ -317,6 +317,87 @@ def test_scan_nan_and_inf_stay_in_their_sequence():
         assert not math.isfinite(float(d0[1, 2])) and int((~torch.isfinite(d0)).sum()) == 1
 
 
+def same_places(name, got, want, sure=None):
+    """Infinities, with their signs, and NaN stand where they stand in `want` (looked at where `sure` says so)."""
+    got, want = (f64(t) if sure is None else f64(t)[sure] for t in (got, want))
+    assert torch.equal(torch.isnan(got), torch.isnan(want)), f"{name}: NaN elsewhere"
+    inf = torch.isinf(want)
+    assert torch.equal(torch.isinf(got), inf), f"{name}: infinite elsewhere"
+    assert torch.equal(got[inf], want[inf]), f"{name}: infinite with the other sign"
+
+
+def scan_places(a, dh, df, dtype, reference):
+    """Both calls against the 64-bit form, finite values and others; `reference`: the arguments of the 64-bit form."""
+    kept = gdn.gdn_scan_checkpoints(a["x"])
+    h, final = gdn.gdn_scan(**a, checkpoints=kept)
+    want = ref.scan(*reference)
+    back = ref.scan_backward(*reference, f64(dh), f64(df))
+    # dg is an infinite gradient times h_{t-1} (- x_t), or an infinite state times a gradient.  A finite factor below its error
+    # may be 0 or of the other sign: fp32's h_{t-1} is off by 2^-24 of its magnitude at least, so that with `mix` and behind a
+    # decay of e^-20 it is x_{t-1} itself, whose difference to an equal x_t (of bf16, one of some 256) is 0, and 0 Inf is NaN,
+    # where 64 bits keep 2e-9 Inf.  (That such a dg is not finite is asked all the same, by close.)
+    x = f64(a["x"])
+    past = want["before"] - x if a["mix"] else want["before"]
+    past_bound = ref.E32 * (want["off"] + (want["big"] + x.abs() if a["mix"] else 0))
+    beyond = lambda value, bound: ~torch.isfinite(value) | (value.abs() > bound)
+    sure = beyond(past, past_bound) & beyond(back["dx"], back["dx_bound"])
+    for c in (kept, None):
+        dx, dg, d_init = gdn.gdn_scan_backward(**a, d_h=dh, d_final_state=df, checkpoints=c)
+        for name, got, w in (("h", h, want["h"]), ("final", final, want["final"]), ("dx", dx, back["dx"]), ("d_init", d_init, back["d_init"])):
+            same_places(name, got, w)
+        same_places("dg", dg, back["dg"], sure)
+        close("h", h, want["h"], want["bound"], dtype)
+        close("final", final, want["final"], want["final_bound"], F32)
+        close("dx", dx, back["dx"], back["dx_bound"], dtype)
+        close("dg", dg, back["dg"], back["dg_bound"], F32)
+        close("d_init", d_init, back["d_init"], back["d_init_bound"], F32)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("mix", [False, True])
+def test_scan_infinities_behind_fast_decays(dtype, mix):
+    # decays whose product over a wave's tokens, over a tile's or over none leaves fp32's range: an infinite state, or an
+    # infinite gradient from behind, stays infinite through all tiles and groups of its sequence
+    lens, C = [1500, 0, 300, 450], 260
+    a, (dh, df) = scan_case(lens, C, mix, True, dtype, seed=31)
+    gen = torch.Generator().manual_seed(32)
+    speed = torch.tensor([0.01, 0.3, 0.9, 2.0, 5.0, 20.0, 80.0])[torch.arange(C) % 7]
+    a["g"] = (-speed * (0.9 + 0.1 * torch.rand((sum(lens), C), generator=gen))).cuda()
+    kind = (torch.arange(C) // 7 % 7).cuda()
+    for n, first in ((0, 0), (3, 1800)):
+        a["initial_state"][n, kind == 0] = math.inf
+        a["x"][first + 40, kind == 1] = -math.inf
+        a["initial_state"][n, kind == 2] = -math.inf
+        a["x"][first + 200, kind == 2] = math.inf
+        df[n, kind == 3] = math.inf
+        dh[first + lens[n] - 33, kind == 4] = -math.inf
+        a["initial_state"][n, kind == 5] = math.nan
+    scan_places(a, dh, df, dtype, scan_reference(a))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("mix", [False, True])
+@pytest.mark.parametrize("gate", [-math.inf, -1e4])
+def test_scan_decays_of_zero(dtype, mix, gate):
+    # two tokens with a decay of 0: what is finite ends there, to the last bit, in whatever tile it is looked at, and
+    # what is infinite becomes NaN
+    T, C = 1300, 260
+    a, (dh, df) = scan_case([T], C, mix, True, dtype, seed=33)
+    a["g"][100] = a["g"][1111] = gate
+    a["initial_state"][0, 0:64] = math.inf
+    a["initial_state"][0, 64:128] = 1e30
+    a["x"][:, 64:128] = 0
+    df[0, 128:192] = -math.inf
+    df[0, 192:256] = 1e30
+    dh[:, 192:256] = 0
+    x, g, cu, mix, init = scan_reference(a)
+    scan_places(a, dh, df, dtype, (x, g.clamp(min=-1e4), cu, mix, init))
+    h, _ = gdn.gdn_scan(**a)
+    dx, _, d_init = gdn.gdn_scan_backward(**a, d_h=dh, d_final_state=df)
+    assert bool(torch.isinf(h[:100, :64]).all()) and bool(torch.isnan(h[100:, :64]).all()) and bool((h[100:, 64:128] == 0).all())
+    assert bool(torch.isnan(dx[:1111, 128:192]).all()) and bool((dx[:1111, 192:256] == 0).all()) and bool((d_init[:, 192:256] == 0).all())
+
+
 def test_scan_past_32_bits():
     # more than 2^32 elements: a part of the channels is as by itself
     T, C = 1100003, 4096
