@@ -77,7 +77,12 @@ constexpr int64_t kApart = 2048;
 constexpr int kLine = 16;   // words
 constexpr int kEach = 1;    // maps that a wave waits for (2: 435 us where 1 takes 422; 4: 567)
 constexpr uint64_t kNotReady = ~0ull;       // of a tile's map
-constexpr int32_t kMostPolls = 1 << 17;     // 0.1 s: no wait is without end, whatever happened to a workspace
+// Some 0.8 s: no wait is without end, whatever happened to a workspace.  What is waited for
+// comes within microseconds, since its workgroup has begun; the rest is for processes that
+// share the device, whose time slices of some ten milliseconds may lie between the two.
+// A call whose every entry is lost ends within a minute (16 turns of 512 workgroups, two
+// waits each, for 8,192).
+constexpr int32_t kMostPolls = 1 << 20;
 
 // The decay of two runs: the product, and where it falls below fp32's numbers the least
 // of them, so that an infinite state stays infinite behind runs as it does from token to

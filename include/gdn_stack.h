@@ -114,13 +114,18 @@ size_t gdn_qk_norm_backward_workspace_bytes(int64_t T_total, int32_t H, int32_t 
  *               input.  Rows behind cu_seqlens[num_seqs] are left as they were.
  *   checkpoints device, gdn_scan_checkpoint_bytes(T_total, C) bytes, written, or
  *               NULL: states along the sequences, for gdn_scan_backward
- *   workspace   gdn_scan_workspace_bytes(T_total, C) bytes, 16-byte aligned
+ *   workspace   gdn_scan_workspace_bytes(T_total, C) bytes, 16-byte aligned.  The
+ *               call's workgroups wait for each other's entries in it, each for about
+ *               0.8 s at most: where something else writes to it before the call has
+ *               ended (a second call, say), the outputs behind a lost entry are NaN,
+ *               and the status is GDN_OK all the same
  *
  * States are fp32; h is rounded once.  e^g is fp32's, and 0 below its normal numbers
  * (g under -87.3).  An infinite state stays infinite however small the product of
  * decays above 0, and a decay of 0 makes it NaN; a finite one it ends, to the last
  * bit.  gdn_scan_backward's l is as the state is.  Alignment: 16 bytes, cu_seqlens 4.  The
- * result does not depend on timing.  Below 2^23 tiles of 64 tokens and 256 channels.
+ * result's bits do not depend on timing (but for a workspace that is written to).
+ * Below 2^23 tiles of 64 tokens and 256 channels.
  * GDN_VALIDATE=1 returns GDN_ERR_DOMAIN for offsets that decrease, do not begin
  * at 0 or end behind T_total, and for g of a sequence above 0 or NaN. */
 int32_t gdn_scan(const void* x, const float* g, const int32_t* cu_seqlens, int32_t num_seqs, int64_t T_total, int32_t C,
@@ -147,7 +152,7 @@ size_t gdn_scan_backward_workspace_bytes(int64_t T_total, int32_t C);
  *   d_initial_state  device fp32 [num_seqs, C], written (the final state's
  *                  gradient for a sequence without a token), or NULL.  It must not
  *                  overlap d_final_state.
- *   workspace      gdn_scan_backward_workspace_bytes(T_total, C) bytes
+ *   workspace      gdn_scan_backward_workspace_bytes(T_total, C) bytes, as gdn_scan's
  *
  * With l_t = d_h_t + e^g_{t+1} l_{t+1} (the last token of a sequence: + its
  * d_final_state): dx = l, with `mix` (1 - e^g) l;  dg = e^g l h_{t-1}, with `mix`
