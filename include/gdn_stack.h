@@ -67,7 +67,8 @@ typedef enum gdn_norm { GDN_NORM_NONE = 0, GDN_NORM_L2 = 1, GDN_NORM_RMS = 2 } g
  * strides a multiple of 16 bytes and at least H * d, positions 4.
  * All arithmetic is fp32, the angles' is 64 bits (a position of a million is
  * turned as exactly as position 1); one rounding to bf16 at the end.  Squares are
- * fp32's: magnitudes above 1e18 normalise to 0, as the formula in fp32 does. */
+ * fp32's: a head whose sum of squares is above fp32's numbers (3.4e38) normalises
+ * to 0, as the formula in fp32 does, and its gradient is 0. */
 int32_t gdn_qk_norm(const void* q, int64_t q_stride, const void* k, int64_t k_stride, int64_t T_total, int32_t H,
                     int32_t H_k, int32_t d, int32_t norm, float eps, const float* q_weight, const float* k_weight,
                     const int32_t* positions, const float* inv_freq, int32_t rotary, int32_t interleaved, float q_scale,

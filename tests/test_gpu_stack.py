@@ -195,6 +195,22 @@ def test_norm_nan_stays_where_it_is(interleaved):
     assert int(torch.isnan(got[2, 1]).sum()) == 2
 
 
+@pytest.mark.parametrize("norm", [gdn.GDN_NORM_L2, gdn.GDN_NORM_RMS])
+def test_norm_large_magnitudes(norm):
+    # a head normalises as long as its sum of squares is a number of fp32, however large a channel is, and to 0 from there on
+    x = torch.zeros((4, 1, 128), device="cuda")
+    x[0, 0, 5] = 1.8e19  # 3.24e38
+    x[1] = 1.6e18        # 128 times 2.56e36: 3.28e38
+    x[2, 0, 5] = 1.9e19  # 3.61e38
+    x[3] = 1.7e18        # 3.70e38
+    y, _ = gdn.gdn_qk_norm(x, norm=norm, eps=1e-6)
+    want, bound = ref.qk_norm(f64(x), norm, 1e-6, None, None, None, False, 1.0)
+    close("y", y[:2], want[:2], bound[:2], F32)
+    assert bool((y[2:] == 0).all())
+    dx, _, _, _ = gdn.gdn_qk_norm_backward(x, None, torch.ones_like(x), None, norm=norm, eps=1e-6)
+    assert bool(torch.isfinite(dx).all()) and bool((dx[2:] == 0).all())
+
+
 # ---------------------------------------------------------------- the recurrence
 
 
