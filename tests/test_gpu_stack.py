@@ -10,7 +10,7 @@ import torch
 import gated_delta_rule_linear_amd as gdn
 import serve_reference as serve
 import stack_reference as ref
-from helpers import log
+from helpers import TOL, log
 
 pytestmark = pytest.mark.gpu
 BF16, F32 = torch.bfloat16, torch.float32
@@ -1040,3 +1040,49 @@ def test_validation_mode(monkeypatch):
         with pytest.raises(gdn.GdnError) as e:
             gdn.gdn_scan_pool(**{**dict(x=y, g=y, states=s, slots=i32([3, 1]), cu_seqlens=good), **kw})
         assert e.value.status == gdn.GDN_ERR_DOMAIN
+
+
+def test_a_training_step_against_64_bits():
+    """The calls of test_a_training_step against float64's automatic differentiation of the definitions, by sequence and
+    head, so that no part of a gradient can be missing: each part is as near as the layer's gradients are held to in full
+    precision, for each of the three calls that it goes through."""
+    gen = torch.Generator().manual_seed(31)
+    T, H, d, lens = 150, 2, 64, [80, 0, 70]
+    r = lambda *s: torch.randn(s, generator=gen)
+    p = dict(q=r(T, H, d), k=r(T, H, d), v=r(T, H, d), g=-torch.rand((T, H, d), generator=gen), beta=torch.sigmoid(r(T, H)),
+             gate=-torch.rand((T, H * d), generator=gen))
+    dy = r(T, H * d)
+    leaves = {n: t.double().requires_grad_() for n, t in p.items()}
+    unit = lambda x: x * (x.square().sum(-1, keepdim=True) + 1e-6).rsqrt()
+    qn, kn = unit(leaves["q"]) * d ** -0.5, unit(leaves["k"])
+    alpha, decay, y, first = leaves["g"].exp(), leaves["gate"].exp(), [], 0
+    for length in lens:
+        S, h = torch.zeros((H, d, d), dtype=torch.float64), torch.zeros(H * d, dtype=torch.float64)
+        for t in range(first, first + length):
+            S = alpha[t][:, :, None] * S
+            gap = leaves["v"][t] - (S * kn[t][:, :, None]).sum(1)
+            S = S + leaves["beta"][t][:, None, None] * kn[t][:, :, None] * gap[:, None, :]
+            o = (S * qn[t][:, :, None]).sum(1).reshape(H * d)
+            h = decay[t] * h + (1 - decay[t]) * o
+            y.append(h)
+        first += length
+    y = torch.stack(y)
+    (y * dy.double()).sum().backward()
+
+    a, cu = {n: t.cuda() for n, t in p.items()}, i32([0, 80, 80, 150])
+    norm = dict(norm=gdn.GDN_NORM_L2, eps=1e-6, q_scale=d ** -0.5)
+    q, k = gdn.gdn_qk_norm(a["q"], a["k"], **norm)
+    o, _ = gdn.gdn_prefill(q, k, a["v"], a["g"], a["beta"], cu)
+    o = o.view(T, H * d)
+    h, _ = gdn.gdn_scan(o, a["gate"], cu, mix=True)
+    dx, dgate, _ = gdn.gdn_scan_backward(o, a["gate"], cu, dy.cuda(), mix=True)
+    dqn, dkn, dv, dg, dbeta, _ = gdn.gdn_prefill_backward(q, k, a["v"], a["g"], a["beta"], cu, dx.view(T, H, d))
+    dq, dk, _, _ = gdn.gdn_qk_norm_backward(a["q"], a["k"], dqn, dkn, **norm)
+    for name, got, want in [("y", h, y)] + [(n, t, leaves[n].grad) for n, t in dict(q=dq, k=dk, v=dv, g=dg, beta=dbeta, gate=dgate).items()]:
+        got, want = f64(got).reshape(T, H, -1), want.detach().reshape(T, H, -1)
+        for lo, hi in ((0, 80), (80, 150)):
+            for head in range(H):
+                x, w = got[lo:hi, head], want[lo:hi, head]
+                off = float((x - w).abs().max() / w.abs().max())
+                log(f"  {name} tokens {lo} to {hi}, head {head}: {off:.2e}")
+                assert off <= 3 * TOL[F32], name
