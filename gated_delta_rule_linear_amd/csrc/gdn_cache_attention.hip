@@ -559,7 +559,7 @@ struct TileShared {
 // Where all tiles of the beginnings are cut, those that have rows are dealt out first, and
 // all their parts: with workgroups that end at once among them, a compute unit here
 // and there received two and others none (64 requests behind 16,384 tokens: 55 us for
-// 51, 256 of them 144 for 127).  Returns the group of tile id % (tiles that have rows) and
+// 51, 256 of them 144 for 131).  Returns the group of tile id % (tiles that have rows) and
 // the group's first, -1 where there is none; `id` becomes the tile, `part` its part.
 __device__ __forceinline__ int32_t group_of(const Attention& a, int br, int32_t& id, int32_t& part, int32_t& first) {
     const int lane = threadIdx.x & 63;
@@ -1107,7 +1107,10 @@ __global__ __launch_bounds__(256) void attention_join_kernel(Attention a, int32_
 // would be 104 MB and the products 17.7 GFLOP, 15 us each.  About 15 us do not
 // depend on the lengths: launches, loads that wait for loads (record, page, codes) and
 // the partial rows.  The two kinds of parts as launches after each other: 71 where one
-// launch took 60.
+// launch took 60.  The one launch's four bodies spill 85 to 106 scalar registers, and three
+// instances use scratch (bf16 of 64 and 128 channels 36 bytes a lane, fp32 of 128 keys'
+// channels 20); in full precision the rows' body, which has two waves to a SIMD by itself,
+// runs at the tile body's one.
 struct Groups {
     const int32_t *offsets, *shared;
     int32_t count;
@@ -1403,8 +1406,11 @@ PrefixPlan plan(const CachePrefixLaunch& c) {
 // gdn_cache_attention's, whose requests read the same pages out of the caches, at
 // some 8 TB/s.  Reading them apart costs 6 us of launches and dependent loads where a group
 // is of few rows and 15 else, and the beginning's products with all rows of the
-// group, at some 0.7 PFLOP/s (0.18 in full precision).  Both sides, in us, shared and
-// not, bf16, 32 heads, 8 for keys, of 128 channels, 64 tokens of their own: 4
+// group, at some 0.7 PFLOP/s (0.18 in full precision).  The partial rows that the join
+// reads are not counted, nor is the type for more than kFewRows rows.  A request's rows are
+// by max_new or by the average, whichever is less: a chunk of 512 among 63 decode requests
+// behind 16,384 shares (244 us, 604 apart).  Both sides, in us, shared and
+// not, bf16, 32 heads, 8 for keys, of 128 channels (others were not timed), 64 tokens of their own: 4
 // requests behind 16,384 tokens 19 and 29, 64 behind them 46 and 217, behind
 // 4,096 29 and 49, behind 1,024 26 and 18; 4 new tokens of 64 behind 16,384 105
 // and 232, of 8 35 and 51, of 16 behind 4,096 28 and 28.  A request of more than
@@ -1412,6 +1418,10 @@ PrefixPlan plan(const CachePrefixLaunch& c) {
 // own, which pays behind long beginnings: 32 new tokens (128 rows) of 64 behind 16,384
 // 574 and 875, of 4 64 and 91, of 8 behind 4,096 44 and 63, but of 64 behind 1,024 102
 // and 87.  With more rows it does not: 256 new tokens of 8 behind 16,384 540 and 528.
+// In full precision: 64 behind 16,384 92 and 242 (1 to 1,024 of their own), 256 of them 279
+// and 817, 4 24 and 30, 64 behind 4,096 39 and 62, behind 1,024 37 and 22; 4 new tokens of
+// 64 behind 16,384 199 and 229, of 8 56 and 54 (both of these are read apart); 32 of 64
+// 1,359 and 2,307, of 8 behind 4,096 79 and 129.
 bool shares(const CachePrefixLaunch& p) {
     const CacheAttentionLaunch& a = p.all;
     if (p.num_groups <= 0 || p.num_groups >= a.num_seqs) return false;  // no request shares with another

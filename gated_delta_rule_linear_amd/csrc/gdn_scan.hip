@@ -27,7 +27,8 @@
 // Measured, bf16 (of what has to be read and written): 65,536 tokens of 4,096
 // channels 372 us, 5.8 TB/s, where a copy reaches 5.1; four sequences of 8,192 191 us
 // forward and 339 backward (5.6 and 5.6), with `mix` 209 (1 - e^g is formed for both
-// passes over the registers) and 347.  A forward pass for the maps, a fold and a
+// passes over the registers) and 347; without the forward call's checkpoints, whose states
+// are another pass, 494 and 505.  A forward pass for the maps, a fold and a
 // pass for the outputs took 1,196 us for the first.  8,300 tokens of 1,028 channels in 8
 // sequences, fp32, 37 us: 650 workgroups for 512 places, and a chain of ticket, inputs,
 // maps and outputs.  What counts: nothing that the rare first and last tokens need may

@@ -204,9 +204,10 @@ int32_t gdn_scan_pool(const void* x, const float* g, float* states, const int32_
  * block table that a group's requests have agree in the blocks of the beginning,
  * and these are read through one of them.  A request that holds fewer than
  * prefix_lens tokens before its new ones (a refused one, say), or whose row is
- * outside the table, takes no part and reads all of its own.  Where the bounds say that reading the beginnings apart
- * would cost more than it saves (short beginnings, few requests, requests of more
- * than 128 rows) the call is gdn_cache_attention itself.  Sums of parts are joined
+ * outside the table, takes no part and reads all of its own.  Where the bounds say
+ * that reading the beginnings apart would cost more than it saves (short beginnings,
+ * few requests, requests of more than 128 rows by max_new and on average) the call is
+ * gdn_cache_attention itself.  Sums of parts are joined
  * in an order that sizes, lengths and groups decide; outputs differ from
  * gdn_cache_attention's by rounding.
  * GDN_VALIDATE=1 returns GDN_ERR_DOMAIN for what gdn_cache_attention does, for
